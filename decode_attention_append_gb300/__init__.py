@@ -18,6 +18,10 @@ Entry points (same names as the C ABI, without the ``daa_`` prefix):
   verification of a tree of draft tokens).
 * ``BatchAttention`` -- plans once from host copies of the page table and owns
   the workspace, for repeated calls over the same batch shape.
+* ``PagePool`` -- the pages of many requests on the device; builds a step's page
+  table there from the requests' lengths, and takes pages back.
+* ``kv_append_q4``, ``kv_dequant_q4``, ``BatchAttentionQ4`` -- append, read-back
+  and attention on a KV cache held in 4 bits (``new_q4_pool``).
 
 Tensors: bf16 ``q [nnz_qo, Hq, d]``, ``k_new/v_new [nnz_new, Hkv, d]``, page
 pool ``kv_pages [num_pages, 2, Hkv, page_size, d]`` (K then V, HND inside a
@@ -25,6 +29,7 @@ page), int32 CSR arrays on the same CUDA device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -42,7 +47,7 @@ DAA_OK = 0
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "page range", -4: "unsupported",
           -5: "CUDA error", -6: "workspace", -7: "alignment"}
 KERNEL_NAMES = {1: "kv_append", 2: "decode_splitkv", 3: "softmax_merge", 4: "prefill_tc", 5: "decode_tc",
-                6: "short_tc"}
+                6: "short_tc", 7: "step_table", 8: "kv_append_q4", 9: "kv_dequant_q4", 10: "attention_q4"}
 
 
 class DaaError(RuntimeError):
@@ -68,6 +73,12 @@ class StepStreams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("upload_stream", "compute_stream", "download_stream",
                                                "uploaded", "computed", "downloaded", "inputs_free",
                                                "out_free")]
+
+
+class _Pool(ctypes.Structure):
+    """daa_page_pool: device arrays of a page pool."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("seq_len", "held", "block_table", "free_pages", "counters")] + \
+               [(n, ctypes.c_int32) for n in ("num_slots", "max_pages", "num_pages", "page_size")]
 
 
 class PlanInfo(ctypes.Structure):
@@ -130,6 +141,21 @@ def load_library():
         lib.daa_append_attention_host.restype = i32
         lib.daa_append_attention_host.argtypes = [vp, vp, ctypes.POINTER(StepLayout), i32, i32, f32, vp, vp,
                                                   vp, vp, sz, _Dims, ctypes.POINTER(StepStreams)]
+        ppool = ctypes.POINTER(_Pool)
+        lib.daa_step_table.restype = i32
+        lib.daa_step_table.argtypes = [ppool, vp, vp, i32, i32, vp, vp, vp, i32, vp, vp, vp, i32, vp]
+        lib.daa_release_pages.restype = i32
+        lib.daa_release_pages.argtypes = [ppool, vp, i32, vp]
+        lib.daa_kv_append_q4.restype = i32
+        lib.daa_kv_append_q4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, _Dims, vp]
+        lib.daa_kv_dequant_q4.restype = i32
+        lib.daa_kv_dequant_q4.argtypes = [vp, vp, vp, i32, vp, _Dims, vp]
+        lib.daa_batch_attention_q4_workspace_size.restype = sz
+        lib.daa_batch_attention_q4_workspace_size.argtypes = [vp, vp, vp, i32, _Dims, ctypes.POINTER(i32)]
+        lib.daa_batch_attention_q4_plan.restype = i32
+        lib.daa_batch_attention_q4_plan.argtypes = [vp, vp, vp, i32, _Dims, vp, sz, pinfo, vp]
+        lib.daa_batch_attention_q4_run.restype = i32
+        lib.daa_batch_attention_q4_run.argtypes = [vp, vp, vp, vp, pinfo, i32, f32, vp, vp, vp, sz, _Dims, vp]
         lib.daa_set_prefill_append_fusion.restype = i32
         lib.daa_set_prefill_append_fusion.argtypes = [i32]
         lib.daa_prefill_append_fusion.restype = i32
@@ -179,6 +205,26 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _on(t: torch.Tensor, name: str, device) -> torch.Tensor:
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t
+
+
+def _device_of(device):
+    """Make a tensor's device current for a call (nothing to do when it is)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _use_stream(stream):
+    """torch's own work of a call on the stream that the call names."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
 def _dims(kv_pages: torch.Tensor, num_qo_heads: int) -> _Dims:
@@ -521,7 +567,9 @@ def append_attention_run(k_new, v_new, q, kv_pages, qo_indptr, kv_indptr, page_i
 
 @dataclass
 class PageTable:
-    """Device int32 CSR page table plus its host mirror (numpy)."""
+    """Device int32 CSR page table plus its host mirror (numpy).  A table built
+    by ``PagePool.step`` also has its new tokens' places in the pool
+    (``slot_map``, int64) and their positions (int32)."""
     qo_indptr: torch.Tensor
     kv_indptr: torch.Tensor
     page_indices: torch.Tensor
@@ -529,6 +577,8 @@ class PageTable:
     h_qo_indptr: np.ndarray
     h_kv_indptr: np.ndarray
     h_last_page_len: np.ndarray
+    slot_map: torch.Tensor | None = None
+    positions: torch.Tensor | None = None
 
     @classmethod
     def from_host(cls, qo_indptr, kv_indptr, page_indices, last_page_len, device="cuda"):
@@ -699,6 +749,309 @@ class HostStep:
 
     def out(self, i):
         return self.h_out[i & 1]
+
+
+class PagePool:
+    """The pages of many requests, on the device: a block-table row of page ids
+    per slot, a stack of free pages, and a kernel that builds a step's page table
+    from lengths (``daa_step_table``).  The host keeps the lengths, never the page
+    ids.
+
+    ``step`` is the call of a serving loop: it checks the lengths on the host,
+    raises before anything is launched when they do not fit, and returns a
+    ``PageTable``.  ``build`` is the kernel alone, on device arrays.  Calls on one
+    pool must be ordered on the GPU (one stream, or events between streams)."""
+
+    PAGE_SIZE = 16
+
+    def __init__(self, num_pages, num_slots, max_pages, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        # the lowest ids come off the stack first
+        free = torch.arange(num_pages - 1, -1, -1, **i32)
+        counters = torch.tensor([num_pages, 0], **i32)
+        self._init(torch.zeros(num_slots, **i32), torch.zeros(num_slots, **i32),
+                   torch.full((num_slots, max_pages), -1, **i32), free, counters)
+        self.h_len, self.h_held, self.h_free = (np.zeros(num_slots, np.int64), np.zeros(num_slots, np.int64),
+                                                int(num_pages))
+
+    @classmethod
+    def from_tensors(cls, seq_len, held, block_table, free_pages, counters):
+        """A pool on the caller's tensors (see ``daa_page_pool``).  Its host
+        copies of the lengths are read from the device by the first ``step``."""
+        self = cls.__new__(cls)
+        self._init(seq_len, held, block_table, free_pages, counters)
+        self.h_len = self.h_held = self.h_free = None
+        return self
+
+    def _init(self, seq_len, held, block_table, free_pages, counters):
+        for n, t in (("seq_len", seq_len), ("held", held), ("block_table", block_table),
+                     ("free_pages", free_pages), ("counters", counters)):
+            _dev_i32(t, n)
+            if t.device != seq_len.device:
+                raise ValueError(f"{n} is on another device than seq_len")
+        if seq_len.dim() != 1 or held.shape != seq_len.shape or block_table.dim() != 2 or \
+                block_table.shape[0] != seq_len.shape[0] or free_pages.dim() != 1 or counters.shape != (2,):
+            raise ValueError("a pool has seq_len [slots], held [slots], block_table [slots, max_pages], "
+                             "free_pages [num_pages] and counters [2]")
+        self.seq_len, self.held, self.block_table = seq_len, held, block_table
+        self.free_pages, self.counters, self.device = free_pages, counters, seq_len.device
+        self._pool = _Pool(_ptr(seq_len), _ptr(held), _ptr(block_table), _ptr(free_pages), _ptr(counters),
+                           seq_len.shape[0], block_table.shape[1], free_pages.shape[0], self.PAGE_SIZE)
+
+    def _mirror(self):
+        if self.h_len is None:
+            self.h_len = self.seq_len.cpu().numpy().astype(np.int64)
+            self.h_held = self.held.cpu().numpy().astype(np.int64)
+            self.h_free = int(self.counters[0])
+
+    def build(self, slots, new_len, qo_indptr, kv_indptr, page_indices, last_page_len, slot_map=None,
+              positions=None, advance=False, stream=None):
+        """``daa_step_table`` on device arrays: fills the given tensors (their
+        sizes are the capacities) and takes the pages the step needs.  What the
+        kernel refuses gives an empty step and sets the device error word.  The
+        host copies of the lengths are not updated: a pool is driven either by
+        ``build`` or by ``step``."""
+        lib = load_library()
+        for n, t in (("slots", slots), ("new_len", new_len), ("qo_indptr", qo_indptr),
+                     ("kv_indptr", kv_indptr), ("page_indices", page_indices),
+                     ("last_page_len", last_page_len)):
+            _on(_dev_i32(t, n), n, self.device)
+        batch = slots.numel()
+        if new_len.numel() != batch or qo_indptr.numel() != batch + 1 or kv_indptr.numel() != batch + 1 \
+                or last_page_len.numel() != batch:
+            raise ValueError("slots, new_len and last_page_len have one entry per request, "
+                             "qo_indptr and kv_indptr one more")
+        rows = None
+        for n, t, dt in (("slot_map", slot_map, torch.int64), ("positions", positions, torch.int32)):
+            if t is not None:
+                if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
+                    raise TypeError(f"{n} must be a contiguous {dt} CUDA tensor")
+                _on(t, n, self.device)
+                rows = t.numel() if rows is None else min(rows, t.numel())
+        if rows is None:
+            rows = 2 ** 31 - 1  # nothing is written per row
+        with _device_of(self.device):
+            _check(lib.daa_step_table(ctypes.byref(self._pool), _ptr(slots), _ptr(new_len), batch,
+                                      int(bool(advance)), _ptr(qo_indptr), _ptr(kv_indptr),
+                                      _ptr(page_indices), page_indices.numel(), _ptr(last_page_len),
+                                      _ptr(slot_map), _ptr(positions), rows, _stream(stream)),
+                   "step_table")
+
+    def step(self, slots, new_lens, advance=True, stream=None) -> PageTable:
+        """The page table of a step that brings ``new_lens[i]`` tokens to slot
+        ``slots[i]`` (host sequences).  With ``advance`` the lengths grow by them;
+        otherwise call ``set_lengths`` once it is known how many were kept."""
+        self._mirror()
+        sl, nl = (np.asarray(x, np.int64).reshape(-1) for x in (slots, new_lens))
+        self._check_slots(sl)
+        if len(nl) != len(sl) or (nl < 0).any():
+            raise ValueError("new_lens must have one entry >= 0 per slot")
+        kv = self.h_len[sl] + nl
+        pages = -(-kv // self.PAGE_SIZE)
+        if len(kv) and pages.max() > self.block_table.shape[1]:
+            raise DaaError(-2, "PagePool.step: a request is longer than its block-table row")
+        take = int(np.maximum(pages - self.h_held[sl], 0).sum())
+        if take > self.h_free:
+            raise DaaError(-3, f"PagePool.step: {take} pages needed, {self.h_free} free")
+        csr = lambda n: np.concatenate([[0], np.cumsum(n)])  # noqa: E731
+        hq, hk = csr(nl), csr(pages)
+        if max(hq[-1], hk[-1]) > 2 ** 31 - 1:
+            raise DaaError(-2, "PagePool.step: the step's rows and pages must fit 32 bits")
+        hl = np.where(pages > 0, kv - (pages - 1) * self.PAGE_SIZE, 0)
+        i32 = dict(dtype=torch.int32, device=self.device)
+        with _device_of(self.device), _use_stream(stream):
+            up = torch.from_numpy(np.stack([sl, nl]).astype(np.int32)).to(self.device)
+            n = len(sl)
+            t = PageTable(torch.empty(n + 1, **i32), torch.empty(n + 1, **i32),
+                          torch.empty(int(hk[-1]), **i32), torch.empty(n, **i32), _host_i32(hq),
+                          _host_i32(hk), _host_i32(hl),
+                          torch.empty(int(hq[-1]), dtype=torch.int64, device=self.device),
+                          torch.empty(int(hq[-1]), **i32))
+            self.build(up[0], up[1], t.qo_indptr, t.kv_indptr, t.page_indices, t.last_page_len,
+                       t.slot_map, t.positions, advance, stream)
+        self.h_held[sl] = np.maximum(self.h_held[sl], pages)
+        self.h_free -= take
+        if advance:
+            self.h_len[sl] = kv
+        return t
+
+    def set_lengths(self, slots, lens, stream=None):
+        """Set the cached lengths of slots (the tokens kept of a step that did
+        not advance, or a request cut back).  Pages stay with their slots."""
+        self._mirror()
+        sl, ln = (np.asarray(x, np.int64).reshape(-1) for x in (slots, lens))
+        self._check_slots(sl)
+        if len(ln) != len(sl) or (ln < 0).any() or (-(-ln // self.PAGE_SIZE) > self.h_held[sl]).any():
+            raise ValueError("lens must have one entry per slot, within the pages the slot holds")
+        with _device_of(self.device), _use_stream(stream):
+            at = torch.from_numpy(sl).to(self.device)
+            self.seq_len.index_copy_(0, at, torch.from_numpy(ln.astype(np.int32)).to(self.device))
+        self.h_len[sl] = ln
+
+    def release(self, slots, stream=None):
+        """Give the pages of slots back (``daa_release_pages``); their lengths become 0."""
+        self._mirror()
+        sl = np.asarray(slots, np.int64).reshape(-1)
+        self._check_slots(sl)
+        lib = load_library()
+        with _device_of(self.device), _use_stream(stream):
+            dev = torch.from_numpy(sl.astype(np.int32)).to(self.device)
+            _check(lib.daa_release_pages(ctypes.byref(self._pool), _ptr(dev), len(sl), _stream(stream)),
+                   "release_pages")
+        self.h_free += int(self.h_held[sl].sum())
+        self.h_len[sl] = self.h_held[sl] = 0
+
+    def _check_slots(self, sl):
+        if len(sl) and (sl.min() < 0 or sl.max() >= len(self.h_len) or len(np.unique(sl)) < len(sl)):
+            raise ValueError("slots must be distinct and within the pool")
+
+
+def new_q4_pool(num_pages, num_kv_heads, head_dim, device="cuda") -> torch.Tensor:
+    """An empty (zero) 4-bit page pool: uint8 [num_pages, Hkv, 2, 9 * head_dim]."""
+    return torch.zeros(num_pages, num_kv_heads, 2, 9 * head_dim, dtype=torch.uint8, device=device)
+
+
+def _q4_dims(kv_pages, num_qo_heads, kv_exp) -> _Dims:
+    if not (isinstance(kv_pages, torch.Tensor) and kv_pages.is_cuda and kv_pages.dtype == torch.uint8
+            and kv_pages.is_contiguous()):
+        raise TypeError("kv_pages must be a contiguous uint8 CUDA tensor")
+    if kv_pages.dim() != 4 or kv_pages.shape[2] != 2 or kv_pages.shape[3] % 9 != 0:
+        raise ValueError("kv_pages must be [num_pages, Hkv, 2, 9 * head_dim]")
+    n, hkv, _, b = kv_pages.shape
+    if kv_exp is not None:
+        _on(_dev_i32(kv_exp, "kv_exp"), "kv_exp", kv_pages.device)
+        if tuple(kv_exp.shape) != (2, hkv):
+            raise ValueError("kv_exp must be [2, Hkv]")
+    return _Dims(hkv if num_qo_heads is None else num_qo_heads, hkv, b // 9, 16, n)
+
+
+def kv_append_q4(k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len,
+                 kv_exp=None, stream=None) -> None:
+    """``kv_append`` into a 4-bit pool: the new tokens' K/V are quantised (e2m1
+    with an e4m3 scale for every 16 dims, and the head's exponent ``kv_exp``
+    [2, Hkv]) and written into their page slots."""
+    lib = load_library()
+    dims = _q4_dims(kv_pages, None, kv_exp)
+    dev = kv_pages.device
+    for n, t in (("k_new", k_new), ("v_new", v_new)):
+        _on(_dev_bf16(t, n), n, dev)
+    for n, t in (("append_indptr", append_indptr), ("page_indices", page_indices),
+                 ("kv_indptr", kv_indptr), ("last_page_len", last_page_len)):
+        _on(_dev_i32(t, n), n, dev)
+    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (dims.num_kv_heads, dims.head_dim) or \
+            v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [nnz_new, Hkv, head_dim]")
+    batch = append_indptr.numel() - 1
+    if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
+        raise ValueError("append_indptr and kv_indptr have batch + 1 entries, last_page_len batch")
+    with _device_of(dev):
+        _check(lib.daa_kv_append_q4(_ptr(k_new), _ptr(v_new), _ptr(kv_pages), _ptr(kv_exp),
+                                    _ptr(append_indptr), _ptr(page_indices), _ptr(kv_indptr),
+                                    _ptr(last_page_len), batch, k_new.shape[0], dims,
+                                    _stream(stream)), "kv_append_q4")
+
+
+def kv_dequant_q4(kv_pages, page_ids, kv_exp=None, out=None, stream=None):
+    """Pages of a 4-bit pool as bf16 pages [n, 2, Hkv, 16, head_dim], exactly."""
+    lib = load_library()
+    dims = _q4_dims(kv_pages, None, kv_exp)
+    dev = kv_pages.device
+    _on(_dev_i32(page_ids, "page_ids"), "page_ids", dev)
+    shape = (page_ids.numel(), 2, dims.num_kv_heads, dims.page_size, dims.head_dim)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _on(_dev_bf16(out, "out"), "out", dev)
+    if tuple(out.shape) != shape:
+        raise ValueError("out must be [n_pages, 2, Hkv, 16, head_dim]")
+    with _device_of(dev):
+        _check(lib.daa_kv_dequant_q4(_ptr(kv_pages), _ptr(kv_exp), _ptr(page_ids), page_ids.numel(),
+                                     _ptr(out), dims, _stream(stream)), "kv_dequant_q4")
+    return out
+
+
+def batch_attention_q4_workspace_size(h_qo_indptr, h_kv_indptr, h_last_page_len, num_qo_heads,
+                                      num_kv_heads, head_dim, page_size, num_pages) -> int:
+    lib = load_library()
+    qo, kv, ll = _host_i32(h_qo_indptr), _host_i32(h_kv_indptr), _host_i32(h_last_page_len)
+    st = ctypes.c_int32(0)
+    n = lib.daa_batch_attention_q4_workspace_size(_ptr(qo), _ptr(kv), _ptr(ll), len(qo) - 1,
+                                                  _Dims(num_qo_heads, num_kv_heads, head_dim,
+                                                        page_size, num_pages), ctypes.byref(st))
+    _check(st.value, "batch_attention_q4_workspace_size")
+    return int(n)
+
+
+class BatchAttentionQ4:
+    """``BatchAttention`` over a 4-bit pool (``new_q4_pool``): plan once from the
+    table's host copies, then append, run or step on it.  ``run`` plans first when
+    ``plan`` has not been called.  Runs of one object share its workspace and must
+    be ordered on the GPU; append and run can be captured into a CUDA graph, plan
+    cannot."""
+
+    def __init__(self, table: PageTable, num_qo_heads: int, kv_pages: torch.Tensor, causal=True,
+                 sm_scale=None, kv_exp=None):
+        self.t = table
+        self.kv_pages, self.kv_exp = kv_pages, kv_exp
+        self.dims = _q4_dims(kv_pages, num_qo_heads, kv_exp)
+        for n in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len"):
+            _on(_dev_i32(getattr(table, n), n), n, kv_pages.device)
+        self.causal = int(bool(causal))
+        self.sm_scale = float(sm_scale if sm_scale is not None else 1.0 / float(self.dims.head_dim) ** 0.5)
+        d = self.dims
+        need = batch_attention_q4_workspace_size(table.h_qo_indptr, table.h_kv_indptr,
+                                                 table.h_last_page_len, d.num_qo_heads, d.num_kv_heads,
+                                                 d.head_dim, d.page_size, d.num_pages)
+        self.rows = int(table.h_qo_indptr[-1])
+        self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=kv_pages.device)
+        self.info = None
+
+    def plan(self, stream=None):
+        """Upload the batch's plan; later runs (one per layer) reuse it."""
+        t, info = self.t, PlanInfo()
+        with _device_of(self.kv_pages.device):
+            _check(load_library().daa_batch_attention_q4_plan(
+                _ptr(t.h_qo_indptr), _ptr(t.h_kv_indptr), _ptr(t.h_last_page_len),
+                len(t.h_qo_indptr) - 1, self.dims, _ptr(self.workspace), self.workspace.numel(),
+                ctypes.byref(info), _stream(stream)), "batch_attention_q4_plan")
+        self.info = info
+        return info
+
+    def append(self, k_new, v_new, stream=None):
+        t = self.t
+        kv_append_q4(k_new, v_new, self.kv_pages, t.qo_indptr, t.page_indices, t.kv_indptr,
+                     t.last_page_len, kv_exp=self.kv_exp, stream=stream)
+
+    def run(self, q, out=None, lse=None, stream=None):
+        """Attention of q [nnz_qo, Hq, head_dim]; returns ``out`` and fills ``lse``."""
+        d, dev = self.dims, self.kv_pages.device
+        _on(_dev_bf16(q, "q"), "q", dev)
+        if tuple(q.shape) != (self.rows, d.num_qo_heads, d.head_dim):
+            raise ValueError("q must be [nnz_qo, Hq, head_dim] of the planned table")
+        if out is None:
+            out = torch.empty_like(q)
+        _on(_dev_bf16(out, "out"), "out", dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
+        if lse is not None:
+            if not (isinstance(lse, torch.Tensor) and lse.is_cuda and lse.dtype == torch.float32
+                    and lse.is_contiguous()):
+                raise TypeError("lse must be a contiguous fp32 CUDA tensor")
+            _on(lse, "lse", dev)
+            if tuple(lse.shape) != (self.rows, d.num_qo_heads):
+                raise ValueError("lse must be [nnz_qo, Hq]")
+        if self.info is None:
+            self.plan(stream)
+        with _device_of(dev):
+            _check(load_library().daa_batch_attention_q4_run(
+                _ptr(q), _ptr(self.kv_pages), _ptr(self.kv_exp), _ptr(self.t.page_indices),
+                ctypes.byref(self.info), self.causal, self.sm_scale, _ptr(out), _ptr(lse),
+                _ptr(self.workspace), self.workspace.numel(), d, _stream(stream)), "batch_attention_q4")
+        return out
+
+    def step(self, k_new, v_new, q, out=None, lse=None, stream=None):
+        """append, then run."""
+        self.append(k_new, v_new, stream)
+        return self.run(q, out=out, lse=lse, stream=stream)
 
 
 def set_prefill_append_fusion(enable: bool) -> None:

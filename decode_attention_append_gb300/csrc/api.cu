@@ -202,6 +202,12 @@ int fuse_min_qo_for(const daa_dims& d) {
 
 }  // namespace
 
+int device_sms() { return num_sms(); }
+
+cudaError_t traced_launch(int32_t kernel_id, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx) {
+  return traced(kernel_id, s, [&] { return launch(ctx); });
+}
+
 daa_status launch_all(const LaunchSet& ls, const PlanLayout& lay, cudaStream_t s, bool trace,
                       bool after_append) {
   const daa_dims& dims = ls.dims;

@@ -159,6 +159,48 @@ struct LaunchSet {
   int fuse_min_qo;
 };
 struct PlanLayout;
+
+// ------------------------------------------------------- step tables, 4-bit cache
+// Step tables from request lengths (step_table.cu); release: only slots, batch
+// and the pool are read.
+struct StepTableArgs {
+  const int32_t* slots;    // [batch]
+  const int32_t* new_len;  // [batch]
+  int batch;
+  int advance;             // 1: seq_len += new_len
+  int32_t* seq_len;        // [num_slots]
+  int32_t* held;           // [num_slots]
+  int32_t* block_table;    // [num_slots][max_pages]
+  int32_t* free_pages;     // [num_pages], a stack
+  int32_t* counters;       // [2]: free pages, CTAs finished (0 between calls)
+  int num_slots, max_pages;
+  int num_pages;
+  int32_t* qo_indptr;      // [batch + 1]
+  int32_t* kv_indptr;      // [batch + 1]
+  int32_t* page_indices;   // [page_capacity]
+  int32_t* last_page_len;  // [batch]
+  int64_t* slot_map;       // [row_capacity] or null
+  int32_t* positions;      // [row_capacity] or null
+  int page_capacity, row_capacity;
+  int* err;
+};
+size_t step_table_smem(int batch, int num_slots);
+cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, cudaStream_t stream);
+
+// 4-bit cache (append_q4.cu): the quantising append, and pages as bf16.
+// kv_exp: [2][Hkv] or null.  dequant: out page i is pool page ids[src ? src[i] : i].
+cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool,
+                                const int32_t* kv_exp, const int32_t* append_indptr,
+                                const int32_t* page_indices, const int32_t* kv_indptr,
+                                const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
+                                int head_dim, int64_t num_pages, int* err, cudaStream_t stream);
+cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
+                                 const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
+                                 int64_t num_pages, void* out, int* err, cudaStream_t stream);
+
+// SMs of the current device, and a launch between the tracer's events (api.cu).
+int device_sms();
+cudaError_t traced_launch(int32_t kernel_id, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx);
 // The kernels run in the order prefill, decode, softmax_merge; each after the
 // first is a programmatic dependent launch, and so is the first when
 // `after_append` (this call's own kv_append kernel precedes it on the stream).

@@ -18,6 +18,20 @@ struct DecodeUnit {
   int32_t pad0, pad1;
 };
 
+// One key split of a request read from the 4-bit cache: its n_tok new tokens
+// (all query heads of a kv head each) over keys [tok_begin, tok_end).  One CTA
+// per (unit, kv head).  Splits are page aligned.
+struct Q4Unit {
+  int32_t q_row;        // row of the request's first new token
+  int32_t n_tok;        // its new tokens
+  int32_t kv_len;
+  int32_t page_base;    // index into page_indices of the request's first page
+  int32_t tok_begin;    // first key (multiple of page_size)
+  int32_t tok_end;      // one past the last key
+  int32_t part;         // partial slot of token 0, or -1: write out / lse_out
+  int32_t part_stride;  // token t writes slot part + t * part_stride
+};
+
 // softmax_merge of the partials of one query row: n_parts consecutive slots
 // from part_begin (the key splits of its request), plus slot `extra` when the
 // row's shared prefix was attended by a prefix-group item (else -1).
@@ -64,6 +78,7 @@ struct PrefillTile {
 // plan under 64 KB is copied inline with the launches.
 
 static_assert(sizeof(DecodeUnit) == 32, "DecodeUnit layout");
+static_assert(sizeof(Q4Unit) == 32, "Q4Unit layout");
 static_assert(sizeof(MergeItem) == 16, "MergeItem layout");
 constexpr int32_t kTileRequest = 0;
 constexpr int32_t kTilePrefixGroup = 1;
@@ -78,6 +93,10 @@ enum KernelId : int32_t {
   kKernelPrefill = 4,
   kKernelTcDecode = 5,
   kKernelShort = 6,   // short multi-token items on the single-CTA kernel (head_dim 128)
+  kKernelStepTable = 7,   // step tables and released pages
+  kKernelAppendQ4 = 8,
+  kKernelDequantQ4 = 9,
+  kKernelAttentionQ4 = 10,
 };
 
 }  // namespace daa

@@ -508,9 +508,153 @@ daa_status daa_batch_attention_noalloc(const void* q, const void* kv_pages,
                                        daa_dims dims, void* stream);
 
 /*
+ * Step tables built on the GPU ("Accelerating Sonar through speculation", section
+ * "Inference with speculative decoding": the KV page information of a step is
+ * metadata that the attention kernel is configured with; "Disaggregated prefill
+ * and decode", section "KV Messenger": pages are allocated per request).
+ *
+ * daa_page_pool holds the pages of many requests on the device, one slot each.
+ * All arrays belong to the caller:
+ *   seq_len      int32 [num_slots]             cached tokens of the slot
+ *   held         int32 [num_slots]             pages in the slot's row
+ *   block_table  int32 [num_slots][max_pages]  their ids, in token order
+ *   free_pages   int32 [num_pages]             a stack; entries [0, counters[0])
+ *   counters     int32 [2]                     free pages; scratch (0 before the
+ *                                              first call, and 0 after each)
+ * held may be more than seq_len needs (a request cut back after rejected draft
+ * tokens keeps its pages and uses them again).
+ *
+ * daa_step_table: for a step that brings new_len[i] >= 0 tokens to slot slots[i],
+ * with kv_i = seq_len + new_len[i] and n_i = ceil(kv_i / page_size),
+ *   qo_indptr, kv_indptr   int32 [batch + 1]: exclusive sums of new_len and n_i
+ *   page_indices           int32 [page_capacity]: the n_i pages of each request;
+ *                          entries past kv_indptr[batch] are left as they were
+ *   last_page_len          int32 [batch]: kv_i - (n_i - 1) * page_size (0 if n_i = 0)
+ *   slot_map               int64 [row_capacity] or NULL: page * page_size + slot of
+ *                          every new token (its place in the pool), in row order
+ *   positions              int32 [row_capacity] or NULL: seq_len + j of new token j
+ * -- the page table of this header's other calls.  Pages a request lacks come
+ * from the top of the free stack, in request order, and are added to its row;
+ * held and the free count follow.  seq_len is advanced by new_len when `advance`
+ * is 1; with 0 it stays, and the same call can be made again (it then takes no
+ * pages), for callers that learn how many tokens were accepted afterwards.
+ *
+ * All or nothing: if a slot is out of range or named twice, new_len < 0, kv_i >
+ * max_pages * page_size, the capacities are too small, or the stack holds too
+ * few pages, the pool is not changed, both indptr arrays and last_page_len are
+ * zero (an empty step), and the device error word is set (3, or 4 for too few
+ * free pages).
+ *
+ * daa_release_pages: the pages of `batch` slots go back on the stack; their
+ * seq_len and held become 0.  Nothing is changed if a slot is out of range or
+ * named twice, or the stack has no room (error word 3).
+ *
+ * Calls on one pool must not overlap on the GPU (they share its counters).  One
+ * kernel launch each, no host copies: both can be captured into a CUDA graph.
+ * Errors (host): DAA_ERR_INVALID_ARG for NULL arrays, negative counts or advance
+ * not 0 or 1; DAA_ERR_UNSUPPORTED for page_size != 16, batch >
+ * DAA_STEP_MAX_BATCH, num_slots > DAA_STEP_MAX_SLOTS; DAA_ERR_ALIGNMENT for a
+ * slot_map that is not 8-byte aligned; DAA_ERR_CUDA for a failed launch.
+ */
+#define DAA_STEP_MAX_BATCH 8192
+#define DAA_STEP_MAX_SLOTS 65536
+
+typedef struct {
+  int32_t* seq_len;
+  int32_t* held;
+  int32_t* block_table;
+  int32_t* free_pages;
+  int32_t* counters;
+  int32_t num_slots;
+  int32_t max_pages; /* pages of a row */
+  int32_t num_pages; /* entries of the stack */
+  int32_t page_size; /* 16 */
+} daa_page_pool;
+
+daa_status daa_step_table(const daa_page_pool* pool, const int32_t* slots, const int32_t* new_len,
+                          int32_t batch, int32_t advance, int32_t* qo_indptr, int32_t* kv_indptr,
+                          int32_t* page_indices, int32_t page_capacity, int32_t* last_page_len,
+                          int64_t* slot_map, int32_t* positions, int32_t row_capacity,
+                          void* stream);
+
+daa_status daa_release_pages(const daa_page_pool* pool, const int32_t* slots, int32_t batch,
+                             void* stream);
+
+/*
+ * The 4-bit KV cache.  Decode attention is bound by the K/V bytes it reads
+ * ("Disaggregated prefill and decode", "Prefill vs decode performance"); this
+ * cache holds 4.5 bits a value instead of 16.
+ *
+ * Format.  A value is e2m1 * e4m3 * 2^e: a 4-bit float (values 0, .5, 1, 1.5, 2,
+ * 3, 4, 6 and their negatives, codes 0..7 and 8..15), the e4m3 scale of its
+ * block of 16 dims of one token and kv head, and the exponent of its kv head.
+ * Pool: uint8 [num_pages][Hkv][2 (K, V)][9 * head_dim] -- heads before tokens, as
+ * the bf16 pool, with a head's K and V of a page side by side.  A slice holds
+ *   16 token rows of head_dim / 2 bytes: dim 2i in the low four bits of byte i,
+ *   dim 2i + 1 in the high four; then head_dim scale bytes:
+ *   K: [16 tokens][head_dim / 16 blocks],  V: [head_dim / 16 blocks][16 tokens].
+ * kv_exp: int32 [2 (K, V)][Hkv] on the device, or NULL for zeros; read as at
+ * least -32 and at most 32.  The same exponents go to every call on a pool.
+ * They centre a head's values in the range of its scales (2^-9 .. 448).
+ *
+ * daa_kv_append_q4: daa_kv_append into a 4-bit pool (same arguments, checks and
+ * errors).  For a block x of 16 bf16 values, y = x * 2^-e:
+ *   scale = e4m3(clamp(max|y| / 6, 2^-9, 448)), code = e2m1(y / scale),
+ * each rounded to the nearest value, ties to the even code, cut at 6; a zero
+ * keeps its sign bit.  NaN is stored as zero and an infinity as +-6 * 448 * 2^e,
+ * so the cache holds finite values only.  Only the new tokens' bytes are written.
+ *
+ * daa_kv_dequant_q4: pages page_ids[0 .. n_pages) (device int32) as bf16 pages
+ * out[i][2][Hkv][16][head_dim], exactly (a value has at most 6 significant bits).
+ * A page id outside [0, num_pages) gives a page of zeros and sets the device
+ * error word (1).  Errors as daa_kv_append.
+ *
+ * daa_batch_attention_q4_*: daa_batch_attention over a 4-bit pool, planned once
+ * and run many times (see daa_batch_attention_plan and _run: same plan rules,
+ * workspace, masks, outputs and errors).  The result is that of
+ * daa_batch_attention on the pool's values in bf16, up to fp32 rounding order
+ * and the rounding of the softmax weights.  Slots past a request's last token
+ * may hold anything.  Requests of up to a few packed (token, query head) rows are
+ * read from the 4-bit pages; the pages of longer chunks are written to the
+ * workspace in bf16 first (2 * Hkv * head_dim * 32 bytes a page), each once.
+ *  plan: host arrays of daa_batch_attention; the workspace (at least
+ *        daa_batch_attention_q4_workspace_size bytes, 256-byte aligned); `info`.
+ *        It copies from host memory, so it cannot be captured into a CUDA graph
+ *        (DAA_ERR_UNSUPPORTED on a capturing stream); run can.
+ *  run:  q, out [nnz_qo][Hq][head_dim] bf16, lse_out fp32 [nnz_qo][Hq] or NULL,
+ *        page_indices (device) of the planned table.
+ * Runs that share a workspace must not overlap on the GPU, whatever stream or
+ * graph they are launched from.
+ */
+daa_status daa_kv_append_q4(const void* k_new, const void* v_new, void* kv_pages,
+                            const int32_t* kv_exp, const int32_t* append_indptr,
+                            const int32_t* page_indices, const int32_t* kv_indptr,
+                            const int32_t* last_page_len, int32_t batch, int32_t nnz_new,
+                            daa_dims dims, void* stream);
+
+daa_status daa_kv_dequant_q4(const void* kv_pages, const int32_t* kv_exp, const int32_t* page_ids,
+                             int32_t n_pages, void* out, daa_dims dims, void* stream);
+
+size_t daa_batch_attention_q4_workspace_size(const int32_t* h_qo_indptr, const int32_t* h_kv_indptr,
+                                             const int32_t* h_last_page_len, int32_t batch,
+                                             daa_dims dims, daa_status* status);
+
+daa_status daa_batch_attention_q4_plan(const int32_t* h_qo_indptr, const int32_t* h_kv_indptr,
+                                       const int32_t* h_last_page_len, int32_t batch, daa_dims dims,
+                                       void* workspace, size_t workspace_bytes, daa_plan_info* info,
+                                       void* stream);
+
+daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const int32_t* kv_exp,
+                                      const int32_t* page_indices, const daa_plan_info* info,
+                                      int32_t causal, float sm_scale, void* out, float* lse_out,
+                                      void* workspace, size_t workspace_bytes, daa_dims dims,
+                                      void* stream);
+
+/*
  * Reads the device error word of the current device into *code (0 = none, 1 =
  * page id out of range, 2 = a bounded wait timed out, 3 = inconsistent request
- * lengths) and clears it when `reset` is non-zero.  Synchronises the device.
+ * lengths, 4 = a step table that needs more pages than are free) and clears it
+ * when `reset` is non-zero.  Synchronises the device.
  * Kernels never trap on these: a page id outside the pool is replaced by page
  * 0 (or, in the append, the row is skipped), so the outputs of that call are
  * undefined but the context stays usable.  Every wait inside a kernel is
@@ -539,7 +683,8 @@ daa_status daa_selftest_bounded_wait(int32_t* gave_up);
  * Kernel ids: 1 kv_append, 2 decode split-KV (CUDA cores), 3 softmax_merge,
  * 4 tensor-core prefill, 5 tensor-core decode split-KV (decode and verify
  * items), 6 tensor-core short multi-token items (head_dim 128: requests whose
- * rows fit two 128-row Q tiles).
+ * rows fit two 128-row Q tiles), 7 step tables and released pages, 8 4-bit
+ * append, 9 4-bit pages to bf16, 10 attention over 4-bit pages.
  */
 daa_status daa_trace_enable(int32_t capacity);
 daa_status daa_trace_disable(void);

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdaa.so")
 SOURCES = ["api.cu", "append.cu", "decode.cu", "merge.cu", "prefill.cu", "prefill_pair.cu", "noalloc.cu",
-           "api_q4.cu", "append_q4.cu", "step_table.cu"]
+           "api_q4.cu", "append_q4.cu", "decode_q4.cu", "step_table.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

@@ -55,7 +55,7 @@ struct PlanRecordQ4 {
   int32_t num_qo_heads, num_kv_heads, head_dim, page_size;
   int64_t num_pages;
   int32_t batch, nnz_qo;
-  int32_t n_units, n_merges, n_parts, n_scratch;
+  int32_t n_units[kQ4Classes], n_merges, n_parts, n_scratch;
   PlanLayout sub;
 };
 constexpr int64_t kPlanMagicQ4 = 0x4441415f51345f50LL;
@@ -232,7 +232,7 @@ daa_status daa_batch_attention_q4_plan(const int32_t* h_qo_indptr, const int32_t
   rec.num_pages = dims.num_pages;
   rec.batch = batch;
   rec.nnz_qo = batch > 0 ? h_qo_indptr[batch] : 0;
-  rec.n_units = lay.n_units;
+  for (int i = 0; i < kQ4Classes; ++i) rec.n_units[i] = lay.n_units[i];
   rec.n_merges = lay.n_merges;
   rec.n_parts = lay.n_parts;
   rec.n_scratch = lay.n_scratch;
@@ -255,7 +255,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     return DAA_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return DAA_ERR_INVALID_ARG;
   Q4Layout lay;
-  lay.n_units = rec.n_units;
+  for (int i = 0; i < kQ4Classes; ++i) lay.n_units[i] = rec.n_units[i];
   lay.n_merges = rec.n_merges;
   lay.n_parts = rec.n_parts;
   lay.n_scratch = rec.n_scratch;
@@ -293,6 +293,41 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     ls.sms = device_sms();
     const daa_status st = launch_all(ls, lay.sub, s, /*trace=*/true, /*after_append=*/false);
     if (st != DAA_OK) return st;
+  }
+  if (lay.units() > 0) {
+    AttentionQ4Args a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.pool = static_cast<const uint8_t*>(kv_pages);
+    a.kv_exp = kv_exp;
+    a.page_indices = page_indices;
+    a.units = reinterpret_cast<const Q4Unit*>(ws + lay.off_units);
+    a.Hq = dims.num_qo_heads;
+    a.Hkv = dims.num_kv_heads;
+    a.group = dims.num_qo_heads / dims.num_kv_heads;
+    a.head_dim = dims.head_dim;
+    a.num_pages = dims.num_pages;
+    a.causal = causal ? 1 : 0;
+    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse_out = lse_out;
+    a.part_o = reinterpret_cast<float*>(ws + lay.off_part_o);
+    a.part_lse = reinterpret_cast<float*>(ws + lay.off_part_lse);
+    a.err = device_error_word();
+    if (traced(kKernelAttentionQ4, s, [&] { return launch_attention_q4(a, lay.n_units, s); }) != cudaSuccess)
+      return DAA_ERR_CUDA;
+    if (lay.n_merges > 0) {
+      MergeArgs m{};
+      m.items = reinterpret_cast<const MergeItem*>(ws + lay.off_merges);
+      m.n_items = lay.n_merges;
+      m.Hq = dims.num_qo_heads;
+      m.head_dim = dims.head_dim;
+      m.part_o = a.part_o;
+      m.part_lse = a.part_lse;
+      m.out = a.out;
+      m.lse_out = lse_out;
+      if (traced(kKernelMerge, s, [&] { return launch_merge(m, s, /*programmatic=*/false); }) != cudaSuccess)
+        return DAA_ERR_CUDA;
+    }
   }
   return DAA_OK;
 }

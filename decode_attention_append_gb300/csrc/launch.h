@@ -198,6 +198,26 @@ cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const 
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
                                  int64_t num_pages, void* out, int* err, cudaStream_t stream);
 
+// Attention over the 4-bit pages (decode_q4.cu); n_units per class, in order.
+struct AttentionQ4Args {
+  const uint16_t* q;       // [nnz_qo][Hq][d]
+  const uint8_t* pool;     // [num_pages][Hkv][2][9 d]
+  const int32_t* kv_exp;   // [2][Hkv] or null
+  const int32_t* page_indices;
+  const Q4Unit* units;
+  int Hq, Hkv, group, head_dim;
+  int64_t num_pages;
+  int causal;
+  float sm_scale_log2;     // sm_scale * log2(e)
+  uint16_t* out;
+  float* lse_out;          // or null
+  float* part_o;           // [n_parts][Hq][d]
+  float* part_lse;         // [n_parts][Hq] (log2 domain)
+  int* err;
+};
+cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_units)[kQ4Classes],
+                                cudaStream_t stream);
+
 // SMs of the current device, and a launch between the tracer's events (api.cu).
 int device_sms();
 cudaError_t traced_launch(int32_t kernel_id, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx);

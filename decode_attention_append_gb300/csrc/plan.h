@@ -18,19 +18,24 @@ struct DecodeUnit {
   int32_t pad0, pad1;
 };
 
-// One key split of a request read from the 4-bit cache: its n_tok new tokens
-// (all query heads of a kv head each) over keys [tok_begin, tok_end).  One CTA
-// per (unit, kv head).  Splits are page aligned.
+// One key split of (some new tokens of) a request read from the 4-bit cache: all
+// query heads of a kv head of its n_tok tokens over keys [tok_begin, tok_end).
+// One CTA per (unit, kv head).  Splits are page aligned.
 struct Q4Unit {
-  int32_t q_row;        // row of the request's first new token
-  int32_t n_tok;        // its new tokens
-  int32_t kv_len;
+  int32_t q_row;        // row of the first of the tokens
+  int32_t n_tok;
+  int32_t pos0;         // its position
+  int32_t kv_len;       // keys of the request
   int32_t page_base;    // index into page_indices of the request's first page
   int32_t tok_begin;    // first key (multiple of page_size)
   int32_t tok_end;      // one past the last key
-  int32_t part;         // partial slot of token 0, or -1: write out / lse_out
+  int32_t part;         // partial slot of the first token, or -1: write out / lse_out
   int32_t part_stride;  // token t writes slot part + t * part_stride
+  int32_t pad0, pad1, pad2;
 };
+// Units come in classes by the query rows (tokens x heads) they hold, each its
+// own launch: up to 8, 16, 32.
+constexpr int kQ4Classes = 3;
 
 // softmax_merge of the partials of one query row: n_parts consecutive slots
 // from part_begin (the key splits of its request), plus slot `extra` when the
@@ -78,7 +83,7 @@ struct PrefillTile {
 // plan under 64 KB is copied inline with the launches.
 
 static_assert(sizeof(DecodeUnit) == 32, "DecodeUnit layout");
-static_assert(sizeof(Q4Unit) == 32, "Q4Unit layout");
+static_assert(sizeof(Q4Unit) == 48, "Q4Unit layout");
 static_assert(sizeof(MergeItem) == 16, "MergeItem layout");
 constexpr int32_t kTileRequest = 0;
 constexpr int32_t kTilePrefixGroup = 1;

@@ -19,19 +19,24 @@
 
 namespace daa {
 
-constexpr int kQ4NativeRows = 0;
+constexpr int kQ4NativeRows = 64;
+constexpr int kQ4UnitsPerSm = 16;
+constexpr int kQ4MinPages = 16;
+constexpr int kQ4UnitRows = 32;  // rows a unit holds at most
 
 // Sections of the workspace, all worked out from the counts and the layout of
 // the bf16 requests' plan.  The first plan_bytes are copied from the host.
 struct Q4Layout {
-  int n_units = 0, n_merges = 0, n_parts = 0, n_scratch = 0;
+  int n_units[kQ4Classes] = {0, 0, 0};
+  int n_merges = 0, n_parts = 0, n_scratch = 0;
   PlanLayout sub;
   size_t off_units, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
       off_pool, total;
+  int units() const { return n_units[0] + n_units[1] + n_units[2]; }
   void finish(const daa_dims& d) {
     size_t off = 0;
     off_units = off;
-    off = plan_align_up(off + (size_t)n_units * sizeof(Q4Unit));
+    off = plan_align_up(off + (size_t)units() * sizeof(Q4Unit));
     off_merges = off;
     off = plan_align_up(off + (size_t)n_merges * sizeof(MergeItem));
     off_src = off;
@@ -47,7 +52,7 @@ struct Q4Layout {
     off = plan_align_up(off + (size_t)n_parts * d.num_qo_heads * sizeof(float));
     off_pool = off;
     off = plan_align_up(off + (size_t)n_scratch * 2 * d.num_kv_heads * d.page_size * d.head_dim * 2);
-    total = n_units == 0 && sub.total == 0 ? 0 : off;
+    total = units() == 0 && sub.total == 0 ? 0 : off;
   }
 };
 
@@ -84,6 +89,8 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
   }
   const int P = d.page_size;
   const int g = d.num_qo_heads / d.num_kv_heads;
+  const int tpu = kQ4UnitRows / g;  // tokens of a unit
+  int64_t native_pages = 0;         // pages that units read, once per unit of a request's tokens
   for (int r = 0; r < batch; ++r) {
     const int64_t nq = (int64_t)qo[r + 1] - qo[r];
     const int64_t np = (int64_t)kv[r + 1] - kv[r];
@@ -98,8 +105,57 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
       pl.sub_kv.push_back(pl.sub_kv.back() + (int32_t)np);
       pl.sub_last.push_back(last[r]);
       for (int64_t p = 0; p < np; ++p) pl.src.push_back((int32_t)(kv[r] + p));
+    } else if (nq > 0) {
+      native_pages += np * ((nq + tpu - 1) / tpu);
     }
   }
+  // Key splits: about kQ4UnitsPerSm units (times kv heads) an SM, so that the
+  // longest is a small part of the pass and the parts to join stay few; at least
+  // kQ4MinPages pages, a few for each of a CTA's warps.
+  int64_t split = (native_pages * d.num_kv_heads + (int64_t)sms * kQ4UnitsPerSm - 1) /
+                  ((int64_t)sms * kQ4UnitsPerSm);
+  split = std::max<int64_t>(kQ4MinPages, (split + 3) / 4 * 4);
+  int n_parts = 0;
+  for (int r = 0; r < batch; ++r) {
+    const int nq = qo[r + 1] - qo[r];
+    if (nq == 0 || nq * g > kQ4NativeRows) continue;
+    const int np = kv[r + 1] - kv[r];
+    const int kv_len = (np - 1) * P + last[r];
+    // splits cut the keys that token 0 sees, so every split starts at a key that
+    // each token sees; the last one also takes the tail
+    const int64_t vis = (int64_t)kv_len - nq + 1;
+    const int nsplit = (int)((vis + split * P - 1) / (split * P));
+    int part0 = -1;
+    if (nsplit > 1) {
+      part0 = n_parts;
+      for (int t = 0; t < nq; ++t)
+        if (!pl.merges.push_back(MergeItem{qo[r] + t, part0 + t * nsplit, nsplit, -1}))
+          return DAA_ERR_WORKSPACE;
+      n_parts += nsplit * nq;
+    }
+    for (int t0 = 0; t0 < nq; t0 += tpu)
+      for (int s = 0; s < nsplit; ++s) {
+        Q4Unit u{};
+        u.q_row = qo[r] + t0;
+        u.n_tok = std::min(tpu, nq - t0);
+        u.pos0 = kv_len - nq + t0;
+        u.kv_len = kv_len;
+        u.page_base = kv[r];
+        u.tok_begin = (int)(s * split * P);
+        u.tok_end = s == nsplit - 1 ? kv_len : (int)((s + 1) * split * P);
+        u.part = part0 >= 0 ? part0 + t0 * nsplit + s : -1;
+        u.part_stride = nsplit;
+        if (!pl.units.push_back(u)) return DAA_ERR_WORKSPACE;
+      }
+  }
+  // by class, then longest first
+  auto cls = [g](const Q4Unit& u) { return u.n_tok * g <= 8 ? 0 : (u.n_tok * g <= 16 ? 1 : 2); };
+  std::sort(pl.units.data(), pl.units.data() + pl.units.size(), [&](const Q4Unit& x, const Q4Unit& y) {
+    if (cls(x) != cls(y)) return cls(x) < cls(y);
+    const int a = x.tok_end - x.tok_begin, b = y.tok_end - y.tok_begin;
+    return a != b ? a > b : (x.q_row != y.q_row ? x.q_row < y.q_row : x.tok_begin < y.tok_begin);
+  });
+  for (size_t i = 0; i < pl.units.size(); ++i) ++pl.lay.n_units[cls(pl.units.data()[i])];
   // the bf16 requests: their own plan, then its query rows moved to their place in the batch
   daa_dims sd = d;
   sd.num_pages = std::max<int64_t>(1, (int64_t)pl.src.size());
@@ -122,7 +178,7 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     PrefillTile& t = pl.sub_tiles.data()[i];
     t.q_row0 = moved(t.q_row0);
   }
-  pl.lay.n_units = (int)pl.units.size();
+  pl.lay.n_parts = n_parts;
   pl.lay.n_merges = (int)pl.merges.size();
   pl.lay.n_scratch = (int)pl.src.size();
   pl.lay.finish(d);
@@ -134,7 +190,7 @@ template <template <class> class Vec>
 void plan_stage_q4(const Q4Plan<Vec>& pl, uint8_t* host) {
   const Q4Layout& lay = pl.lay;
   std::memset(host, 0, lay.plan_bytes);
-  if (lay.n_units) std::memcpy(host + lay.off_units, pl.units.data(), lay.n_units * sizeof(Q4Unit));
+  if (lay.units()) std::memcpy(host + lay.off_units, pl.units.data(), lay.units() * sizeof(Q4Unit));
   if (lay.n_merges) std::memcpy(host + lay.off_merges, pl.merges.data(), lay.n_merges * sizeof(MergeItem));
   if (lay.n_scratch) {
     std::memcpy(host + lay.off_src, pl.src.data(), lay.n_scratch * sizeof(int32_t));

@@ -87,11 +87,11 @@ def make_table(rng, cached, new, spare=5):
 
 
 def attention(q, pool, t, exps, d, scale, causal=True):
-    """float64 (out, lse, A, B): A = sum of weights times |v|, B = the largest scale * sum |q k| of a row's keys --
-    the sizes that the error bounds of the tests are relative to.  q float64 [rows, Hq, d]."""
+    """float64 (out, lse, A, B, C): A = sum of weights times |v|, B = the largest scale * sum |q k| of a row's keys,
+    C = sum of |v| over them -- the sizes that the error bounds of the tests are relative to.  q float64 [rows, Hq, d]."""
     hq, hkv = q.shape[1], pool.shape[1]
     g = hq // hkv
-    out, A = np.zeros(q.shape), np.zeros(q.shape)
+    out, A, C = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     lse, B = np.zeros(q.shape[:2]), np.zeros(q.shape[:2])
     for r in range(len(t["last_page_len"])):
         a0, a1 = t["qo_indptr"][r], t["qo_indptr"][r + 1]
@@ -113,9 +113,10 @@ def attention(q, pool, t, exps, d, scale, causal=True):
         w = (s - z[..., None]).exp()
         out[a0:a1] = torch.einsum("thgk,hkd->thgd", w, vv).reshape(a1 - a0, hq, d).numpy()
         A[a0:a1] = torch.einsum("thgk,hkd->thgd", w, vv.abs()).reshape(a1 - a0, hq, d).numpy()
+        C[a0:a1] = torch.einsum("thgk,hkd->thgd", (s > -torch.inf).double(), vv.abs()).reshape(a1 - a0, hq, d).numpy()
         lse[a0:a1] = z.reshape(a1 - a0, hq).numpy()
         B[a0:a1] = big.amax(-1).reshape(a1 - a0, hq).numpy()
-    return out, lse, A, B
+    return out, lse, A, B, C
 
 
 def check_attention(out, lse, ref, d):
@@ -123,12 +124,14 @@ def check_attention(out, lse, ref, d):
     scores   fp32 sums of d products and a scaling: off by at most ds = (d + 8) 2^-24 B
     weights  bf16 (2^-8) at the coarsest, from scores and a maximum that are off by ds each, and an exponential good to
              2^-22: relative error dw = 2^-8 + 2 ds + 2^-22, on both sides of the quotient but the rounding
+             fp16 weights end at a step of 2^-24; they are held times 2^7 over a maximum that is at most the row's, so
+             half a step is 2^-32 of the largest weight, and the sum of weights is at least the largest: 2^-32 C
     sums     fp32 over the keys, split and joined: 2^-16 covers 2^8 additions in a row at 2^-24 each
     out      one rounding to bf16 (2^-8), and 2^-24 for values near zero next to A"""
-    r_out, r_lse, A, B = ref
+    r_out, r_lse, A, B, C = ref
     ds = (d + 8) * 2.0 ** -24 * B
     dw = (2.0 ** -8 + 4 * ds + 2.0 ** -21 + 2.0 ** -16)[..., None]
-    tol = 2.0 ** -8 * (np.abs(r_out) + dw * A) + dw * A + 1e-30
+    tol = 2.0 ** -8 * (np.abs(r_out) + dw * A) + dw * A + 2.0 ** -32 * C + 1e-30
     err = np.abs(out - r_out)
     assert np.isfinite(out).all()
     assert (err <= tol).all(), (float((err / tol).max()), np.unravel_index((err / tol).argmax(), err.shape))

@@ -55,7 +55,7 @@ struct PlanRecordQ4 {
   int32_t num_qo_heads, num_kv_heads, head_dim, page_size;
   int64_t num_pages;
   int32_t batch, nnz_qo;
-  int32_t n_units[kQ4Classes], n_merges, n_parts, n_scratch;
+  int32_t n_ranges[kQ4Classes], n_units, n_merges, n_parts, n_scratch;
   PlanLayout sub;
 };
 constexpr int64_t kPlanMagicQ4 = 0x4441415f51345f50LL;
@@ -232,7 +232,8 @@ daa_status daa_batch_attention_q4_plan(const int32_t* h_qo_indptr, const int32_t
   rec.num_pages = dims.num_pages;
   rec.batch = batch;
   rec.nnz_qo = batch > 0 ? h_qo_indptr[batch] : 0;
-  for (int i = 0; i < kQ4Classes; ++i) rec.n_units[i] = lay.n_units[i];
+  for (int i = 0; i < kQ4Classes; ++i) rec.n_ranges[i] = lay.n_ranges[i];
+  rec.n_units = lay.n_units;
   rec.n_merges = lay.n_merges;
   rec.n_parts = lay.n_parts;
   rec.n_scratch = lay.n_scratch;
@@ -255,7 +256,8 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     return DAA_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale) || !(sm_scale > 0.f)) return DAA_ERR_INVALID_ARG;
   Q4Layout lay;
-  for (int i = 0; i < kQ4Classes; ++i) lay.n_units[i] = rec.n_units[i];
+  for (int i = 0; i < kQ4Classes; ++i) lay.n_ranges[i] = rec.n_ranges[i];
+  lay.n_units = rec.n_units;
   lay.n_merges = rec.n_merges;
   lay.n_parts = rec.n_parts;
   lay.n_scratch = rec.n_scratch;
@@ -294,13 +296,14 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     const daa_status st = launch_all(ls, lay.sub, s, /*trace=*/true, /*after_append=*/false);
     if (st != DAA_OK) return st;
   }
-  if (lay.units() > 0) {
+  if (lay.n_units > 0) {
     AttentionQ4Args a{};
     a.q = static_cast<const uint16_t*>(q);
     a.pool = static_cast<const uint8_t*>(kv_pages);
     a.kv_exp = kv_exp;
     a.page_indices = page_indices;
     a.units = reinterpret_cast<const Q4Unit*>(ws + lay.off_units);
+    a.seg_begin = reinterpret_cast<const int32_t*>(ws + lay.off_segs);
     a.Hq = dims.num_qo_heads;
     a.Hkv = dims.num_kv_heads;
     a.group = dims.num_qo_heads / dims.num_kv_heads;
@@ -313,7 +316,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     a.part_o = reinterpret_cast<float*>(ws + lay.off_part_o);
     a.part_lse = reinterpret_cast<float*>(ws + lay.off_part_lse);
     a.err = device_error_word();
-    if (traced(kKernelAttentionQ4, s, [&] { return launch_attention_q4(a, lay.n_units, s); }) != cudaSuccess)
+    if (traced(kKernelAttentionQ4, s, [&] { return launch_attention_q4(a, lay.n_ranges, s); }) != cudaSuccess)
       return DAA_ERR_CUDA;
     if (lay.n_merges > 0) {
       MergeArgs m{};

@@ -30,11 +30,12 @@
 // and O are fp32.
 //
 // Bound: HBM.  A (page, head) is 18 d bytes; at the measured 6.7 TB/s an SM gets
-// one of d = 128 every 52 ns (99 clocks), in which it can issue about 400 warp
-// instructions; this loop takes about 200.  Warps work alone: each streams its
-// own pages (every fourth of the unit) through its own ring with one bulk copy a
-// page (K and V of a head are side by side), so nothing but the end of the unit
-// synchronises the CTA.
+// one of d = 128 every 52 ns (about 99 clocks), in which it can issue about 400
+// warp instructions.  Warps work alone: each streams a range of pages of its own
+// (the units of one kv head, cut so that every resident warp has the same cost)
+// through its own ring with one bulk copy a page (K and V of a head are side by
+// side), over the ends of requests, and writes its own parts; nothing in a CTA
+// is synchronised.
 #include <climits>
 
 #include "launch.h"
@@ -48,20 +49,21 @@ constexpr int kP = kQ4Page;
 constexpr int kWarps = 4;
 constexpr float kBias = 7.f;     // P = 2^(s - m + kBias)
 constexpr float kRaise = 8.f;    // the maximum is raised when a score passes it by this
+constexpr float kNoMax = -1e37f;  // `off` of a row that has seen no key
+constexpr int kHidden = 0x40000000;  // a key position past every request
 
 template <int D, int NT>
 struct Shape {
   static constexpr int SLICE = q4_slice_bytes(D);
-  static constexpr int STAGE = 2 * SLICE;              // K and V of one (page, head)
-  static constexpr int NSTAGE = D == 128 ? 5 : 8;
-  static constexpr int ROWS = 8 * NT;
+  static constexpr int PAGE = 2 * SLICE;               // K and V of one (page, head)
+  static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // meant to share an SM
+  static constexpr int PAIRS = (NT == 1 ? 3 : (NT == 2 ? 4 : 6)) * (D == 128 ? 1 : 2);  // ring, in pairs of pages
+  static constexpr int STAGE = 2 * PAGE;
   static constexpr int TILES = D / 16;                 // 16-dim tiles of O^T
   static constexpr int KSTEPS = D / 16;
-  static constexpr int RING = kWarps * NSTAGE * STAGE;
-  static constexpr int MERGE = kWarps * ROWS * (D + 2) * 4;
-  static constexpr int BODY = RING > MERGE ? RING : MERGE;
-  static constexpr int OFF_BAR = BODY;
-  static constexpr int SMEM = OFF_BAR + kWarps * NSTAGE * 8;
+  static constexpr int OFF_BAR = kWarps * PAIRS * STAGE;
+  static constexpr int SMEM = OFF_BAR + kWarps * PAIRS * 8;
+  static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory of the CTAs of an SM");
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -85,61 +87,98 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t nibbles(uint32_t lo, uint32_t hi) {  // (lo & 0x0F..) | (hi & 0xF0..)
-  return (lo & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u);
+// (lo & 0x0F0F0F0F) | (hi & 0xF0F0F0F0) in one instruction (two masks would take two)
+__device__ __forceinline__ uint32_t nibbles(uint32_t lo, uint32_t hi) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, 0x0F0F0F0F, 0xE4;" : "=r"(d) : "r"(lo), "r"(hi));
+  return d;
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
+__global__ void __launch_bounds__(32 * kWarps, Shape<D, NT>::CTAS)
 attention_q4_kernel(const AttentionQ4Args a) {
   using S = Shape<D, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, c = lane & 3;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * S::NSTAGE;
-  uint8_t* ring = smem + warp * (S::NSTAGE * S::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * S::PAIRS;
+  uint8_t* ring = smem + warp * (S::PAIRS * S::STAGE);
 
-  // the heads of a unit side by side: their slices of a page are, too
-  const Q4Unit u = a.units[blockIdx.x / a.Hkv];
-  const int kvh = blockIdx.x % a.Hkv;
+  // the heads of a range in warps side by side: their slices of a page are, too
+  const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+  const int range = (int)(id / a.Hkv);
+  if (range >= a.n_ranges) return;
+  const int kvh = (int)(id - (int64_t)range * a.Hkv);
   const int g = a.group;
-  const int rows = u.n_tok * g;
-  const int key_end = a.causal ? min(u.tok_end, u.pos0 + u.n_tok) : u.tok_end;
-  const int pg0 = u.tok_begin / kP + warp;
-  const int pg_end = (key_end + kP - 1) / kP;
-  const int my_n = pg_end > pg0 ? (pg_end - pg0 + kWarps - 1) / kWarps : 0;
+  const int seg_first = __ldg(a.seg_begin + range), seg_end = __ldg(a.seg_begin + range + 1);
+  const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(__ldg(a.kv_exp + kvh)) : 1.f);
+  const float f_v = a.kv_exp ? q4_pow2(__ldg(a.kv_exp + a.Hkv + kvh)) : 1.f;
+  auto pages_of = [&](const Q4Unit& u) {
+    const int key_end = a.causal ? min(u.tok_end, u.pos0 + u.n_tok) : u.tok_end;
+    return max(0, (key_end + kP - 1) / kP - u.tok_begin / kP);
+  };
 
-  if (threadIdx.x == 0) grid_dep_launch();  // the merge may launch; it waits for this grid
+  grid_dep_launch();  // the merge may launch; it waits for this grid
   if (lane == 0) {
-    for (int i = 0; i < S::NSTAGE; ++i) mbar_init(&full[i], 1);
+    for (int i = 0; i < S::PAIRS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   __syncwarp();
 
-  // page ids, 32 of this warp's pages at a time (lane l: page base + l)
+  // The loads run ahead of the products by the ring's depth, over the end of a
+  // unit into the next ones: in_seg, in_j, in_n are the unit, page and page count
+  // of the next pair to load; lane l holds the id of page in_j - in_j % 32 + l.
+  int in_seg = seg_first - 1, in_j = 0, in_n = 0;
+  const int32_t* in_ids = nullptr;
   int32_t ids = 0;
-  auto load_ids = [&](int k0) {
-    const int k = k0 + lane;
-    ids = k < my_n ? __ldg(a.page_indices + u.page_base + pg0 + k * kWarps) : 0;
+  const uint8_t* head = a.pool + (int64_t)kvh * S::PAGE;
+  const int64_t page_stride = (int64_t)a.Hkv * S::PAGE;
+  auto load_ids = [&]() {
+    ids = in_j + lane < in_n ? __ldg(in_ids + in_j + lane) : 0;
     if (ids < 0 || ids >= a.num_pages) {
       set_device_error(a.err, kDevErrPageRange);
       ids = 0;  // a valid page instead; the output is undefined anyway
     }
   };
-  auto issue = [&](int k) {  // whole warp, k < my_n
-    const int64_t page = __shfl_sync(0xffffffffu, ids, k & 31);
-    if (lane == 0) {
-      const int st = k % S::NSTAGE;
-      mbar_arrive_expect_tx(&full[st], S::STAGE);
-      bulk_g2s(ring + st * S::STAGE, a.pool + (page * a.Hkv + kvh) * S::STAGE, S::STAGE, &full[st]);
+  auto load_next = [&](int st) {  // whole warp
+    while (in_j >= in_n) {
+      if (in_seg + 1 >= seg_end) return;
+      const Q4Unit u = a.units[++in_seg];
+      in_n = pages_of(u);
+      in_ids = a.page_indices + u.page_base + u.tok_begin / kP;
+      in_j = 0;
+      load_ids();
     }
-    if ((k & 31) == 31) load_ids(k + 1);
+    // pages in_j and in_j + 1, by the lanes that hold their ids
+    const int k = lane - (in_j & 31);
+    if (k == 0) mbar_arrive_expect_tx(&full[st], in_j + 1 < in_n ? 2 * S::PAGE : S::PAGE);
+    if ((k & ~1) == 0 && in_j + k < in_n)
+      bulk_g2s(ring + st * S::STAGE + k * S::PAGE, head + ids * page_stride, S::PAGE, &full[st]);
+    in_j += 2;
+    if ((in_j & 31) == 0) load_ids();
   };
-  load_ids(0);
-  for (int k = 0; k < S::NSTAGE && k < my_n; ++k) issue(k);
+#pragma unroll 1
+  for (int i = 0; i < S::PAIRS; ++i) load_next(i);
+
+  // Key of row r of S^T: the keys of a pair change places in odd threads of a
+  // quad, so that the V rows a quad reads at once lie in different banks.
+  const int key_r = r ^ ((r >> 1) & 1);
+  const int key_v = 2 * c + (c & 1);                   // first key of a thread's pair of V rows
+  const uint32_t pair_sel = (c & 1) ? 0x1032u : 0x3210u;
+  const int k_off = key_r * (D / 2) + c * (D / 8);     // K codes of the thread, key row r
+  const int v_off = S::SLICE + key_v * (D / 2) + r * (D / 16);
+  const int v_step = (c & 1) ? -(D / 2) : D / 2;       // to the pair's other key
+  const int sv_off = S::SLICE + 8 * D + (D == 128 ? r : r >> 1) * kP + 2 * c;
+
+  int st = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int seg = seg_first; seg < seg_end; ++seg) {
+  const Q4Unit u = a.units[seg];
+  const int rows = u.n_tok * g;
+  const int n_pages = pages_of(u);
 
   // Q^T fragments: rows n = 8 t + r, this thread's dims [c * D/4, (c + 1) * D/4)
-  const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(__ldg(a.kv_exp + kvh)) : 1.f);
   uint32_t qf[NT][S::KSTEPS][2];
   float fs[NT][2];       // score factor of rows 8 t + 2 c, + 1
   int lim[NT][2];        // keys of those rows: [0, lim)
@@ -190,52 +229,57 @@ attention_q4_kernel(const AttentionQ4Args a) {
   lim_min = __reduce_min_sync(0xffffffffu, lim_min);
 
   float o[NT][S::TILES][4];
-  float m_run[NT][2], l_run[NT][2];
+  // weights are 2^(s * fs - off), off = running maximum - kBias; before the first
+  // visible key off is so low that any score raises it, and hidden ones (-inf)
+  // weigh nothing
+  float off[NT][2], l_run[NT][2];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m_run[t][0] = m_run[t][1] = -INFINITY;
+    off[t][0] = off[t][1] = kNoMax;
     l_run[t][0] = l_run[t][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < S::TILES; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[t][i][e] = 0.f;
   }
-  // the two keys of a pair are swapped in odd threads of a quad (see the V loads)
-  const uint32_t pair_sel = (c & 1) ? 0x1032u : 0x3210u;
+#pragma unroll 1
+  for (int j = 0; j < n_pages; j += 2) {
+    mbar_wait(&full[st], phase, a.err);
+    // the second page of a last single one is whatever the slot holds, with every
+    // key hidden
+    const uint8_t* stage = ring + st * S::STAGE;
+    const int key0[2] = {u.tok_begin + j * kP, j + 1 < n_pages ? u.tok_begin + (j + 1) * kP : kHidden};
 
-  constexpr int PPI = 2;  // pages per pass of the loop
-  for (int k = 0; k < my_n; k += PPI) {
-    // ---- S^T of two pages
-    float s[PPI][NT][4];
+    // ---- S^T of the two pages
+    float s[2][NT][4];
 #pragma unroll
-    for (int p = 0; p < PPI; ++p) {
+    for (int p = 0; p < 2; ++p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[p][t][e] = 0.f;
-      if (k + p >= my_n) continue;
-      const int st = (k + p) % S::NSTAGE;
-      mbar_wait(&full[st], ((k + p) / S::NSTAGE) & 1, a.err);
-      const uint8_t* kb = ring + st * S::STAGE;
       constexpr int W = D / 32;  // code words of a thread per key row
       uint32_t w0[W], w1[W];
-      uint32_t sc0[2], sc1[2];   // block scales of the thread's dims, keys r and r + 8
+      uint32_t sc0[2], sc1[2];   // block scales of the thread's dims, key rows r and r + 8
+      const uint8_t* kb = stage + p * S::PAGE + k_off;
       if constexpr (D == 128) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(kb + r * 64 + c * 16);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(kb + (r + 8) * 64 + c * 16);
+        const uint4 x0 = *reinterpret_cast<const uint4*>(kb);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(kb + 8 * 64);
         w0[0] = x0.x; w0[1] = x0.y; w0[2] = x0.z; w0[3] = x0.w;
         w1[0] = x1.x; w1[1] = x1.y; w1[2] = x1.z; w1[3] = x1.w;
-        const uint32_t y0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(kb + 1024 + r * 8 + 2 * c));
-        const uint32_t y1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(kb + 1024 + (r + 8) * 8 + 2 * c));
+        const uint8_t* sb = stage + p * S::PAGE + 1024 + key_r * 8 + 2 * c;
+        const uint32_t y0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb));
+        const uint32_t y1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb + 64));
         sc0[0] = __byte_perm(y0, y0, 0x1010); sc0[1] = __byte_perm(y0, y0, 0x3232);
         sc1[0] = __byte_perm(y1, y1, 0x1010); sc1[1] = __byte_perm(y1, y1, 0x3232);
       } else {
-        const uint2 x0 = *reinterpret_cast<const uint2*>(kb + r * 32 + c * 8);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(kb + (r + 8) * 32 + c * 8);
+        const uint2 x0 = *reinterpret_cast<const uint2*>(kb);
+        const uint2 x1 = *reinterpret_cast<const uint2*>(kb + 8 * 32);
         w0[0] = x0.x; w0[1] = x0.y;
         w1[0] = x1.x; w1[1] = x1.y;
-        // one block a thread: keys r and r + 8 in one conversion
-        const uint32_t y = e4m3x2_to_f16x2((uint16_t)(kb[512 + r * 4 + c] | (kb[512 + (r + 8) * 4 + c] << 8)));
+        // one block a thread: key rows r and r + 8 in one conversion
+        const uint8_t* sb = stage + p * S::PAGE + 512 + key_r * 4 + c;
+        const uint32_t y = e4m3x2_to_f16x2((uint16_t)(sb[0] | (sb[32] << 8)));
         sc0[0] = sc0[1] = __byte_perm(y, y, 0x1010);
         sc1[0] = sc1[1] = __byte_perm(y, y, 0x3232);
       }
@@ -257,219 +301,200 @@ attention_q4_kernel(const AttentionQ4Args a) {
         }
       }
     }
-
-    // ---- scores in the log2 domain, hidden keys at -inf
-    bool raise = false;
+    const bool tail = max(key0[0], key0[1]) + kP > lim_min;  // some row does not see some key
+    if (tail) {
+      __syncwarp();  // a branch of its own: predicated, these would be issued for every pair
 #pragma unroll
-    for (int p = 0; p < PPI; ++p) {
-      const int key = (pg0 + (k + p) * kWarps) * kP + r;  // of s[..][0], [1]; + 8 of [2], [3]
-      const bool masked = k + p >= my_n || key - r + kP > lim_min;
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[p][t][e] * fs[t][e & 1];
-          if (masked && (k + p >= my_n || key + (e >= 2 ? 8 : 0) >= lim[t][e & 1])) x = -INFINITY;
-          s[p][t][e] = x;
-          raise |= x > m_run[t][e & 1] + kRaise;
-        }
+          for (int e = 0; e < 4; ++e)
+            if (key0[p] + key_r + (e >= 2 ? 8 : 0) >= lim[t][e & 1]) s[p][t][e] = -INFINITY;
     }
-    if (__any_sync(0xffffffffu, raise)) {
+
+    // ---- exponents; the maximum is raised when one passes it by kRaise
+    float x[2][NT][4];
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[p][t][e] = fmaf(s[p][t][e], fs[t][e & 1], -off[t][e & 1]);
+        top = fmax3(top, x[p][t][0], x[p][t][1]);
+        top = fmax3(top, x[p][t][2], x[p][t][3]);
+      }
+    }
+    if (__any_sync(0xffffffffu, top > kRaise + kBias)) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          float mx = m_run[t][b];
-#pragma unroll
-          for (int p = 0; p < PPI; ++p) mx = fmax3(mx, s[p][t][b], s[p][t][b + 2]);
+          float mx = fmax3(s[0][t][b], s[0][t][b + 2], fmaxf(s[1][t][b], s[1][t][b + 2]));
 #pragma unroll
           for (int m = 4; m <= 16; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-          const float alpha = mx == -INFINITY ? 1.f : ex2_approx(m_run[t][b] - mx);
-          m_run[t][b] = mx;
+          const float raised = fmaxf(off[t][b], mx * fs[t][b] - kBias);
+          const float alpha = ex2_approx(off[t][b] - raised);  // 0 from kNoMax
+          off[t][b] = raised;
           l_run[t][b] *= alpha;
 #pragma unroll
           for (int i = 0; i < S::TILES; ++i) {
             o[t][i][b] *= alpha;
             o[t][i][b + 2] *= alpha;
           }
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            x[p][t][b] = fmaf(s[p][t][b], fs[t][b], -off[t][b]);
+            x[p][t][b + 2] = fmaf(s[p][t][b + 2], fs[t][b], -off[t][b]);
+          }
         }
     }
 
     // ---- P (fp16), transposed into the B operand of O^T += V^T P^T
-    uint32_t pb[PPI][NT][2];
+    uint32_t pf[2][NT][2];
 #pragma unroll
-    for (int p = 0; p < PPI; ++p)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float m = m_run[t][i & 1];
-          // a row with no visible key yet keeps m = -inf: its scores are -inf too
-          e[i] = ex2_approx(s[p][t][i] - (m == -INFINITY ? 0.f : m - kBias));
-        }
+        for (int i = 0; i < 4; ++i) e[i] = ex2_approx(x[p][t][i]);
         l_run[t][0] += e[0] + e[2];
         l_run[t][1] += e[1] + e[3];
-        pb[p][t][0] = __byte_perm(transpose8(pack_f16x2(e[0], e[1])), 0u, pair_sel);
-        pb[p][t][1] = __byte_perm(transpose8(pack_f16x2(e[2], e[3])), 0u, pair_sel);
+        pf[p][t][0] = transpose8(pack_f16x2(e[0], e[1]));
+        pf[p][t][1] = transpose8(pack_f16x2(e[2], e[3]));
       }
 
     // ---- O^T += V^T P^T
 #pragma unroll
-    for (int p = 0; p < PPI; ++p) {
-      if (k + p >= my_n) continue;
-      const int st = (k + p) % S::NSTAGE;
-      const uint8_t* vb = ring + st * S::STAGE + S::SLICE;
+    for (int p = 0; p < 2; ++p) {
       constexpr int W = D / 64;        // code words of a thread per key
-      constexpr int BPR = D / 16;      // bytes of a thread per key
-      // Keys 2c, 2c + 1 (pair 0) and 2c + 8, 2c + 9 (pair 1) of the page.  Key rows
-      // of one parity share their banks (d = 128), so odd threads of a quad read
-      // the pair's second key first; P and the scales are swapped to match.
-      uint32_t w[2][2][W];
-#pragma unroll
-      for (int pr = 0; pr < 2; ++pr)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* row = vb + (8 * pr + 2 * c + (h ^ (c & 1))) * (D / 2) + r * BPR;
-          if constexpr (D == 128) {
-            const uint2 x = *reinterpret_cast<const uint2*>(row);
-            w[pr][h][0] = x.x;
-            w[pr][h][W - 1] = x.y;
-          } else {
-            w[pr][h][0] = *reinterpret_cast<const uint32_t*>(row);
-          }
-        }
-      const int blk = D == 128 ? r : r >> 1;
+      uint32_t w[2][2][W];             // [pair of keys][key][word]
       uint32_t sc[2];
-      const int key0 = (pg0 + (k + p) * kWarps) * kP;
 #pragma unroll
       for (int pr = 0; pr < 2; ++pr) {
-        sc[pr] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(vb + 8 * D + blk * kP + 8 * pr + 2 * c));
-        // slots past the last key may hold anything: their scales count as zero
-        const int over = key0 + 8 * pr + 2 * c - u.kv_len;  // >= 0: both keys, -1: the second
-        if (over >= -1) sc[pr] = over >= 0 ? 0u : sc[pr] & 0xFFFFu;
-        sc[pr] = __byte_perm(sc[pr], 0u, pair_sel);
-      }
+        const uint8_t* row = stage + p * S::PAGE + v_off + pr * (4 * D);
 #pragma unroll
-      for (int x = 0; x < W; ++x) {
-        uint32_t lo[2][4], hi[2][4];  // dims 2i, 2i + 1 of tile 4 x + j, for the two pairs
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (D == 128) {
+            const uint2 y = *reinterpret_cast<const uint2*>(row + h * v_step);
+            w[pr][h][0] = y.x;
+            w[pr][h][W - 1] = y.y;
+          } else {
+            w[pr][h][0] = *reinterpret_cast<const uint32_t*>(row + h * v_step);
+          }
+        }
+        sc[pr] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(stage + p * S::PAGE + sv_off + 8 * pr));
+      }
+      if (tail) {
+        __syncwarp();
+        // slots past the last key may hold anything: their scales count as zero
 #pragma unroll
         for (int pr = 0; pr < 2; ++pr) {
-          e2m1x8_to_f16x2(nibbles(w[pr][0][x], w[pr][1][x] << 4), lo[pr]);
-          e2m1x8_to_f16x2(nibbles(w[pr][0][x] >> 4, w[pr][1][x]), hi[pr]);
+          const int over = key0[p] + 8 * pr + 2 * c - u.kv_len;  // >= 0: both keys, -1: the second
+          if (over >= -1) sc[pr] = over >= 0 ? 0u : sc[pr] & 0xFFFFu;
+        }
+      }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            lo[pr][j] = mul_f16x2(lo[pr][j], sc[pr]);
-            hi[pr][j] = mul_f16x2(hi[pr][j], sc[pr]);
+      for (int pr = 0; pr < 2; ++pr) sc[pr] = __byte_perm(sc[pr], 0u, pair_sel);
+#pragma unroll
+      for (int y = 0; y < W; ++y) {
+        uint32_t lo[2][4], hi[2][4];  // dims 2i, 2i + 1 of tile 4 y + i, for the two pairs
+#pragma unroll
+        for (int pr = 0; pr < 2; ++pr) {
+          e2m1x8_to_f16x2(nibbles(w[pr][0][y], w[pr][1][y] << 4), lo[pr]);
+          e2m1x8_to_f16x2(nibbles(w[pr][0][y] >> 4, w[pr][1][y]), hi[pr]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            lo[pr][i] = mul_f16x2(lo[pr][i], sc[pr]);
+            hi[pr][i] = mul_f16x2(hi[pr][i], sc[pr]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            mma_f16(o[t][4 * x + j], lo[0][j], hi[0][j], lo[1][j], hi[1][j], pb[p][t][0], pb[p][t][1]);
+            mma_f16(o[t][4 * y + i], lo[0][i], hi[0][i], lo[1][i], hi[1][i], pf[p][t][0], pf[p][t][1]);
       }
     }
     __syncwarp();  // both pages have been read
-#pragma unroll
-    for (int p = 0; p < PPI; ++p)
-      if (k + p + S::NSTAGE < my_n) issue(k + p + S::NSTAGE);
+    load_next(st);
+    if (++st == S::PAIRS) {
+      st = 0;
+      phase ^= 1u;
+    }
   }
 
-  // ---- join the four warps in shared memory (the rings are free), then write
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int m = 4; m <= 16; m <<= 1) l_run[t][b] += __shfl_xor_sync(0xffffffffu, l_run[t][b], m);
-  __syncthreads();
-  float* mo = reinterpret_cast<float*>(smem);        // [warp][row][D]
-  float* mm = mo + kWarps * S::ROWS * D;             // [warp][row]
-  float* ml = mm + kWarps * S::ROWS;                 // [warp][row]
+  // ---- write: a thread has D/8 dims in a row of two rows (2c, 2c + 1) a tile
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
+      float L = l_run[t][b];
+#pragma unroll
+      for (int m = 4; m <= 16; m <<= 1) L += __shfl_xor_sync(0xffffffffu, L, m);
       const int n = 8 * t + 2 * c + b;
       if (n >= rows) continue;
-      float* dst = mo + (warp * S::ROWS + n) * D + r * (D / 8);
+      const float inv = L > 0.f || L != L ? f_v / L : 0.f;  // no visible key: zero, lse -inf
+      const float lse2 = off[t][b] + __log2f(L);            // a weight is 2^(s - off)
+      const int tok = n / g;
+      const int hq = kvh * g + (n - tok * g);
+      if (u.part < 0) {
+        const int64_t row = (int64_t)(u.q_row + tok) * a.Hq + hq;
+        uint4* dst = reinterpret_cast<uint4*>(a.out + row * D + r * (D / 8));
 #pragma unroll
-      for (int i = 0; i < S::TILES; i += 2)
-        *reinterpret_cast<float4*>(dst + 2 * i) =
-            make_float4(o[t][i][b], o[t][i][b + 2], o[t][i + 1][b], o[t][i + 1][b + 2]);
-      if (r == 0) {
-        mm[warp * S::ROWS + n] = m_run[t][b];
-        ml[warp * S::ROWS + n] = l_run[t][b];
+        for (int i = 0; i < S::TILES; i += 4) {
+          uint4 pk;
+          pk.x = pack_bf16x2(o[t][i][b] * inv, o[t][i][b + 2] * inv);
+          pk.y = pack_bf16x2(o[t][i + 1][b] * inv, o[t][i + 1][b + 2] * inv);
+          pk.z = pack_bf16x2(o[t][i + 2][b] * inv, o[t][i + 2][b + 2] * inv);
+          pk.w = pack_bf16x2(o[t][i + 3][b] * inv, o[t][i + 3][b + 2] * inv);
+          dst[i / 4] = pk;
+        }
+        if (r == 0 && a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
+      } else {
+        const int64_t row = ((int64_t)u.part + (int64_t)tok * u.part_stride) * a.Hq + hq;
+        float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + r * (D / 8));
+#pragma unroll
+        for (int i = 0; i < S::TILES; i += 2)
+          dst[i / 2] = make_float4(o[t][i][b] * inv, o[t][i][b + 2] * inv, o[t][i + 1][b] * inv,
+                                   o[t][i + 1][b + 2] * inv);
+        if (r == 0) a.part_lse[row] = lse2;
       }
-    }
-  __syncthreads();
-  const float f_v = a.kv_exp ? q4_pow2(__ldg(a.kv_exp + a.Hkv + kvh)) : 1.f;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += 32 * kWarps) {
-    const int n = i / (D / 4), d0 = (i - n * (D / 4)) * 4;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * S::ROWS + n]);
-    float L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float m = mm[w * S::ROWS + n];
-      const float wt = m == -INFINITY ? 0.f : ex2_approx(m - M);
-      const float4 v = *reinterpret_cast<const float4*>(mo + (w * S::ROWS + n) * D + d0);
-      L += wt * ml[w * S::ROWS + n];
-      acc[0] += wt * v.x;
-      acc[1] += wt * v.y;
-      acc[2] += wt * v.z;
-      acc[3] += wt * v.w;
-    }
-    const float inv = L > 0.f ? f_v / L : 0.f;  // no visible key: zero, lse -inf
-    const float lse2 = M - kBias + __log2f(L);
-    const int tok = n / g;
-    const int hq = kvh * g + (n - tok * g);
-    if (u.part < 0) {
-      const int64_t row = (int64_t)(u.q_row + tok) * a.Hq + hq;
-      uint2 pk;
-      pk.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-      pk.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-      *reinterpret_cast<uint2*>(a.out + row * D + d0) = pk;
-      if (d0 == 0 && a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
-    } else {
-      const int64_t row = ((int64_t)u.part + (int64_t)tok * u.part_stride) * a.Hq + hq;
-      *reinterpret_cast<float4*>(a.part_o + row * D + d0) =
-          make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-      if (d0 == 0) a.part_lse[row] = lse2;
     }
   }
 }
 
 template <int D, int NT>
-cudaError_t launch_t(const AttentionQ4Args& a, int n_units, cudaStream_t stream) {
+cudaError_t launch_t(AttentionQ4Args a, int n_ranges, cudaStream_t stream) {
   using S = Shape<D, NT>;
+  a.n_ranges = n_ranges;
   auto kern = attention_q4_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
-  if ((int64_t)a.Hkv * n_units > INT32_MAX) return cudaErrorInvalidValue;
-  kern<<<a.Hkv * n_units, 32 * kWarps, S::SMEM, stream>>>(a);
+  const int64_t warps = (int64_t)a.Hkv * n_ranges;
+  kern<<<(unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, S::SMEM, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_d(AttentionQ4Args a, const int (&n_units)[kQ4Classes], cudaStream_t stream) {
+cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < kQ4Classes && e == cudaSuccess; ++i) {
-    if (n_units[i] == 0) continue;
-    e = i == 0 ? launch_t<D, 1>(a, n_units[i], stream)
-               : (i == 1 ? launch_t<D, 2>(a, n_units[i], stream) : launch_t<D, 4>(a, n_units[i], stream));
-    a.units += n_units[i];
+    if (n_ranges[i] == 0) continue;
+    e = i == 0 ? launch_t<D, 1>(a, n_ranges[i], stream)
+               : (i == 1 ? launch_t<D, 2>(a, n_ranges[i], stream) : launch_t<D, 4>(a, n_ranges[i], stream));
+    a.seg_begin += n_ranges[i];
   }
   return e;
 }
 
 }  // namespace
 
-cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_units)[kQ4Classes],
+cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
                                 cudaStream_t stream) {
-  return a.head_dim == 128 ? launch_d<128>(a, n_units, stream) : launch_d<64>(a, n_units, stream);
+  return a.head_dim == 128 ? launch_d<128>(a, n_ranges, stream) : launch_d<64>(a, n_ranges, stream);
 }
 
 }  // namespace daa

@@ -198,13 +198,15 @@ cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const 
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
                                  int64_t num_pages, void* out, int* err, cudaStream_t stream);
 
-// Attention over the 4-bit pages (decode_q4.cu); n_units per class, in order.
+// Attention over the 4-bit pages (decode_q4.cu); n_ranges per class, in order.
 struct AttentionQ4Args {
   const uint16_t* q;       // [nnz_qo][Hq][d]
   const uint8_t* pool;     // [num_pages][Hkv][2][9 d]
   const int32_t* kv_exp;   // [2][Hkv] or null
   const int32_t* page_indices;
   const Q4Unit* units;
+  const int32_t* seg_begin;  // range i: units [seg_begin[i], seg_begin[i + 1])
+  int n_ranges;            // set by the launch of each class
   int Hq, Hkv, group, head_dim;
   int64_t num_pages;
   int causal;
@@ -215,7 +217,7 @@ struct AttentionQ4Args {
   float* part_lse;         // [n_parts][Hq] (log2 domain)
   int* err;
 };
-cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_units)[kQ4Classes],
+cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
                                 cudaStream_t stream);
 
 // SMs of the current device, and a launch between the tracer's events (api.cu).

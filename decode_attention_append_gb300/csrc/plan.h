@@ -20,7 +20,8 @@ struct DecodeUnit {
 
 // One key split of (some new tokens of) a request read from the 4-bit cache: all
 // query heads of a kv head of its n_tok tokens over keys [tok_begin, tok_end).
-// One CTA per (unit, kv head).  Splits are page aligned.
+// A warp takes a range of consecutive units, for one kv head.  Splits are page
+// aligned.
 struct Q4Unit {
   int32_t q_row;        // row of the first of the tokens
   int32_t n_tok;
@@ -34,7 +35,7 @@ struct Q4Unit {
   int32_t pad0, pad1, pad2;
 };
 // Units come in classes by the query rows (tokens x heads) they hold, each its
-// own launch: up to 8, 16, 32.
+// own ranges and launch: up to 8, 16, 32.
 constexpr int kQ4Classes = 3;
 
 // softmax_merge of the partials of one query row: n_parts consecutive slots

@@ -20,23 +20,29 @@
 namespace daa {
 
 constexpr int kQ4NativeRows = 64;
-constexpr int kQ4UnitsPerSm = 16;
-constexpr int kQ4MinPages = 16;
-constexpr int kQ4UnitRows = 32;  // rows a unit holds at most
+constexpr int kQ4UnitRows = 32;   // rows a unit holds at most
+constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages
+constexpr int kQ4MinPages = 4;    // pages of a range at least
+
+inline int q4_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : 2); }
+// Warps of the class's kernel on an SM (its shared memory and registers).
+inline int q4_warps_per_sm(int cls) { return 4 * (4 - cls); }
 
 // Sections of the workspace, all worked out from the counts and the layout of
 // the bf16 requests' plan.  The first plan_bytes are copied from the host.
 struct Q4Layout {
-  int n_units[kQ4Classes] = {0, 0, 0};
-  int n_merges = 0, n_parts = 0, n_scratch = 0;
+  int n_ranges[kQ4Classes] = {0, 0, 0};
+  int n_units = 0, n_merges = 0, n_parts = 0, n_scratch = 0;
   PlanLayout sub;
-  size_t off_units, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
+  size_t off_units, off_segs, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
       off_pool, total;
-  int units() const { return n_units[0] + n_units[1] + n_units[2]; }
+  int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2]; }
   void finish(const daa_dims& d) {
     size_t off = 0;
     off_units = off;
-    off = plan_align_up(off + (size_t)units() * sizeof(Q4Unit));
+    off = plan_align_up(off + (size_t)n_units * sizeof(Q4Unit));
+    off_segs = off;
+    off = plan_align_up(off + (size_t)(ranges() + 1) * sizeof(int32_t));
     off_merges = off;
     off = plan_align_up(off + (size_t)n_merges * sizeof(MergeItem));
     off_src = off;
@@ -52,7 +58,7 @@ struct Q4Layout {
     off = plan_align_up(off + (size_t)n_parts * d.num_qo_heads * sizeof(float));
     off_pool = off;
     off = plan_align_up(off + (size_t)n_scratch * 2 * d.num_kv_heads * d.page_size * d.head_dim * 2);
-    total = units() == 0 && sub.total == 0 ? 0 : off;
+    total = n_units == 0 && sub.total == 0 ? 0 : off;
   }
 };
 
@@ -64,6 +70,7 @@ struct Q4Plan {
   Vec<DecodeUnit> sub_units;
   Vec<MergeItem> sub_merges;
   Vec<PrefillTile> sub_tiles;
+  std::vector<int32_t> seg_begin;              // [ranges + 1]
   std::vector<int32_t> src;                    // scratch page -> index into page_indices
   std::vector<int32_t> req, sub_qo, sub_kv, sub_last;  // the bf16 requests' table
   Q4Layout lay;
@@ -74,6 +81,7 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
                          const daa_dims& d, int sms, Q4Plan<Vec>& pl) {
   pl.units.clear();
   pl.merges.clear();
+  pl.seg_begin.assign(1, 0);
   pl.src.clear();
   pl.req.clear();
   pl.sub_qo.assign(1, 0);
@@ -90,7 +98,12 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
   const int P = d.page_size;
   const int g = d.num_qo_heads / d.num_kv_heads;
   const int tpu = kQ4UnitRows / g;  // tokens of a unit
-  int64_t native_pages = 0;         // pages that units read, once per unit of a request's tokens
+  // what units are cut from: some new tokens of a request, by class
+  struct Stream {
+    int r, t0, n_tok, pages, n_units, unit0;
+  };
+  thread_local std::vector<Stream> streams[kQ4Classes];
+  for (auto& v : streams) v.clear();
   for (int r = 0; r < batch; ++r) {
     const int64_t nq = (int64_t)qo[r + 1] - qo[r];
     const int64_t np = (int64_t)kv[r + 1] - kv[r];
@@ -106,56 +119,75 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
       pl.sub_last.push_back(last[r]);
       for (int64_t p = 0; p < np; ++p) pl.src.push_back((int32_t)(kv[r] + p));
     } else if (nq > 0) {
-      native_pages += np * ((nq + tpu - 1) / tpu);
-    }
-  }
-  // Key splits: about kQ4UnitsPerSm units (times kv heads) an SM, so that the
-  // longest is a small part of the pass and the parts to join stay few; at least
-  // kQ4MinPages pages, a few for each of a CTA's warps.
-  int64_t split = (native_pages * d.num_kv_heads + (int64_t)sms * kQ4UnitsPerSm - 1) /
-                  ((int64_t)sms * kQ4UnitsPerSm);
-  split = std::max<int64_t>(kQ4MinPages, (split + 3) / 4 * 4);
-  int n_parts = 0;
-  for (int r = 0; r < batch; ++r) {
-    const int nq = qo[r + 1] - qo[r];
-    if (nq == 0 || nq * g > kQ4NativeRows) continue;
-    const int np = kv[r + 1] - kv[r];
-    const int kv_len = (np - 1) * P + last[r];
-    // splits cut the keys that token 0 sees, so every split starts at a key that
-    // each token sees; the last one also takes the tail
-    const int64_t vis = (int64_t)kv_len - nq + 1;
-    const int nsplit = (int)((vis + split * P - 1) / (split * P));
-    int part0 = -1;
-    if (nsplit > 1) {
-      part0 = n_parts;
-      for (int t = 0; t < nq; ++t)
-        if (!pl.merges.push_back(MergeItem{qo[r] + t, part0 + t * nsplit, nsplit, -1}))
-          return DAA_ERR_WORKSPACE;
-      n_parts += nsplit * nq;
-    }
-    for (int t0 = 0; t0 < nq; t0 += tpu)
-      for (int s = 0; s < nsplit; ++s) {
-        Q4Unit u{};
-        u.q_row = qo[r] + t0;
-        u.n_tok = std::min(tpu, nq - t0);
-        u.pos0 = kv_len - nq + t0;
-        u.kv_len = kv_len;
-        u.page_base = kv[r];
-        u.tok_begin = (int)(s * split * P);
-        u.tok_end = s == nsplit - 1 ? kv_len : (int)((s + 1) * split * P);
-        u.part = part0 >= 0 ? part0 + t0 * nsplit + s : -1;
-        u.part_stride = nsplit;
-        if (!pl.units.push_back(u)) return DAA_ERR_WORKSPACE;
+      for (int t0 = 0; t0 < nq; t0 += tpu) {
+        const int n = std::min<int>(tpu, (int)nq - t0);
+        streams[q4_class(n * g)].push_back(Stream{r, t0, n, (int)np, 0, 0});
       }
+    }
   }
-  // by class, then longest first
-  auto cls = [g](const Q4Unit& u) { return u.n_tok * g <= 8 ? 0 : (u.n_tok * g <= 16 ? 1 : 2); };
-  std::sort(pl.units.data(), pl.units.data() + pl.units.size(), [&](const Q4Unit& x, const Q4Unit& y) {
-    if (cls(x) != cls(y)) return cls(x) < cls(y);
-    const int a = x.tok_end - x.tok_begin, b = y.tok_end - y.tok_begin;
-    return a != b ? a > b : (x.q_row != y.q_row ? x.q_row < y.q_row : x.tok_begin < y.tok_begin);
-  });
-  for (size_t i = 0; i < pl.units.size(); ++i) ++pl.lay.n_units[cls(pl.units.data()[i])];
+  // Ranges: one for every warp that can be resident (over the kv heads), each with
+  // the same cost of pages and units, so that all end together and none waits for
+  // a second wave; a unit is cut where a range is full.
+  int n_parts = 0;
+  for (int cls = 0; cls < kQ4Classes; ++cls) {
+    auto& ss = streams[cls];
+    if (ss.empty()) continue;
+    int64_t pages = 0;
+    for (const Stream& s : ss) pages += s.pages;
+    int64_t n_ranges = (int64_t)sms * q4_warps_per_sm(cls) / d.num_kv_heads;
+    n_ranges = std::max<int64_t>(1, std::min<int64_t>(n_ranges, pages / kQ4MinPages));
+    const int64_t cost = pages + kQ4UnitPages * ((int64_t)ss.size() + n_ranges - 1);
+    const int64_t each = (cost + n_ranges - 1) / n_ranges;
+    const int first_range = (int)pl.seg_begin.size() - 1;
+    int64_t room = each;  // of the open range
+    for (Stream& s : ss) {
+      s.unit0 = (int)pl.units.size();
+      for (int at = 0; at < s.pages;) {
+        const int left = s.pages - at;
+        const bool last_range = (int)pl.seg_begin.size() - first_range == (int)n_ranges;
+        if (!last_range && room < std::min<int64_t>(left, kQ4MinPages / 2) + kQ4UnitPages) {
+          pl.seg_begin.push_back((int32_t)pl.units.size());
+          room = each;
+          continue;
+        }
+        int n = last_range ? left : (int)std::min<int64_t>(left, room - kQ4UnitPages);
+        if (left - n < kQ4MinPages / 2) n = left;  // no small rest
+        Q4Unit u{};
+        u.tok_begin = at * P;
+        u.tok_end = (at + n) * P;
+        if (!pl.units.push_back(u)) return DAA_ERR_WORKSPACE;
+        room -= n + kQ4UnitPages;
+        at += n;
+      }
+      s.n_units = (int)pl.units.size() - s.unit0;
+    }
+    pl.seg_begin.push_back((int32_t)pl.units.size());
+    pl.lay.n_ranges[cls] = (int)pl.seg_begin.size() - 1 - first_range;
+    // the units' requests and partial slots: token t of unit s of a stream writes
+    // slot part0 + t * n_units + s, so a token's parts lie side by side
+    for (const Stream& s : ss) {
+      const int nq = qo[s.r + 1] - qo[s.r];
+      const int kv_len = (s.pages - 1) * P + last[s.r];
+      const int part0 = s.n_units > 1 ? n_parts : -1;
+      if (part0 >= 0) {
+        for (int t = 0; t < s.n_tok; ++t)
+          if (!pl.merges.push_back(MergeItem{qo[s.r] + s.t0 + t, part0 + t * s.n_units, s.n_units, -1}))
+            return DAA_ERR_WORKSPACE;
+        n_parts += s.n_units * s.n_tok;
+      }
+      for (int i = 0; i < s.n_units; ++i) {
+        Q4Unit& u = pl.units.data()[s.unit0 + i];
+        u.q_row = qo[s.r] + s.t0;
+        u.n_tok = s.n_tok;
+        u.pos0 = kv_len - nq + s.t0;
+        u.kv_len = kv_len;
+        u.page_base = kv[s.r];
+        u.tok_end = std::min(u.tok_end, kv_len);
+        u.part = part0 >= 0 ? part0 + i : -1;
+        u.part_stride = s.n_units;
+      }
+    }
+  }
   // the bf16 requests: their own plan, then its query rows moved to their place in the batch
   daa_dims sd = d;
   sd.num_pages = std::max<int64_t>(1, (int64_t)pl.src.size());
@@ -178,6 +210,7 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     PrefillTile& t = pl.sub_tiles.data()[i];
     t.q_row0 = moved(t.q_row0);
   }
+  pl.lay.n_units = (int)pl.units.size();
   pl.lay.n_parts = n_parts;
   pl.lay.n_merges = (int)pl.merges.size();
   pl.lay.n_scratch = (int)pl.src.size();
@@ -190,7 +223,10 @@ template <template <class> class Vec>
 void plan_stage_q4(const Q4Plan<Vec>& pl, uint8_t* host) {
   const Q4Layout& lay = pl.lay;
   std::memset(host, 0, lay.plan_bytes);
-  if (lay.units()) std::memcpy(host + lay.off_units, pl.units.data(), lay.units() * sizeof(Q4Unit));
+  if (lay.n_units) {
+    std::memcpy(host + lay.off_units, pl.units.data(), lay.n_units * sizeof(Q4Unit));
+    std::memcpy(host + lay.off_segs, pl.seg_begin.data(), pl.seg_begin.size() * sizeof(int32_t));
+  }
   if (lay.n_merges) std::memcpy(host + lay.off_merges, pl.merges.data(), lay.n_merges * sizeof(MergeItem));
   if (lay.n_scratch) {
     std::memcpy(host + lay.off_src, pl.src.data(), lay.n_scratch * sizeof(int32_t));

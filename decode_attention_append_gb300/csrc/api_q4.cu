@@ -303,7 +303,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     a.kv_exp = kv_exp;
     a.page_indices = page_indices;
     a.units = reinterpret_cast<const Q4Unit*>(ws + lay.off_units);
-    a.seg_begin = reinterpret_cast<const int32_t*>(ws + lay.off_segs);
+    a.ranges = reinterpret_cast<const Q4Range*>(ws + lay.off_ranges);
     a.Hq = dims.num_qo_heads;
     a.Hkv = dims.num_kv_heads;
     a.group = dims.num_qo_heads / dims.num_kv_heads;

@@ -110,7 +110,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   if (range >= a.n_ranges) return;
   const int kvh = (int)(id - (int64_t)range * a.Hkv);
   const int g = a.group;
-  const int seg_first = __ldg(a.seg_begin + range), seg_end = __ldg(a.seg_begin + range + 1);
+  const Q4Range rec = a.ranges[range];
   const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(__ldg(a.kv_exp + kvh)) : 1.f);
   const float f_v = a.kv_exp ? q4_pow2(__ldg(a.kv_exp + a.Hkv + kvh)) : 1.f;
   auto pages_of = [&](const Q4Unit& u) {
@@ -126,13 +126,13 @@ attention_q4_kernel(const AttentionQ4Args a) {
   __syncwarp();
 
   // The loads run ahead of the products by the ring's depth, over the end of a
-  // unit into the next ones: in_seg, in_j, in_n are the unit, page and page count
+  // unit into the next ones: in_unit, in_j, in_n are the unit, page and page count
   // of the next pair to load; lane l holds the id of page in_j - in_j % 32 + l.
-  int in_seg = seg_first - 1, in_j = 0, in_n = 0;
-  const int32_t* in_ids = nullptr;
+  int in_unit = rec.unit, in_j = 0, in_n = pages_of(rec.first);
+  const int32_t* in_ids = a.page_indices + rec.first.page_base + rec.first.tok_begin / kP;
   int32_t ids = 0;
   const uint8_t* head = a.pool + (int64_t)kvh * S::PAGE;
-  const int64_t page_stride = (int64_t)a.Hkv * S::PAGE;
+  const uint32_t page_stride = (uint32_t)a.Hkv * S::PAGE;
   auto load_ids = [&]() {
     ids = in_j + lane < in_n ? __ldg(in_ids + in_j + lane) : 0;
     if (ids < 0 || ids >= a.num_pages) {
@@ -142,21 +142,26 @@ attention_q4_kernel(const AttentionQ4Args a) {
   };
   auto load_next = [&](int st) {  // whole warp
     while (in_j >= in_n) {
-      if (in_seg + 1 >= seg_end) return;
-      const Q4Unit u = a.units[++in_seg];
+      if (in_unit + 1 >= rec.unit_end) return;
+      const Q4Unit u = a.units[++in_unit];
       in_n = pages_of(u);
       in_ids = a.page_indices + u.page_base + u.tok_begin / kP;
       in_j = 0;
       load_ids();
     }
-    // pages in_j and in_j + 1, by the lanes that hold their ids
-    const int k = lane - (in_j & 31);
-    if (k == 0) mbar_arrive_expect_tx(&full[st], in_j + 1 < in_n ? 2 * S::PAGE : S::PAGE);
-    if ((k & ~1) == 0 && in_j + k < in_n)
-      bulk_g2s(ring + st * S::STAGE + k * S::PAGE, head + ids * page_stride, S::PAGE, &full[st]);
+    const uint32_t id0 = (uint32_t)__shfl_sync(0xffffffffu, ids, in_j & 31);
+    const uint32_t id1 = (uint32_t)__shfl_sync(0xffffffffu, ids, (in_j + 1) & 31);
+    if (lane == 0) {
+      const bool two = in_j + 1 < in_n;
+      uint8_t* dst = ring + st * S::STAGE;
+      mbar_arrive_expect_tx(&full[st], two ? 2 * S::PAGE : S::PAGE);
+      bulk_g2s(dst, head + (uint64_t)id0 * page_stride, S::PAGE, &full[st]);
+      if (two) bulk_g2s(dst + S::PAGE, head + (uint64_t)id1 * page_stride, S::PAGE, &full[st]);
+    }
     in_j += 2;
     if ((in_j & 31) == 0) load_ids();
   };
+  load_ids();
 #pragma unroll 1
   for (int i = 0; i < S::PAIRS; ++i) load_next(i);
 
@@ -173,8 +178,8 @@ attention_q4_kernel(const AttentionQ4Args a) {
   int st = 0;
   uint32_t phase = 0;
 #pragma unroll 1
-  for (int seg = seg_first; seg < seg_end; ++seg) {
-  const Q4Unit u = a.units[seg];
+  for (int unit = rec.unit; unit < rec.unit_end; ++unit) {
+  const Q4Unit u = unit == rec.unit ? rec.first : a.units[unit];
   const int rows = u.n_tok * g;
   const int n_pages = pages_of(u);
 
@@ -485,7 +490,7 @@ cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], cudaS
     if (n_ranges[i] == 0) continue;
     e = i == 0 ? launch_t<D, 1>(a, n_ranges[i], stream)
                : (i == 1 ? launch_t<D, 2>(a, n_ranges[i], stream) : launch_t<D, 4>(a, n_ranges[i], stream));
-    a.seg_begin += n_ranges[i];
+    a.ranges += n_ranges[i];
   }
   return e;
 }

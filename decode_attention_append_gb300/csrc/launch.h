@@ -205,7 +205,7 @@ struct AttentionQ4Args {
   const int32_t* kv_exp;   // [2][Hkv] or null
   const int32_t* page_indices;
   const Q4Unit* units;
-  const int32_t* seg_begin;  // range i: units [seg_begin[i], seg_begin[i + 1])
+  const Q4Range* ranges;
   int n_ranges;            // set by the launch of each class
   int Hq, Hkv, group, head_dim;
   int64_t num_pages;

@@ -3,6 +3,7 @@
 #pragma once
 #include <cstddef>
 #include <cstdint>
+#include <cuda_runtime.h>
 
 namespace daa {
 
@@ -22,7 +23,7 @@ struct DecodeUnit {
 // query heads of a kv head of its n_tok tokens over keys [tok_begin, tok_end).
 // A warp takes a range of consecutive units, for one kv head.  Splits are page
 // aligned.
-struct Q4Unit {
+struct __align__(16) Q4Unit {
   int32_t q_row;        // row of the first of the tokens
   int32_t n_tok;
   int32_t pos0;         // its position
@@ -33,6 +34,13 @@ struct Q4Unit {
   int32_t part;         // partial slot of the first token, or -1: write out / lse_out
   int32_t part_stride;  // token t writes slot part + t * part_stride
   int32_t pad0, pad1, pad2;
+};
+// What one warp takes: units [unit, unit_end), and a copy of the first (one load
+// less before its pages can be asked for).
+struct __align__(16) Q4Range {
+  Q4Unit first;
+  int32_t unit, unit_end;
+  int32_t pad0, pad1;
 };
 // Units come in classes by the query rows (tokens x heads) they hold, each its
 // own ranges and launch: up to 8, 16, 32.
@@ -84,7 +92,7 @@ struct PrefillTile {
 // plan under 64 KB is copied inline with the launches.
 
 static_assert(sizeof(DecodeUnit) == 32, "DecodeUnit layout");
-static_assert(sizeof(Q4Unit) == 48, "Q4Unit layout");
+static_assert(sizeof(Q4Unit) == 48 && sizeof(Q4Range) == 64, "Q4Unit, Q4Range layout");
 static_assert(sizeof(MergeItem) == 16, "MergeItem layout");
 constexpr int32_t kTileRequest = 0;
 constexpr int32_t kTilePrefixGroup = 1;

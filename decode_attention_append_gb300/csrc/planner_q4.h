@@ -34,15 +34,15 @@ struct Q4Layout {
   int n_ranges[kQ4Classes] = {0, 0, 0};
   int n_units = 0, n_merges = 0, n_parts = 0, n_scratch = 0;
   PlanLayout sub;
-  size_t off_units, off_segs, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
+  size_t off_units, off_ranges, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
       off_pool, total;
   int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2]; }
   void finish(const daa_dims& d) {
     size_t off = 0;
     off_units = off;
     off = plan_align_up(off + (size_t)n_units * sizeof(Q4Unit));
-    off_segs = off;
-    off = plan_align_up(off + (size_t)(ranges() + 1) * sizeof(int32_t));
+    off_ranges = off;
+    off = plan_align_up(off + (size_t)ranges() * sizeof(Q4Range));
     off_merges = off;
     off = plan_align_up(off + (size_t)n_merges * sizeof(MergeItem));
     off_src = off;
@@ -70,7 +70,7 @@ struct Q4Plan {
   Vec<DecodeUnit> sub_units;
   Vec<MergeItem> sub_merges;
   Vec<PrefillTile> sub_tiles;
-  std::vector<int32_t> seg_begin;              // [ranges + 1]
+  std::vector<int32_t> seg_begin;              // [ranges + 1], first unit of each
   std::vector<int32_t> src;                    // scratch page -> index into page_indices
   std::vector<int32_t> req, sub_qo, sub_kv, sub_last;  // the bf16 requests' table
   Q4Layout lay;
@@ -136,29 +136,38 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     for (const Stream& s : ss) pages += s.pages;
     int64_t n_ranges = (int64_t)sms * q4_warps_per_sm(cls) / d.num_kv_heads;
     n_ranges = std::max<int64_t>(1, std::min<int64_t>(n_ranges, pages / kQ4MinPages));
-    const int64_t cost = pages + kQ4UnitPages * ((int64_t)ss.size() + n_ranges - 1);
-    const int64_t each = (cost + n_ranges - 1) / n_ranges;
     const int first_range = (int)pl.seg_begin.size() - 1;
-    int64_t room = each;  // of the open range
+    int64_t left_pages = pages;  // not yet in a unit
+    int64_t left_streams = (int64_t)ss.size();
+    // cost of the next range: what is left over the ranges left (each but the last
+    // may cut a stream, which costs a unit more)
+    auto share = [&] {
+      const int64_t left = first_range + n_ranges - (int64_t)(pl.seg_begin.size() - 1);
+      return (left_pages + kQ4UnitPages * (left_streams + left - 1) + left - 1) / left;
+    };
+    int64_t room = share();  // of the open range
     for (Stream& s : ss) {
       s.unit0 = (int)pl.units.size();
       for (int at = 0; at < s.pages;) {
         const int left = s.pages - at;
         const bool last_range = (int)pl.seg_begin.size() - first_range == (int)n_ranges;
-        if (!last_range && room < std::min<int64_t>(left, kQ4MinPages / 2) + kQ4UnitPages) {
+        if (!last_range && room < std::min<int64_t>(left, kQ4MinPages / 2) + kQ4UnitPages &&
+            (int)pl.units.size() > pl.seg_begin.back()) {
           pl.seg_begin.push_back((int32_t)pl.units.size());
-          room = each;
+          room = share();
           continue;
         }
-        int n = last_range ? left : (int)std::min<int64_t>(left, room - kQ4UnitPages);
+        int n = last_range ? left : (int)std::max<int64_t>(1, std::min<int64_t>(left, room - kQ4UnitPages));
         if (left - n < kQ4MinPages / 2) n = left;  // no small rest
         Q4Unit u{};
         u.tok_begin = at * P;
         u.tok_end = (at + n) * P;
         if (!pl.units.push_back(u)) return DAA_ERR_WORKSPACE;
         room -= n + kQ4UnitPages;
+        left_pages -= n;
         at += n;
       }
+      --left_streams;
       s.n_units = (int)pl.units.size() - s.unit0;
     }
     pl.seg_begin.push_back((int32_t)pl.units.size());
@@ -225,7 +234,9 @@ void plan_stage_q4(const Q4Plan<Vec>& pl, uint8_t* host) {
   std::memset(host, 0, lay.plan_bytes);
   if (lay.n_units) {
     std::memcpy(host + lay.off_units, pl.units.data(), lay.n_units * sizeof(Q4Unit));
-    std::memcpy(host + lay.off_segs, pl.seg_begin.data(), pl.seg_begin.size() * sizeof(int32_t));
+    Q4Range* ranges = reinterpret_cast<Q4Range*>(host + lay.off_ranges);
+    for (size_t i = 0; i + 1 < pl.seg_begin.size(); ++i)
+      ranges[i] = Q4Range{pl.units.data()[pl.seg_begin[i]], pl.seg_begin[i], pl.seg_begin[i + 1], 0, 0};
   }
   if (lay.n_merges) std::memcpy(host + lay.off_merges, pl.merges.data(), lay.n_merges * sizeof(MergeItem));
   if (lay.n_scratch) {

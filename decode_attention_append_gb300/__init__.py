@@ -31,6 +31,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -93,6 +94,8 @@ def library_path() -> str:
 def load_library():
     """Load libdaa.so (built by ``build.build()``); raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -207,17 +210,42 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _on(t: torch.Tensor, name: str, device) -> torch.Tensor:
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t
+def _addr(t, name: str, dtype, dev: int) -> int:
+    """The address of a contiguous tensor of `dtype` on CUDA device `dev`.  A few
+    attribute reads: these checks are most of what a small call costs the host."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous {str(dtype).removeprefix('torch.')} CUDA tensor")
+    raise ValueError(f"{name} must be on cuda:{dev}")
 
 
-def _device_of(device):
-    """Make a tensor's device current for a call (nothing to do when it is)."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call(fn, what, dev: int, stream, *args):
+    """fn(*args, stream) with device `dev` current; raises on an error status."""
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    else:
+        stream = int(stream)
+    if _current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != DAA_OK:
+        raise DaaError(st, what)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
 
 
 def _use_stream(stream):
@@ -784,19 +812,20 @@ class PagePool:
         return self
 
     def _init(self, seq_len, held, block_table, free_pages, counters):
-        for n, t in (("seq_len", seq_len), ("held", held), ("block_table", block_table),
-                     ("free_pages", free_pages), ("counters", counters)):
-            _dev_i32(t, n)
-            if t.device != seq_len.device:
-                raise ValueError(f"{n} is on another device than seq_len")
+        tensors = (("seq_len", seq_len), ("held", held), ("block_table", block_table),
+                   ("free_pages", free_pages), ("counters", counters))
+        self.dev = seq_len.get_device() if isinstance(seq_len, torch.Tensor) else -1
+        if self.dev < 0:
+            raise TypeError("seq_len must be a contiguous int32 CUDA tensor")
+        ptrs = [_addr(t, n, torch.int32, self.dev) for n, t in tensors]
         if seq_len.dim() != 1 or held.shape != seq_len.shape or block_table.dim() != 2 or \
                 block_table.shape[0] != seq_len.shape[0] or free_pages.dim() != 1 or counters.shape != (2,):
             raise ValueError("a pool has seq_len [slots], held [slots], block_table [slots, max_pages], "
                              "free_pages [num_pages] and counters [2]")
         self.seq_len, self.held, self.block_table = seq_len, held, block_table
         self.free_pages, self.counters, self.device = free_pages, counters, seq_len.device
-        self._pool = _Pool(_ptr(seq_len), _ptr(held), _ptr(block_table), _ptr(free_pages), _ptr(counters),
-                           seq_len.shape[0], block_table.shape[1], free_pages.shape[0], self.PAGE_SIZE)
+        self._pool = _Pool(*ptrs, seq_len.shape[0], block_table.shape[1], free_pages.shape[0], self.PAGE_SIZE)
+        self._pool_ref = ctypes.byref(self._pool)
 
     def _mirror(self):
         if self.h_len is None:
@@ -811,31 +840,22 @@ class PagePool:
         kernel refuses gives an empty step and sets the device error word.  The
         host copies of the lengths are not updated: a pool is driven either by
         ``build`` or by ``step``."""
-        lib = load_library()
-        for n, t in (("slots", slots), ("new_len", new_len), ("qo_indptr", qo_indptr),
-                     ("kv_indptr", kv_indptr), ("page_indices", page_indices),
-                     ("last_page_len", last_page_len)):
-            _on(_dev_i32(t, n), n, self.device)
+        i32, dev = torch.int32, self.dev
+        args = (_addr(slots, "slots", i32, dev), _addr(new_len, "new_len", i32, dev),
+                _addr(qo_indptr, "qo_indptr", i32, dev), _addr(kv_indptr, "kv_indptr", i32, dev),
+                _addr(page_indices, "page_indices", i32, dev), _addr(last_page_len, "last_page_len", i32, dev))
         batch = slots.numel()
         if new_len.numel() != batch or qo_indptr.numel() != batch + 1 or kv_indptr.numel() != batch + 1 \
                 or last_page_len.numel() != batch:
             raise ValueError("slots, new_len and last_page_len have one entry per request, "
                              "qo_indptr and kv_indptr one more")
-        rows = None
-        for n, t, dt in (("slot_map", slot_map, torch.int64), ("positions", positions, torch.int32)):
-            if t is not None:
-                if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dt and t.is_contiguous()):
-                    raise TypeError(f"{n} must be a contiguous {dt} CUDA tensor")
-                _on(t, n, self.device)
-                rows = t.numel() if rows is None else min(rows, t.numel())
-        if rows is None:
-            rows = 2 ** 31 - 1  # nothing is written per row
-        with _device_of(self.device):
-            _check(lib.daa_step_table(ctypes.byref(self._pool), _ptr(slots), _ptr(new_len), batch,
-                                      int(bool(advance)), _ptr(qo_indptr), _ptr(kv_indptr),
-                                      _ptr(page_indices), page_indices.numel(), _ptr(last_page_len),
-                                      _ptr(slot_map), _ptr(positions), rows, _stream(stream)),
-                   "step_table")
+        rows, p_map, p_pos = 2 ** 31 - 1, None, None  # without either nothing is written per row
+        if slot_map is not None:
+            p_map, rows = _addr(slot_map, "slot_map", torch.int64, dev), slot_map.numel()
+        if positions is not None:
+            p_pos, rows = _addr(positions, "positions", i32, dev), min(rows, positions.numel())
+        _call(load_library().daa_step_table, "step_table", dev, stream, self._pool_ref, args[0], args[1], batch,
+              1 if advance else 0, args[2], args[3], args[4], page_indices.numel(), args[5], p_map, p_pos, rows)
 
     def step(self, slots, new_lens, advance=True, stream=None) -> PageTable:
         """The page table of a step that brings ``new_lens[i]`` tokens to slot
@@ -859,7 +879,7 @@ class PagePool:
             raise DaaError(-2, "PagePool.step: the step's rows and pages must fit 32 bits")
         hl = np.where(pages > 0, kv - (pages - 1) * self.PAGE_SIZE, 0)
         i32 = dict(dtype=torch.int32, device=self.device)
-        with _device_of(self.device), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream):
             up = torch.from_numpy(np.stack([sl, nl]).astype(np.int32)).to(self.device)
             n = len(sl)
             t = PageTable(torch.empty(n + 1, **i32), torch.empty(n + 1, **i32),
@@ -883,7 +903,7 @@ class PagePool:
         self._check_slots(sl)
         if len(ln) != len(sl) or (ln < 0).any() or (-(-ln // self.PAGE_SIZE) > self.h_held[sl]).any():
             raise ValueError("lens must have one entry per slot, within the pages the slot holds")
-        with _device_of(self.device), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream):
             at = torch.from_numpy(sl).to(self.device)
             self.seq_len.index_copy_(0, at, torch.from_numpy(ln.astype(np.int32)).to(self.device))
         self.h_len[sl] = ln
@@ -893,11 +913,10 @@ class PagePool:
         self._mirror()
         sl = np.asarray(slots, np.int64).reshape(-1)
         self._check_slots(sl)
-        lib = load_library()
-        with _device_of(self.device), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream):
             dev = torch.from_numpy(sl.astype(np.int32)).to(self.device)
-            _check(lib.daa_release_pages(ctypes.byref(self._pool), _ptr(dev), len(sl), _stream(stream)),
-                   "release_pages")
+            _call(load_library().daa_release_pages, "release_pages", self.dev, stream, self._pool_ref,
+                  dev.data_ptr(), len(sl))
         self.h_free += int(self.h_held[sl].sum())
         self.h_len[sl] = self.h_held[sl] = 0
 
@@ -911,18 +930,27 @@ def new_q4_pool(num_pages, num_kv_heads, head_dim, device="cuda") -> torch.Tenso
     return torch.zeros(num_pages, num_kv_heads, 2, 9 * head_dim, dtype=torch.uint8, device=device)
 
 
-def _q4_dims(kv_pages, num_qo_heads, kv_exp) -> _Dims:
-    if not (isinstance(kv_pages, torch.Tensor) and kv_pages.is_cuda and kv_pages.dtype == torch.uint8
-            and kv_pages.is_contiguous()):
-        raise TypeError("kv_pages must be a contiguous uint8 CUDA tensor")
-    if kv_pages.dim() != 4 or kv_pages.shape[2] != 2 or kv_pages.shape[3] % 9 != 0:
+@functools.lru_cache(maxsize=64)
+def _q4_dims_of(shape, num_qo_heads) -> _Dims:
+    if len(shape) != 4 or shape[2] != 2 or shape[3] % 9 != 0:
         raise ValueError("kv_pages must be [num_pages, Hkv, 2, 9 * head_dim]")
-    n, hkv, _, b = kv_pages.shape
-    if kv_exp is not None:
-        _on(_dev_i32(kv_exp, "kv_exp"), "kv_exp", kv_pages.device)
-        if tuple(kv_exp.shape) != (2, hkv):
-            raise ValueError("kv_exp must be [2, Hkv]")
+    n, hkv, _, b = shape
     return _Dims(hkv if num_qo_heads is None else num_qo_heads, hkv, b // 9, 16, n)
+
+
+def _q4_pool(kv_pages, kv_exp, num_qo_heads=None):
+    """(device index, pool address, exponents' address or None, dims) of a 4-bit pool."""
+    dev = kv_pages.get_device() if isinstance(kv_pages, torch.Tensor) else -1
+    pool = _addr(kv_pages, "kv_pages", torch.uint8, dev)
+    if dev < 0:
+        raise TypeError("kv_pages must be a contiguous uint8 CUDA tensor")
+    dims = _q4_dims_of(kv_pages.shape, num_qo_heads)
+    if kv_exp is None:
+        return dev, pool, None, dims
+    exp = _addr(kv_exp, "kv_exp", torch.int32, dev)
+    if kv_exp.shape != (2, dims.num_kv_heads):
+        raise ValueError("kv_exp must be [2, Hkv]")
+    return dev, pool, exp, dims
 
 
 def kv_append_q4(k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len,
@@ -930,42 +958,31 @@ def kv_append_q4(k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr,
     """``kv_append`` into a 4-bit pool: the new tokens' K/V are quantised (e2m1
     with an e4m3 scale for every 16 dims, and the head's exponent ``kv_exp``
     [2, Hkv]) and written into their page slots."""
-    lib = load_library()
-    dims = _q4_dims(kv_pages, None, kv_exp)
-    dev = kv_pages.device
-    for n, t in (("k_new", k_new), ("v_new", v_new)):
-        _on(_dev_bf16(t, n), n, dev)
-    for n, t in (("append_indptr", append_indptr), ("page_indices", page_indices),
-                 ("kv_indptr", kv_indptr), ("last_page_len", last_page_len)):
-        _on(_dev_i32(t, n), n, dev)
-    if k_new.dim() != 3 or tuple(k_new.shape[1:]) != (dims.num_kv_heads, dims.head_dim) or \
-            v_new.shape != k_new.shape:
+    dev, pool, exp, dims = _q4_pool(kv_pages, kv_exp)
+    i32, bf16 = torch.int32, torch.bfloat16
+    k, v = _addr(k_new, "k_new", bf16, dev), _addr(v_new, "v_new", bf16, dev)
+    table = (_addr(append_indptr, "append_indptr", i32, dev), _addr(page_indices, "page_indices", i32, dev),
+             _addr(kv_indptr, "kv_indptr", i32, dev), _addr(last_page_len, "last_page_len", i32, dev))
+    rows = k_new.shape[0] if k_new.dim() == 3 else 0
+    if k_new.shape != (rows, dims.num_kv_heads, dims.head_dim) or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [nnz_new, Hkv, head_dim]")
     batch = append_indptr.numel() - 1
     if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
         raise ValueError("append_indptr and kv_indptr have batch + 1 entries, last_page_len batch")
-    with _device_of(dev):
-        _check(lib.daa_kv_append_q4(_ptr(k_new), _ptr(v_new), _ptr(kv_pages), _ptr(kv_exp),
-                                    _ptr(append_indptr), _ptr(page_indices), _ptr(kv_indptr),
-                                    _ptr(last_page_len), batch, k_new.shape[0], dims,
-                                    _stream(stream)), "kv_append_q4")
+    _call(load_library().daa_kv_append_q4, "kv_append_q4", dev, stream, k, v, pool, exp, *table, batch, rows, dims)
 
 
 def kv_dequant_q4(kv_pages, page_ids, kv_exp=None, out=None, stream=None):
     """Pages of a 4-bit pool as bf16 pages [n, 2, Hkv, 16, head_dim], exactly."""
-    lib = load_library()
-    dims = _q4_dims(kv_pages, None, kv_exp)
-    dev = kv_pages.device
-    _on(_dev_i32(page_ids, "page_ids"), "page_ids", dev)
-    shape = (page_ids.numel(), 2, dims.num_kv_heads, dims.page_size, dims.head_dim)
+    dev, pool, exp, dims = _q4_pool(kv_pages, kv_exp)
+    ids, n = _addr(page_ids, "page_ids", torch.int32, dev), page_ids.numel()
+    shape = (n, 2, dims.num_kv_heads, dims.page_size, dims.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    _on(_dev_bf16(out, "out"), "out", dev)
-    if tuple(out.shape) != shape:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+    o = _addr(out, "out", torch.bfloat16, dev)
+    if out.shape != shape:
         raise ValueError("out must be [n_pages, 2, Hkv, 16, head_dim]")
-    with _device_of(dev):
-        _check(lib.daa_kv_dequant_q4(_ptr(kv_pages), _ptr(kv_exp), _ptr(page_ids), page_ids.numel(),
-                                     _ptr(out), dims, _stream(stream)), "kv_dequant_q4")
+    _call(load_library().daa_kv_dequant_q4, "kv_dequant_q4", dev, stream, pool, exp, ids, n, o, dims)
     return out
 
 
@@ -992,27 +1009,25 @@ class BatchAttentionQ4:
                  sm_scale=None, kv_exp=None):
         self.t = table
         self.kv_pages, self.kv_exp = kv_pages, kv_exp
-        self.dims = _q4_dims(kv_pages, num_qo_heads, kv_exp)
+        self.dev, _, _, self.dims = _q4_pool(kv_pages, kv_exp, num_qo_heads)
         for n in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len"):
-            _on(_dev_i32(getattr(table, n), n), n, kv_pages.device)
+            _addr(getattr(table, n), n, torch.int32, self.dev)
         self.causal = int(bool(causal))
         self.sm_scale = float(sm_scale if sm_scale is not None else 1.0 / float(self.dims.head_dim) ** 0.5)
         d = self.dims
         need = batch_attention_q4_workspace_size(table.h_qo_indptr, table.h_kv_indptr,
                                                  table.h_last_page_len, d.num_qo_heads, d.num_kv_heads,
                                                  d.head_dim, d.page_size, d.num_pages)
-        self.rows = int(table.h_qo_indptr[-1])
+        self.shape = (int(table.h_qo_indptr[-1]), d.num_qo_heads, d.head_dim)
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=kv_pages.device)
         self.info = None
 
     def plan(self, stream=None):
         """Upload the batch's plan; later runs (one per layer) reuse it."""
         t, info = self.t, PlanInfo()
-        with _device_of(self.kv_pages.device):
-            _check(load_library().daa_batch_attention_q4_plan(
-                _ptr(t.h_qo_indptr), _ptr(t.h_kv_indptr), _ptr(t.h_last_page_len),
-                len(t.h_qo_indptr) - 1, self.dims, _ptr(self.workspace), self.workspace.numel(),
-                ctypes.byref(info), _stream(stream)), "batch_attention_q4_plan")
+        _call(load_library().daa_batch_attention_q4_plan, "batch_attention_q4_plan", self.dev, stream,
+              _ptr(t.h_qo_indptr), _ptr(t.h_kv_indptr), _ptr(t.h_last_page_len), len(t.h_qo_indptr) - 1,
+              self.dims, self.workspace.data_ptr(), self.workspace.numel(), ctypes.byref(info))
         self.info = info
         return info
 
@@ -1023,29 +1038,26 @@ class BatchAttentionQ4:
 
     def run(self, q, out=None, lse=None, stream=None):
         """Attention of q [nnz_qo, Hq, head_dim]; returns ``out`` and fills ``lse``."""
-        d, dev = self.dims, self.kv_pages.device
-        _on(_dev_bf16(q, "q"), "q", dev)
-        if tuple(q.shape) != (self.rows, d.num_qo_heads, d.head_dim):
+        d, dev, bf16 = self.dims, self.dev, torch.bfloat16
+        pq = _addr(q, "q", bf16, dev)
+        if q.shape != self.shape:
             raise ValueError("q must be [nnz_qo, Hq, head_dim] of the planned table")
         if out is None:
             out = torch.empty_like(q)
-        _on(_dev_bf16(out, "out"), "out", dev)
-        if out.shape != q.shape:
+        po = _addr(out, "out", bf16, dev)
+        if out.shape != self.shape:
             raise ValueError("out must have the shape of q")
+        pl = None
         if lse is not None:
-            if not (isinstance(lse, torch.Tensor) and lse.is_cuda and lse.dtype == torch.float32
-                    and lse.is_contiguous()):
-                raise TypeError("lse must be a contiguous fp32 CUDA tensor")
-            _on(lse, "lse", dev)
-            if tuple(lse.shape) != (self.rows, d.num_qo_heads):
+            pl = _addr(lse, "lse", torch.float32, dev)
+            if lse.shape != self.shape[:2]:
                 raise ValueError("lse must be [nnz_qo, Hq]")
         if self.info is None:
             self.plan(stream)
-        with _device_of(dev):
-            _check(load_library().daa_batch_attention_q4_run(
-                _ptr(q), _ptr(self.kv_pages), _ptr(self.kv_exp), _ptr(self.t.page_indices),
-                ctypes.byref(self.info), self.causal, self.sm_scale, _ptr(out), _ptr(lse),
-                _ptr(self.workspace), self.workspace.numel(), d, _stream(stream)), "batch_attention_q4")
+        exp = None if self.kv_exp is None else self.kv_exp.data_ptr()
+        _call(load_library().daa_batch_attention_q4_run, "batch_attention_q4", dev, stream, pq,
+              self.kv_pages.data_ptr(), exp, self.t.page_indices.data_ptr(), self.info, self.causal, self.sm_scale,
+              po, pl, self.workspace.data_ptr(), self.workspace.numel(), d)
         return out
 
     def step(self, k_new, v_new, q, out=None, lse=None, stream=None):

@@ -204,6 +204,8 @@ int fuse_min_qo_for(const daa_dims& d) {
 
 int device_sms() { return num_sms(); }
 
+bool tracer_on() { return tracing(); }
+
 cudaError_t traced_launch(int32_t kernel_id, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx) {
   return traced(kernel_id, s, [&] { return launch(ctx); });
 }

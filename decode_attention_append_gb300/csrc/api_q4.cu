@@ -316,7 +316,12 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     a.part_o = reinterpret_cast<float*>(ws + lay.off_part_o);
     a.part_lse = reinterpret_cast<float*>(ws + lay.off_part_lse);
     a.err = device_error_word();
-    if (traced(kKernelAttentionQ4, s, [&] { return launch_attention_q4(a, lay.n_ranges, s); }) != cudaSuccess)
+    // beside the bf16 requests' kernels (none of which it reads), and its merge
+    // behind it; each kernel alone while the tracer times them
+    const bool programmatic = !tracer_on();
+    if (traced(kKernelAttentionQ4, s, [&] {
+          return launch_attention_q4(a, lay.n_ranges, programmatic && lay.n_scratch > 0, s);
+        }) != cudaSuccess)
       return DAA_ERR_CUDA;
     if (lay.n_merges > 0) {
       MergeArgs m{};
@@ -328,7 +333,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
       m.part_lse = a.part_lse;
       m.out = a.out;
       m.lse_out = lse_out;
-      if (traced(kKernelMerge, s, [&] { return launch_merge(m, s, /*programmatic=*/false); }) != cudaSuccess)
+      if (traced(kKernelMerge, s, [&] { return launch_merge_q4(m, lay.n_parts, programmatic, s); }) != cudaSuccess)
         return DAA_ERR_CUDA;
     }
   }

@@ -104,6 +104,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * S::PAIRS;
   uint8_t* ring = smem + warp * (S::PAIRS * S::STAGE);
 
+  grid_dep_launch();  // the next kernel of the call may start its CTAs
   // the heads of a range in warps side by side: their slices of a page are, too
   const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
   const int range = (int)(id / a.Hkv);
@@ -118,7 +119,6 @@ attention_q4_kernel(const AttentionQ4Args a) {
     return max(0, (key_end + kP - 1) / kP - u.tok_begin / kP);
   };
 
-  grid_dep_launch();  // the merge may launch; it waits for this grid
   if (lane == 0) {
     for (int i = 0; i < S::PAIRS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
@@ -469,27 +469,115 @@ attention_q4_kernel(const AttentionQ4Args a) {
       }
     }
   }
+  // This grid reads nothing of the one before it in the call; its completion
+  // still has to imply that one's, for what follows on the stream.
+  if (blockIdx.x == 0) grid_dep_wait();
+}
+
+// softmax_merge of the parts of a (token, query head): M = max lse, weights
+// 2^(lse - M), their sum and the weighted sum of the parts (lse in the log2
+// domain).  Bound: latency (a load of lse, then one of the parts for every
+// kMergeLoads of them).  W warps share a row: one where rows have few parts, so
+// that a wave of CTAs holds as many rows as it can; four where they have many
+// (GB300, decode of 128 requests, 12 heads, 15 parts on average and 47 at most:
+// 16 us with one, 11 with four; 160 tokens, 32 heads, 6 parts: 7 us and 12).
+constexpr int kMergeWarps = 4;
+constexpr int kMergeLoads = 4;
+constexpr int kMergeWideParts = 10;  // parts of a token, on average, from which four warps share it
+
+template <int D, int W>
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeArgs a) {
+  constexpr int EPL = D / 32;  // dims of a lane
+  __shared__ float s_acc[W > 1 ? W : 1][W > 1 ? D : 1];
+  __shared__ float s_sum[W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const MergeItem it = a.items[blockIdx.x];
+  const int hq = blockIdx.y * (kMergeWarps / W) + warp / W;
+  const int share = warp % W;
+  if (hq >= a.Hq) return;  // W == 1 only
+  const float* lse = a.part_lse + (int64_t)it.part_begin * a.Hq + hq;
+  const float* part = a.part_o + ((int64_t)it.part_begin * a.Hq + hq) * D + lane * EPL;
+  const int64_t stride = (int64_t)a.Hq * D;
+  grid_dep_wait();  // the parts come from the kernel launched before
+  float M = -INFINITY;
+  for (int p = lane; p < it.n_parts; p += 32) M = fmaxf(M, lse[(int64_t)p * a.Hq]);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
+  float acc[EPL], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
+  for (int p0 = share; p0 < it.n_parts; p0 += W * kMergeLoads) {
+    float w[kMergeLoads], v[kMergeLoads][EPL];
+#pragma unroll
+    for (int i = 0; i < kMergeLoads; ++i) {
+      const int p = p0 + i * W;
+      w[i] = p < it.n_parts ? lse[(int64_t)p * a.Hq] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = 0.f;
+      if (p < it.n_parts) {
+        if constexpr (EPL == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(part + p * stride);
+          v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(part + p * stride);
+          v[i][0] = x.x; v[i][1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeLoads; ++i) {
+      const float x = ex2_approx(w[i] - M);
+      sum += x;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x, v[i][e], acc[e]);
+    }
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) s_acc[warp][lane * EPL + e] = acc[e];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      sum += s_sum[w];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] += s_acc[w][lane * EPL + e];
+    }
+  }
+  const float inv = 1.f / sum;
+  const int64_t row = (int64_t)it.q_row * a.Hq + hq;
+  uint16_t* dst = a.out + row * D + lane * EPL;
+  if constexpr (EPL == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0 && a.lse_out) a.lse_out[row] = (M + __log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int D, int NT>
-cudaError_t launch_t(AttentionQ4Args a, int n_ranges, cudaStream_t stream) {
+cudaError_t launch_t(AttentionQ4Args a, int n_ranges, bool programmatic, cudaStream_t stream) {
   using S = Shape<D, NT>;
   a.n_ranges = n_ranges;
   auto kern = attention_q4_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t warps = (int64_t)a.Hkv * n_ranges;
-  kern<<<(unsigned)((warps + kWarps - 1) / kWarps), 32 * kWarps, S::SMEM, stream>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(32 * kWarps), S::SMEM,
+                       stream, programmatic, a);
 }
 
 template <int D>
-cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], cudaStream_t stream) {
+cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], bool programmatic,
+                     cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < kQ4Classes && e == cudaSuccess; ++i) {
     if (n_ranges[i] == 0) continue;
-    e = i == 0 ? launch_t<D, 1>(a, n_ranges[i], stream)
-               : (i == 1 ? launch_t<D, 2>(a, n_ranges[i], stream) : launch_t<D, 4>(a, n_ranges[i], stream));
+    e = i == 0 ? launch_t<D, 1>(a, n_ranges[i], programmatic, stream)
+               : (i == 1 ? launch_t<D, 2>(a, n_ranges[i], programmatic, stream)
+                         : launch_t<D, 4>(a, n_ranges[i], programmatic, stream));
+    programmatic = true;
     a.ranges += n_ranges[i];
   }
   return e;
@@ -498,8 +586,18 @@ cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], cudaS
 }  // namespace
 
 cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
-                                cudaStream_t stream) {
-  return a.head_dim == 128 ? launch_d<128>(a, n_ranges, stream) : launch_d<64>(a, n_ranges, stream);
+                                bool programmatic, cudaStream_t stream) {
+  return a.head_dim == 128 ? launch_d<128>(a, n_ranges, programmatic, stream)
+                           : launch_d<64>(a, n_ranges, programmatic, stream);
+}
+
+cudaError_t launch_merge_q4(const MergeArgs& a, int n_parts, bool programmatic, cudaStream_t stream) {
+  if (a.n_items <= 0) return cudaSuccess;
+  const bool wide = n_parts >= kMergeWideParts * a.n_items;
+  const dim3 grid(a.n_items, wide ? a.Hq : (a.Hq + kMergeWarps - 1) / kMergeWarps), block(32 * kMergeWarps);
+  void (*kern)(MergeArgs) = a.head_dim == 128 ? (wide ? merge_q4_kernel<128, 4> : merge_q4_kernel<128, 1>)
+                                              : (wide ? merge_q4_kernel<64, 4> : merge_q4_kernel<64, 1>);
+  return launch_kernel(kern, grid, block, 0, stream, programmatic, a);
 }
 
 }  // namespace daa

@@ -217,11 +217,15 @@ struct AttentionQ4Args {
   float* part_lse;         // [n_parts][Hq] (log2 domain)
   int* err;
 };
+// programmatic: the kernel before on the stream is of the same call and is not read.
 cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
-                                cudaStream_t stream);
+                                bool programmatic, cudaStream_t stream);
+// softmax_merge of its n_parts parts (items without a prefix part).
+cudaError_t launch_merge_q4(const MergeArgs& a, int n_parts, bool programmatic, cudaStream_t stream);
 
 // SMs of the current device, and a launch between the tracer's events (api.cu).
 int device_sms();
+bool tracer_on();
 cudaError_t traced_launch(int32_t kernel_id, cudaStream_t s, cudaError_t (*launch)(void*), void* ctx);
 // The kernels run in the order prefill, decode, softmax_merge; each after the
 // first is a programmatic dependent launch, and so is the first when

@@ -574,9 +574,10 @@ cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], bool 
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < kQ4Classes && e == cudaSuccess; ++i) {
     if (n_ranges[i] == 0) continue;
-    e = i == 0 ? launch_t<D, 1>(a, n_ranges[i], programmatic, stream)
-               : (i == 1 ? launch_t<D, 2>(a, n_ranges[i], programmatic, stream)
-                         : launch_t<D, 4>(a, n_ranges[i], programmatic, stream));
+    e = i == 0   ? launch_t<D, 1>(a, n_ranges[i], programmatic, stream)
+        : i == 1 ? launch_t<D, 2>(a, n_ranges[i], programmatic, stream)
+        : i == 2 ? launch_t<D, 3>(a, n_ranges[i], programmatic, stream)
+                 : launch_t<D, 4>(a, n_ranges[i], programmatic, stream);
     programmatic = true;
     a.ranges += n_ranges[i];
   }

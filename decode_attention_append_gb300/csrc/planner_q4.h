@@ -25,19 +25,19 @@ constexpr int kQ4UnitRows = 32;   // rows a unit holds at most
 constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages
 constexpr int kQ4MinPages = 4;    // pages of a range at least
 
-inline int q4_class(int rows) { return rows <= 8 ? 0 : (rows <= 16 ? 1 : 2); }
+inline int q4_class(int rows) { return (rows - 1) / 8; }
 // Warps of the class's kernel on an SM (its shared memory and registers).
-inline int q4_warps_per_sm(int cls) { return 4 * (4 - cls); }
+inline int q4_warps_per_sm(int cls) { return cls == 0 ? 16 : (cls == 1 ? 12 : 8); }
 
 // Sections of the workspace, all worked out from the counts and the layout of
 // the bf16 requests' plan.  The first plan_bytes are copied from the host.
 struct Q4Layout {
-  int n_ranges[kQ4Classes] = {0, 0, 0};
+  int n_ranges[kQ4Classes] = {};
   int n_units = 0, n_merges = 0, n_parts = 0, n_scratch = 0;
   PlanLayout sub;
   size_t off_units, off_ranges, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
       off_pool, total;
-  int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2]; }
+  int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2] + n_ranges[3]; }
   void finish(const daa_dims& d) {
     size_t off = 0;
     off_units = off;

@@ -162,7 +162,7 @@ daa_status daa_kv_append_q4(const void* k_new, const void* v_new, void* kv_pages
   return traced(kKernelAppendQ4, s, [&] {
            return launch_kv_append_q4(k_new, v_new, kv_pages, kv_exp, append_indptr, page_indices,
                                       kv_indptr, last_page_len, batch, nnz_new, dims.num_kv_heads,
-                                      dims.head_dim, dims.num_pages, device_error_word(), s);
+                                      dims.head_dim, dims.num_pages, device_sms(), device_error_word(), s);
          }) == cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;

@@ -11,9 +11,12 @@
 // Rounding y / s without a division per value: y has the 8 significant bits of
 // a bf16 and every midpoint of two e2m1 values times s has at most 7, so y / s
 // is either exactly a midpoint or at least 2^-9 (relative) away from one.
-// y * (1 / s) is off by at most 2^-23, so rounding it to 12 bits first (add half
-// of the 12th bit's step, cut the bits below) lands on the midpoint exactly when
-// y / s does, and the conversion's tie rule then applies to the exact quotient.
+// y * (1 / s) is off by at most 2^-23, so rounding it to fp16 (11 bits, a half
+// step of 2^-11 at most) lands on the midpoint exactly when y / s does, and the
+// conversion's tie rule then applies to the exact quotient.
+//
+// Bound: HBM (2 + 9/16 bytes a value); about four instructions a value (widen,
+// scale, the maximum taken on packed bits, two conversions a pair).
 #include "launch.h"
 #include "ptx.cuh"
 #include "q4.cuh"
@@ -22,9 +25,11 @@ namespace daa {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAppendU = 2;                     // blocks of 16 dims per thread in flight
-constexpr int kAppendSpan = kThreads * kAppendU;
-constexpr int kMaxRows = kAppendSpan / 4 + 2;   // rows a CTA touches (a row has >= 4 blocks)
+// Blocks of 16 dims per thread in flight: two for small appends (a CTA's chain of
+// loads is what they wait for, so they are cut fine), six once the CTAs fill the
+// GPU more than once.
+constexpr int kSmallU = 2, kLargeU = 6;
+constexpr int kMaxBatch = 1023;                 // requests whose indptr a CTA holds
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
@@ -34,42 +39,45 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
+// The largest |value| of 16 bf16 values as bits, taken two at a time: without a
+// sign bf16 values are ordered as their bits, and NaN is above infinity.
+__device__ __forceinline__ uint32_t max_abs_bits(const uint32_t (&w)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  return max(m & 0xFFFFu, m >> 16);
+}
+
 // One block of 16 bf16 values -> 8 code bytes and the scale byte.
 __device__ __forceinline__ uint2 quantise_block(const uint4& a, const uint4& b, float two_to_minus_e,
                                                 uint8_t& scale) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float x[16];
-  float amax = 0.f;
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t top = max_abs_bits(w);
+  if (top > 0x7F80u) {  // a NaN: they count as zeros
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = bf16lo_to_f32(w[i]);
-    x[2 * i + 1] = bf16hi_to_f32(w[i]);
-    amax = fmaxf(amax, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));  // fmaxf drops NaN
+    for (int i = 0; i < 8; ++i) {
+      if ((w[i] & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFF0000u;
+      if ((w[i] & 0x7FFF0000u) > 0x7F800000u) w[i] &= 0x0000FFFFu;
+    }
+    top = max_abs_bits(w);
   }
+  const float amax = __uint_as_float(top << 16);
   // clamp(max|y| / 6): a true division, so that its ties are ties
   const float s6 = fminf(fmaxf(__fdiv_rn(amax * two_to_minus_e, 6.f), 0.001953125f), 448.f);
   const uint16_t sb = f32x2_to_e4m3x2(s6, 0.f);
   const float r = __fdiv_rn(1.f, f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x) * two_to_minus_e;
   scale = (uint8_t)(sb & 0xFFu);
-  uint2 out;
-  float v[8];
+  uint32_t h[8];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float xi = x[8 * half + i];
-      const float y = (xi == xi) ? xi * r : 0.f;
-      v[i] = __uint_as_float((__float_as_uint(y) + 0x800u) & 0xFFFFF000u);
-    }
-    (half == 0 ? out.x : out.y) = f32x8_to_e2m1x8(v);
-  }
-  return out;
+  for (int i = 0; i < 8; ++i) h[i] = f32x2_to_f16x2(bf16lo_to_f32(w[i]) * r, bf16hi_to_f32(w[i]) * r);
+  const uint32_t lo[4] = {h[0], h[1], h[2], h[3]}, hi[4] = {h[4], h[5], h[6], h[7]};
+  return make_uint2(f16x8_to_e2m1x8(lo), f16x8_to_e2m1x8(hi));
 }
 
 // Flat blocks (row, head, block of 16 dims) of K (blockIdx.y 0) or V (1), cut
 // into equal contiguous ranges, one per CTA; the owner of each row a CTA
 // touches is found once by binary search.
-template <int D>
+template <int D, int kAppendU>
 __global__ void __launch_bounds__(kThreads)
 kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
                     uint8_t* __restrict__ pool, const int32_t* __restrict__ kv_exp,
@@ -78,8 +86,11 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
                     const int32_t* __restrict__ last_page_len, int batch, int nnz_new, int Hkv,
                     int64_t num_pages, int* err) {
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
+  constexpr int kAppendSpan = kThreads * kAppendU;
+  constexpr int kMaxRows = kAppendSpan / NB + 2;  // rows a CTA touches (a row has NB blocks or more)
   __shared__ int64_t s_page[kMaxRows];  // page * Hkv of the row, -1: not written
   __shared__ int s_slot[kMaxRows];
+  __shared__ int s_indptr[kMaxBatch + 1];
   const int kv = blockIdx.y;
   const int per_row = Hkv * NB;
   const int64_t total = (int64_t)nnz_new * per_row;
@@ -99,14 +110,22 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
       b[u] = ld_stream(src + 2 * i + 1);
     }
   }
+  // the search for a row's request is a chain of loads: in shared memory where the
+  // array fits, so that a small append waits for memory three times and not ten
+  const int32_t* indptr = append_indptr;
+  if (batch <= kMaxBatch) {
+    for (int t = threadIdx.x; t <= batch; t += kThreads) s_indptr[t] = __ldg(append_indptr + t);
+    __syncthreads();
+    indptr = s_indptr;
+  }
   for (int t = threadIdx.x; t < nrows; t += kThreads) {
     const int row = row0 + t;
-    int lo = 0, hi = batch - 1;  // largest r with append_indptr[r] <= row
+    int lo = 0, hi = batch - 1;  // largest r with indptr[r] <= row
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(append_indptr + mid) <= row) lo = mid; else hi = mid - 1;
+      if (indptr[mid] <= row) lo = mid; else hi = mid - 1;
     }
-    const int a0 = __ldg(append_indptr + lo), a1 = __ldg(append_indptr + lo + 1);
+    const int a0 = indptr[lo], a1 = indptr[lo + 1];
     const int p0 = __ldg(kv_indptr + lo), np = __ldg(kv_indptr + lo + 1) - p0;
     const int last_len = np > 0 ? __ldg(last_page_len + lo) : 0;
     const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * P + last_len : 0;
@@ -210,12 +229,15 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                                 const int32_t* kv_exp, const int32_t* append_indptr,
                                 const int32_t* page_indices, const int32_t* kv_indptr,
                                 const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
-                                int head_dim, int64_t num_pages, int* err, cudaStream_t stream) {
+                                int head_dim, int64_t num_pages, int sms, int* err, cudaStream_t stream) {
   if (nnz_new <= 0 || batch <= 0) return cudaSuccess;
   const int64_t total = (int64_t)nnz_new * Hkv * (head_dim / kQ4Block);
-  const int64_t grid = (total + kAppendSpan - 1) / kAppendSpan;
+  const bool large = total >= (int64_t)sms * 16 * kThreads * kSmallU;  // 16 CTAs an SM
+  const int span = kThreads * (large ? kLargeU : kSmallU);
+  const int64_t grid = (total + span - 1) / span;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  auto kern = head_dim == 128 ? kv_append_q4_kernel<128> : kv_append_q4_kernel<64>;
+  auto kern = head_dim == 128 ? (large ? kv_append_q4_kernel<128, kLargeU> : kv_append_q4_kernel<128, kSmallU>)
+                              : (large ? kv_append_q4_kernel<64, kLargeU> : kv_append_q4_kernel<64, kSmallU>);
   kern<<<dim3((unsigned)grid, 2), kThreads, 0, stream>>>(
       (const uint4*)k_new, (const uint4*)v_new, (uint8_t*)pool, kv_exp, append_indptr, page_indices,
       kv_indptr, last_page_len, batch, nnz_new, Hkv, num_pages, err);

@@ -56,8 +56,8 @@ template <int D, int NT>
 struct Shape {
   static constexpr int SLICE = q4_slice_bytes(D);
   static constexpr int PAGE = 2 * SLICE;               // K and V of one (page, head)
-  static constexpr int CTAS = NT == 1 ? 4 : (NT == 2 ? 3 : 2);  // meant to share an SM
-  static constexpr int PAIRS = (NT == 1 ? 3 : (NT == 2 ? 4 : 6)) * (D == 128 ? 1 : 2);  // ring, in pairs of pages
+  static constexpr int CTAS = NT == 1 ? 4 : 2;  // meant to share an SM
+  static constexpr int PAIRS = (NT == 1 ? 2 : 3) * (D == 128 ? 1 : 2);  // ring, in pairs of pages
   static constexpr int STAGE = 2 * PAGE;
   static constexpr int TILES = D / 16;                 // 16-dim tiles of O^T
   static constexpr int KSTEPS = D / 16;
@@ -162,8 +162,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
     if ((in_j & 31) == 0) load_ids();
   };
   load_ids();
-#pragma unroll 1
-  for (int i = 0; i < S::PAIRS; ++i) load_next(i);
+  load_next(0);
 
   // Key of row r of S^T: the keys of a pair change places in odd threads of a
   // quad, so that the V rows a quad reads at once lie in different banks.
@@ -229,6 +228,12 @@ attention_q4_kernel(const AttentionQ4Args a) {
       lim[t][b] = a.causal && m < rows ? min(u.pos0 + m / g + 1, u.kv_len) : u.kv_len;
       lim_min = min(lim_min, lim[t][b]);
     }
+  }
+  // The rest of the ring once the first unit's rows are here: asked for at once by
+  // every warp, it would queue in front of other warps' first pages.
+  if (unit == rec.unit) {
+#pragma unroll 1
+    for (int i = 1; i < S::PAIRS; ++i) load_next(i);
   }
   // every lane agrees on whether a page needs masks
   lim_min = __reduce_min_sync(0xffffffffu, lim_min);

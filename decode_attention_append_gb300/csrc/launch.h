@@ -193,7 +193,8 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                                 const int32_t* kv_exp, const int32_t* append_indptr,
                                 const int32_t* page_indices, const int32_t* kv_indptr,
                                 const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
-                                int head_dim, int64_t num_pages, int* err, cudaStream_t stream);
+                                int head_dim, int64_t num_pages, int sms, int* err,
+                                cudaStream_t stream);
 cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
                                  int64_t num_pages, void* out, int* err, cudaStream_t stream);

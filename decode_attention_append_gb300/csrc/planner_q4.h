@@ -27,7 +27,7 @@ constexpr int kQ4MinPages = 4;    // pages of a range at least
 
 inline int q4_class(int rows) { return (rows - 1) / 8; }
 // Warps of the class's kernel on an SM (its shared memory and registers).
-inline int q4_warps_per_sm(int cls) { return cls == 0 ? 16 : (cls == 1 ? 12 : 8); }
+inline int q4_warps_per_sm(int cls) { return cls == 0 ? 16 : 8; }
 
 // Sections of the workspace, all worked out from the counts and the layout of
 // the bf16 requests' plan.  The first plan_bytes are copied from the host.

@@ -66,17 +66,24 @@ __device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Eight floats -> e2m1 codes, nearest, ties to even, cut at 6 (first lowest).
-__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
+// Eight fp16 values -> e2m1 codes, nearest, ties to even, cut at 6 (first lowest).
+__device__ __forceinline__ uint32_t f16x8_to_e2m1x8(const uint32_t (&h)[4]) {
   uint32_t r;
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b0, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b1, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b2, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b3, %4;\n\t"
       "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
+  return r;
+}
+
+// Two floats -> fp16 pair, nearest (lo in the low half); infinities stay.
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 

@@ -22,6 +22,7 @@
 // slot, lengths past a row, more pages or rows than the buffers hold or the pool
 // has): the tables then describe an empty step and the error word says why.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "ptx.cuh"
@@ -58,19 +59,25 @@ struct Smem {
   }
 };
 
+// W: 64-bit sums, for batches whose longest possible step passes 32 bits.
+template <bool W>
 struct Sums {
-  long long pages, rows, take;
+  using T = typename std::conditional<W, long long, int>::type;
+  T pages, rows, take;
 };
 
 // Inclusive sums over the block's threads of three values at once; `total`
 // gets the block's sums.
-__device__ __forceinline__ Sums block_scan(Sums v, long long* ws, Sums& total) {
+template <bool W>
+__device__ __forceinline__ Sums<W> block_scan(Sums<W> v, long long* sums, Sums<W>& total) {
+  using T = typename Sums<W>::T;
+  T* ws = reinterpret_cast<T*>(sums);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, v.pages, m);
-    const long long b = __shfl_up_sync(0xffffffffu, v.rows, m);
-    const long long c = __shfl_up_sync(0xffffffffu, v.take, m);
+    const T a = __shfl_up_sync(0xffffffffu, v.pages, m);
+    const T b = __shfl_up_sync(0xffffffffu, v.rows, m);
+    const T c = __shfl_up_sync(0xffffffffu, v.take, m);
     if (lane >= m) {
       v.pages += a;
       v.rows += b;
@@ -83,10 +90,10 @@ __device__ __forceinline__ Sums block_scan(Sums v, long long* ws, Sums& total) {
     ws[2 * kWarps + warp] = v.take;
   }
   __syncthreads();
-  total = Sums{0, 0, 0};
+  total = Sums<W>{0, 0, 0};
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    const long long a = ws[w], b = ws[kWarps + w], c = ws[2 * kWarps + w];
+    const T a = ws[w], b = ws[kWarps + w], c = ws[2 * kWarps + w];
     if (w < warp) {
       v.pages += a;
       v.rows += b;
@@ -114,15 +121,16 @@ __device__ __forceinline__ int find_owner(const int* s, int n, int i) {
 // Reads the batch and leaves its sums in shared memory.  RELEASE: the pages of a
 // slot are those it holds, and there are no rows.  Returns the error code that
 // every CTA works out alike (0: none).
-template <bool RELEASE>
-__device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l, Sums& sum) {
+template <bool RELEASE, bool W>
+__device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l) {
+  const int free_count = a.counters[0];
   for (int i = threadIdx.x; i < l.words; i += kThreads) s.seen[i] = 0;
   __syncthreads();
-  sum = Sums{0, 0, 0};
+  Sums<W> sum{0, 0, 0};
   int bad = 0;
   for (int base = 0; base < a.batch; base += kThreads) {
     const int i = base + threadIdx.x;
-    Sums v{0, 0, 0};
+    Sums<W> v{0, 0, 0};
     int slot = -1, held = 0, len = 0;
     if (i < a.batch) {
       slot = __ldg(a.slots + i);
@@ -140,14 +148,15 @@ __device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l
         if (held < 0 || held > a.max_pages || len < 0 || kv > (long long)a.max_pages * kP) {
           bad = 1;
         } else {
-          v.pages = RELEASE ? held : (kv + kP - 1) / kP;
+          const int pages = RELEASE ? held : (int)((kv + kP - 1) / kP);
+          v.pages = pages;
           v.rows = n;
-          v.take = RELEASE ? 0 : max(0ll, v.pages - held);
+          v.take = RELEASE ? 0 : max(0, pages - held);
         }
       }
     }
-    Sums total;
-    const Sums inc = block_scan(v, s.warp_sums, total);
+    Sums<W> total;
+    const Sums<W> inc = block_scan<W>(v, s.warp_sums, total);
     if (i < a.batch) {
       s.kp[i] = (int)(sum.pages + inc.pages - v.pages);
       s.qo[i] = (int)(sum.rows + inc.rows - v.rows);
@@ -166,9 +175,8 @@ __device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l
     s.tp[a.batch] = (int)sum.take;
   }
   if (__syncthreads_or(bad)) return kDevErrShape;
-  const int free_count = a.counters[0];
   if (free_count < 0 || free_count > a.num_pages) return kDevErrShape;
-  if (RELEASE) return sum.pages > (long long)a.num_pages - free_count ? kDevErrShape : 0;
+  if (RELEASE) return sum.pages > a.num_pages - free_count ? kDevErrShape : 0;
   if (sum.pages > a.page_capacity || sum.rows > a.row_capacity) return kDevErrShape;
   return sum.take > free_count ? kDevErrNoPages : 0;
 }
@@ -186,12 +194,12 @@ __device__ __forceinline__ bool last_cta(int* ticket) {
   return s_last != 0;
 }
 
+template <bool W>
 __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const Layout l{a.batch, (a.num_slots + 31) / 32};
   const Smem s(smem, l);
-  Sums sum;
-  const int err = read_batch<false>(a, s, l, sum);
+  const int err = read_batch<false, W>(a, s, l);
   const int n = a.batch;
   if (err != 0) {
     if (blockIdx.x == 0) {
@@ -219,8 +227,9 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
       }
     }
   }
-  // page ids, four consecutive ones per thread (one search); new pages also
-  // enter their row of the block table
+  // page ids, four consecutive ones per thread (one search; a warp taking 128 in a
+  // row, lane by lane, measured slower: 18 us and 14 for 1.2 million pages); new
+  // pages also enter their row of the block table
   const int n_pages = s.kp[n], n_rows = s.qo[n];
   const int stride = (int)gridDim.x * kThreads;
   for (int64_t p0 = 4ll * (blockIdx.x * kThreads + threadIdx.x); p0 < n_pages; p0 += 4ll * stride) {
@@ -272,12 +281,12 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
 // The pages of the batch's slots go back on the stack in the reverse of the
 // order in which a step would take them, so releasing what was just taken
 // restores the stack.
+template <bool W>
 __global__ void __launch_bounds__(kThreads) release_pages_kernel(const StepTableArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const Layout l{a.batch, (a.num_slots + 31) / 32};
   const Smem s(smem, l);
-  Sums sum;
-  const int err = read_batch<true>(a, s, l, sum);
+  const int err = read_batch<true, W>(a, s, l);
   if (err != 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_device_error(a.err, err);
     return;
@@ -306,7 +315,10 @@ size_t step_table_smem(int batch, int num_slots) { return Layout{batch, (num_slo
 
 cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, cudaStream_t stream) {
   const size_t smem = step_table_smem(a.batch, a.num_slots);
-  auto kern = release ? release_pages_kernel : step_table_kernel;
+  // sums of pages and of tokens: at most max_pages * 16 a request
+  const bool wide = (int64_t)a.batch * a.max_pages * kP > INT32_MAX;
+  auto kern = release ? (wide ? release_pages_kernel<true> : release_pages_kernel<false>)
+                      : (wide ? step_table_kernel<true> : step_table_kernel<false>);
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

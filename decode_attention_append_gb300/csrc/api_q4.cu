@@ -121,7 +121,7 @@ daa_status daa_step_table(const daa_page_pool* pool, const int32_t* slots, const
   a.page_capacity = page_capacity;
   a.row_capacity = row_capacity;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return traced(kKernelStepTable, s, [&] { return launch_step_table(a, false, device_sms(), s); }) ==
+  return traced(kKernelStepTable, s, [&] { return launch_step_table(a, false, device_sms(), !tracer_on(), s); }) ==
                  cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;
@@ -139,7 +139,7 @@ daa_status daa_release_pages(const daa_page_pool* pool, const int32_t* slots, in
   a.slots = slots;
   a.batch = batch;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return traced(kKernelStepTable, s, [&] { return launch_step_table(a, true, device_sms(), s); }) ==
+  return traced(kKernelStepTable, s, [&] { return launch_step_table(a, true, device_sms(), !tracer_on(), s); }) ==
                  cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;
@@ -162,7 +162,8 @@ daa_status daa_kv_append_q4(const void* k_new, const void* v_new, void* kv_pages
   return traced(kKernelAppendQ4, s, [&] {
            return launch_kv_append_q4(k_new, v_new, kv_pages, kv_exp, append_indptr, page_indices,
                                       kv_indptr, last_page_len, batch, nnz_new, dims.num_kv_heads,
-                                      dims.head_dim, dims.num_pages, device_sms(), device_error_word(), s);
+                                      dims.head_dim, dims.num_pages, device_sms(), device_error_word(),
+                                      !tracer_on(), s);
          }) == cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;
@@ -179,7 +180,7 @@ daa_status daa_kv_dequant_q4(const void* kv_pages, const int32_t* kv_exp, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(kKernelDequantQ4, s, [&] {
            return launch_kv_dequant_q4(kv_pages, kv_exp, page_ids, nullptr, n_pages, dims.num_kv_heads,
-                                       dims.head_dim, dims.num_pages, out, device_error_word(), s);
+                                       dims.head_dim, dims.num_pages, out, device_error_word(), !tracer_on(), s);
          }) == cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;
@@ -276,7 +277,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
       return launch_kv_dequant_q4(kv_pages, kv_exp, page_indices,
                                   reinterpret_cast<const int32_t*>(ws + lay.off_src), lay.n_scratch,
                                   dims.num_kv_heads, dims.head_dim, dims.num_pages, ws + lay.off_pool,
-                                  device_error_word(), s);
+                                  device_error_word(), !tracer_on(), s);
     });
     if (e != cudaSuccess) return DAA_ERR_CUDA;
     LaunchSet ls{};
@@ -320,7 +321,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     // behind it; each kernel alone while the tracer times them
     const bool programmatic = !tracer_on();
     if (traced(kKernelAttentionQ4, s, [&] {
-          return launch_attention_q4(a, lay.n_ranges, programmatic && lay.n_scratch > 0, s);
+          return launch_attention_q4(a, lay.n_ranges, programmatic, programmatic && lay.n_scratch > 0, s);
         }) != cudaSuccess)
       return DAA_ERR_CUDA;
     if (lay.n_merges > 0) {

@@ -91,6 +91,8 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
   __shared__ int64_t s_page[kMaxRows];  // page * Hkv of the row, -1: not written
   __shared__ int s_slot[kMaxRows];
   __shared__ int s_indptr[kMaxBatch + 1];
+  grid_dep_launch();
+  grid_dep_wait();
   const int kv = blockIdx.y;
   const int per_row = Hkv * NB;
   const int64_t total = (int64_t)nnz_new * per_row;
@@ -174,6 +176,8 @@ kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict
                      int64_t n_slices, int Hkv, int64_t num_pages, uint16_t* __restrict__ out,
                      int* err) {
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
+  grid_dep_launch();
+  grid_dep_wait();
   const int tok = threadIdx.x / NB, blk = threadIdx.x % NB;
   const int64_t s0 = (int64_t)blockIdx.x * kDeqU;
   uint2 codes[kDeqU];
@@ -229,7 +233,8 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                                 const int32_t* kv_exp, const int32_t* append_indptr,
                                 const int32_t* page_indices, const int32_t* kv_indptr,
                                 const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
-                                int head_dim, int64_t num_pages, int sms, int* err, cudaStream_t stream) {
+                                int head_dim, int64_t num_pages, int sms, int* err, bool programmatic,
+                                cudaStream_t stream) {
   if (nnz_new <= 0 || batch <= 0) return cudaSuccess;
   const int64_t total = (int64_t)nnz_new * Hkv * (head_dim / kQ4Block);
   const bool large = total >= (int64_t)sms * 16 * kThreads * kSmallU;  // 16 CTAs an SM
@@ -238,23 +243,23 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   auto kern = head_dim == 128 ? (large ? kv_append_q4_kernel<128, kLargeU> : kv_append_q4_kernel<128, kSmallU>)
                               : (large ? kv_append_q4_kernel<64, kLargeU> : kv_append_q4_kernel<64, kSmallU>);
-  kern<<<dim3((unsigned)grid, 2), kThreads, 0, stream>>>(
-      (const uint4*)k_new, (const uint4*)v_new, (uint8_t*)pool, kv_exp, append_indptr, page_indices,
-      kv_indptr, last_page_len, batch, nnz_new, Hkv, num_pages, err);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3((unsigned)grid, 2), dim3(kThreads), 0, stream, programmatic,
+                       (const uint4*)k_new, (const uint4*)v_new, (uint8_t*)pool, kv_exp, append_indptr,
+                       page_indices, kv_indptr, last_page_len, batch, nnz_new, Hkv, num_pages, err);
 }
 
 cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
-                                 int64_t num_pages, void* out, int* err, cudaStream_t stream) {
+                                 int64_t num_pages, void* out, int* err, bool programmatic,
+                                 cudaStream_t stream) {
   if (n_pages <= 0) return cudaSuccess;
   const int64_t n_slices = n_pages * 2 * Hkv;
   const int64_t grid = (n_slices + kDeqU - 1) / kDeqU;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   auto kern = head_dim == 128 ? kv_dequant_q4_kernel<128> : kv_dequant_q4_kernel<64>;
-  kern<<<(unsigned)grid, kQ4Page * (head_dim / kQ4Block), 0, stream>>>(
-      (const uint8_t*)pool, kv_exp, ids, src, n_slices, Hkv, num_pages, (uint16_t*)out, err);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kQ4Page * (head_dim / kQ4Block)), 0, stream,
+                       programmatic, (const uint8_t*)pool, kv_exp, ids, src, n_slices, Hkv, num_pages,
+                       (uint16_t*)out, err);
 }
 
 }  // namespace daa

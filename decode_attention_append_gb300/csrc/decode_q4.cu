@@ -104,7 +104,10 @@ attention_q4_kernel(const AttentionQ4Args a) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * S::PAIRS;
   uint8_t* ring = smem + warp * (S::PAIRS * S::STAGE);
 
-  grid_dep_launch();  // the next kernel of the call may start its CTAs
+  // The next kernel may start its CTAs, but not before this one may read: the next
+  // class's launch does not wait by itself.
+  if (a.wait_first) grid_dep_wait();
+  grid_dep_launch();
   // the heads of a range in warps side by side: their slices of a page are, too
   const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
   const int range = (int)(id / a.Hkv);
@@ -562,9 +565,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeA
 }
 
 template <int D, int NT>
-cudaError_t launch_t(AttentionQ4Args a, int n_ranges, bool programmatic, cudaStream_t stream) {
+cudaError_t launch_t(AttentionQ4Args a, int n_ranges, bool programmatic, bool beside, cudaStream_t stream) {
   using S = Shape<D, NT>;
   a.n_ranges = n_ranges;
+  a.wait_first = !beside;
   auto kern = attention_q4_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
   if (e != cudaSuccess) return e;
@@ -574,16 +578,15 @@ cudaError_t launch_t(AttentionQ4Args a, int n_ranges, bool programmatic, cudaStr
 }
 
 template <int D>
-cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], bool programmatic,
+cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], bool programmatic, bool beside,
                      cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < kQ4Classes && e == cudaSuccess; ++i) {
     if (n_ranges[i] == 0) continue;
-    e = i == 0   ? launch_t<D, 1>(a, n_ranges[i], programmatic, stream)
-        : i == 1 ? launch_t<D, 2>(a, n_ranges[i], programmatic, stream)
-        : i == 2 ? launch_t<D, 3>(a, n_ranges[i], programmatic, stream)
-                 : launch_t<D, 4>(a, n_ranges[i], programmatic, stream);
-    programmatic = true;
+    e = i == 0   ? launch_t<D, 1>(a, n_ranges[i], programmatic, beside, stream)
+        : i == 1 ? launch_t<D, 2>(a, n_ranges[i], programmatic, beside, stream)
+                 : launch_t<D, 3>(a, n_ranges[i], programmatic, beside, stream);
+    beside = programmatic;
     a.ranges += n_ranges[i];
   }
   return e;
@@ -592,9 +595,9 @@ cudaError_t launch_d(AttentionQ4Args a, const int (&n_ranges)[kQ4Classes], bool 
 }  // namespace
 
 cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
-                                bool programmatic, cudaStream_t stream) {
-  return a.head_dim == 128 ? launch_d<128>(a, n_ranges, programmatic, stream)
-                           : launch_d<64>(a, n_ranges, programmatic, stream);
+                                bool programmatic, bool beside, cudaStream_t stream) {
+  return a.head_dim == 128 ? launch_d<128>(a, n_ranges, programmatic, beside, stream)
+                           : launch_d<64>(a, n_ranges, programmatic, beside, stream);
 }
 
 cudaError_t launch_merge_q4(const MergeArgs& a, int n_parts, bool programmatic, cudaStream_t stream) {

@@ -161,6 +161,9 @@ struct LaunchSet {
 struct PlanLayout;
 
 // ------------------------------------------------------- step tables, 4-bit cache
+// These kernels are launched programmatically (unless the tracer times them): each
+// lets the next one start its CTAs at once and waits for the kernel before it
+// before its first access, so that of two in a row only the launch overlaps.
 // Step tables from request lengths (step_table.cu); release: only slots, batch
 // and the pool are read.
 struct StepTableArgs {
@@ -185,7 +188,8 @@ struct StepTableArgs {
   int* err;
 };
 size_t step_table_smem(int batch, int num_slots);
-cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, cudaStream_t stream);
+cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, bool programmatic,
+                              cudaStream_t stream);
 
 // 4-bit cache (append_q4.cu): the quantising append, and pages as bf16.
 // kv_exp: [2][Hkv] or null.  dequant: out page i is pool page ids[src ? src[i] : i].
@@ -194,10 +198,11 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                                 const int32_t* page_indices, const int32_t* kv_indptr,
                                 const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
                                 int head_dim, int64_t num_pages, int sms, int* err,
-                                cudaStream_t stream);
+                                bool programmatic, cudaStream_t stream);
 cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
-                                 int64_t num_pages, void* out, int* err, cudaStream_t stream);
+                                 int64_t num_pages, void* out, int* err, bool programmatic,
+                                 cudaStream_t stream);
 
 // Attention over the 4-bit pages (decode_q4.cu); n_ranges per class, in order.
 struct AttentionQ4Args {
@@ -208,6 +213,7 @@ struct AttentionQ4Args {
   const Q4Unit* units;
   const Q4Range* ranges;
   int n_ranges;            // set by the launch of each class
+  int wait_first;          // read nothing before the kernel before has completed
   int Hq, Hkv, group, head_dim;
   int64_t num_pages;
   int causal;
@@ -218,9 +224,9 @@ struct AttentionQ4Args {
   float* part_lse;         // [n_parts][Hq] (log2 domain)
   int* err;
 };
-// programmatic: the kernel before on the stream is of the same call and is not read.
+// beside: the kernel before on the stream is of the same call and is not read.
 cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[kQ4Classes],
-                                bool programmatic, cudaStream_t stream);
+                                bool programmatic, bool beside, cudaStream_t stream);
 // softmax_merge of its n_parts parts (items without a prefix part).
 cudaError_t launch_merge_q4(const MergeArgs& a, int n_parts, bool programmatic, cudaStream_t stream);
 

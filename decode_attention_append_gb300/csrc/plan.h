@@ -43,8 +43,8 @@ struct __align__(16) Q4Range {
   int32_t pad0, pad1;
 };
 // Units come in classes by the query rows (tokens x heads) they hold, each its
-// own ranges and launch: up to 8, 16, 24, 32.
-constexpr int kQ4Classes = 4;
+// own ranges and launch: up to 8, 16, 24.
+constexpr int kQ4Classes = 3;
 
 // softmax_merge of the partials of one query row: n_parts consecutive slots
 // from part_begin (the key splits of its request), plus slot `extra` when the

@@ -21,11 +21,14 @@
 namespace daa {
 
 constexpr int kQ4NativeRows = 64;
-constexpr int kQ4UnitRows = 32;   // rows a unit holds at most
+// Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
+// page on an SM: 62, 90 and 153 ns with 8, 16 and 24 rows).  Where all units of 8
+// rows find a free warp, smaller ones end sooner.
+constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
 constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages
 constexpr int kQ4MinPages = 4;    // pages of a range at least
 
-inline int q4_class(int rows) { return (rows - 1) / 8; }
+inline int q4_class(int rows) { return (rows - 1) / 8; }  // up to 8, 16, 24 rows
 // Warps of the class's kernel on an SM (its shared memory and registers).
 inline int q4_warps_per_sm(int cls) { return cls == 0 ? 16 : 8; }
 
@@ -37,7 +40,7 @@ struct Q4Layout {
   PlanLayout sub;
   size_t off_units, off_ranges, off_merges, off_src, off_ids, off_sub, plan_bytes, off_part_o, off_part_lse,
       off_pool, total;
-  int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2] + n_ranges[3]; }
+  int ranges() const { return n_ranges[0] + n_ranges[1] + n_ranges[2]; }
   void finish(const daa_dims& d) {
     size_t off = 0;
     off_units = off;
@@ -98,13 +101,18 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
   }
   const int P = d.page_size;
   const int g = d.num_qo_heads / d.num_kv_heads;
-  const int tpu = kQ4UnitRows / g;  // tokens of a unit
+  // units of a request at `rows` a unit
+  auto units_of = [g](int64_t nq, int rows) {
+    const int64_t tokens = std::max(1, rows / g);
+    return (nq + tokens - 1) / tokens;
+  };
   // what units are cut from: some new tokens of a request, by class
   struct Stream {
     int r, t0, n_tok, pages, n_units, unit0;
   };
   thread_local std::vector<Stream> streams[kQ4Classes];
   for (auto& v : streams) v.clear();
+  int64_t small_pages = 0;  // pages that units of few rows would read
   for (int r = 0; r < batch; ++r) {
     const int64_t nq = (int64_t)qo[r + 1] - qo[r];
     const int64_t np = (int64_t)kv[r + 1] - kv[r];
@@ -119,11 +127,20 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
       pl.sub_kv.push_back(pl.sub_kv.back() + (int32_t)np);
       pl.sub_last.push_back(last[r]);
       for (int64_t p = 0; p < np; ++p) pl.src.push_back((int32_t)(kv[r] + p));
-    } else if (nq > 0) {
-      for (int t0 = 0; t0 < nq; t0 += tpu) {
-        const int n = std::min<int>(tpu, (int)nq - t0);
-        streams[q4_class(n * g)].push_back(Stream{r, t0, n, (int)np, 0, 0});
-      }
+    } else {
+      small_pages += np * units_of(nq, kQ4SmallUnitRows);
+    }
+  }
+  const int64_t free_warps = (int64_t)sms * q4_warps_per_sm(0) / d.num_kv_heads;
+  const int unit_rows = small_pages <= free_warps * kQ4MinPages ? kQ4SmallUnitRows : kQ4UnitRows;
+  for (int r = 0; r < batch; ++r) {
+    const int nq = qo[r + 1] - qo[r];
+    if (nq == 0 || nq * g > kQ4NativeRows) continue;
+    const int n_units = (int)units_of(nq, unit_rows);
+    for (int i = 0, t0 = 0; i < n_units; ++i) {  // as equal as they come
+      const int n = (nq - t0 + n_units - i - 1) / (n_units - i);
+      streams[q4_class(n * g)].push_back(Stream{r, t0, n, kv[r + 1] - kv[r], 0, 0});
+      t0 += n;
     }
   }
   // Ranges: one for every warp that can be resident (over the kv heads), each with

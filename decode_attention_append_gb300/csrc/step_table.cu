@@ -199,6 +199,8 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
   extern __shared__ __align__(16) uint8_t smem[];
   const Layout l{a.batch, (a.num_slots + 31) / 32};
   const Smem s(smem, l);
+  grid_dep_launch();
+  grid_dep_wait();
   const int err = read_batch<false, W>(a, s, l);
   const int n = a.batch;
   if (err != 0) {
@@ -286,6 +288,8 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const StepTable
   extern __shared__ __align__(16) uint8_t smem[];
   const Layout l{a.batch, (a.num_slots + 31) / 32};
   const Smem s(smem, l);
+  grid_dep_launch();
+  grid_dep_wait();
   const int err = read_batch<true, W>(a, s, l);
   if (err != 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_device_error(a.err, err);
@@ -313,7 +317,8 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const StepTable
 
 size_t step_table_smem(int batch, int num_slots) { return Layout{batch, (num_slots + 31) / 32}.bytes(); }
 
-cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, cudaStream_t stream) {
+cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, bool programmatic,
+                              cudaStream_t stream) {
   const size_t smem = step_table_smem(a.batch, a.num_slots);
   // sums of pages and of tokens: at most max_pages * 16 a request
   const bool wide = (int64_t)a.batch * a.max_pages * kP > INT32_MAX;
@@ -329,8 +334,7 @@ cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, cud
   const int64_t want = std::max<int64_t>((pages + 4 * kThreads - 1) / (4 * kThreads),
                                          release ? 1 : (a.row_capacity + kThreads - 1) / kThreads);
   const int grid = (int)std::min<int64_t>(std::max<int64_t>(want, 1), sms);
-  kern<<<grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3(grid), dim3(kThreads), smem, stream, programmatic, a);
 }
 
 }  // namespace daa

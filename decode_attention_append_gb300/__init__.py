@@ -252,7 +252,9 @@ def _use_stream(stream):
     """torch's own work of a call on the stream that the call names."""
     if stream is None:
         return contextlib.nullcontext()
-    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _dims(kv_pages: torch.Tensor, num_qo_heads: int) -> _Dims:

@@ -20,7 +20,9 @@
 
 namespace daa {
 
-constexpr int kQ4NativeRows = 64;
+// GB300, 8 kv heads, d = 128, 32 requests of 2500 keys, 4 and 8 heads a kv head: 96
+// rows 140 us from the 4-bit pages and 167 by way of bf16, 128 rows 206 and 172.
+constexpr int kQ4NativeRows = 96;
 // Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
 // page on an SM: 62, 90 and 153 ns with 8, 16 and 24 rows).  Where all units of 8
 // rows find a free warp, smaller ones end sooner.

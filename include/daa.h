@@ -614,7 +614,7 @@ daa_status daa_release_pages(const daa_page_pool* pool, const int32_t* slots, in
  * workspace, masks, outputs and errors).  The result is that of
  * daa_batch_attention on the pool's values in bf16, up to fp32 rounding order
  * and the rounding of the softmax weights.  Slots past a request's last token
- * may hold anything.  Requests of up to a few packed (token, query head) rows are
+ * may hold anything.  Requests of up to 96 packed (token, query head) rows are
  * read from the 4-bit pages; the pages of longer chunks are written to the
  * workspace in bf16 first (2 * Hkv * head_dim * 32 bytes a page), each once.
  *  plan: host arrays of daa_batch_attention; the workspace (at least

@@ -475,3 +475,143 @@ def test_serving_steps_together(daa, hq, hkv, d, exps):
         if i == 2:
             pool.release([1, 2])
     assert np.isin(t.slot_map.cpu().numpy() // 16, t.page_indices.cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("hq,hkv,new", [(8, 1, [12]), (8, 1, [13]), (4, 1, [24, 25]), (16, 1, [6, 7, 1])])
+def test_attention_around_the_row_threshold(daa, hq, hkv, new):
+    """The largest requests read from the 4-bit pages and the smallest that go by way of bf16 ones."""
+    _check(daa, np.random.default_rng(21), hq, hkv, 128, [333] * len(new), new)
+    _check(daa, np.random.default_rng(22), hq, hkv, 64, [90] * len(new), new, causal=False)
+
+
+def test_attention_many_small_requests(daa):
+    rng = np.random.default_rng(23)
+    n = 1500
+    _check(daa, rng, 6, 3, 64, rng.integers(0, 40, n).tolist(), rng.integers(0, 3, n).tolist())
+
+
+def test_offsets_past_32_bits(daa):
+    """Pages whose bytes lie past 4 GB: appended, read back and attended to."""
+    rng = np.random.default_rng(24)
+    hkv, d = 4, 128
+    n = (1 << 32) // (hkv * 2 * 9 * d) + 100
+    pool = torch.zeros(n, hkv, 2, 9 * d, dtype=torch.uint8, device=DEV)
+    t, used = ref.make_table(rng, [0, 0], [50, 129], spare=0)
+    low = t["page_indices"].copy()
+    t["page_indices"] = (n - used + low).astype(np.int32)
+    g = {x: _dev(y) for x, y in t.items()}
+    k, v, q = _bf16(rng, (179, hkv, d)), _bf16(rng, (179, hkv, d)), _bf16(rng, (179, 2 * hkv, d))
+    daa.kv_append_q4(k.to(DEV), v.to(DEV), pool, g["qo_indptr"], g["page_indices"], g["kv_indptr"], g["last_page_len"])
+    host = np.zeros((used, hkv, 2, 9 * d), np.uint8)
+    small = dict(t, page_indices=low)
+    ref.append(host, k.double().numpy(), v.double().numpy(), small, None)
+    assert np.array_equal(pool[n - used:].cpu().numpy(), host)
+    assert not pool[:n - used].any()
+    back = daa.kv_dequant_q4(pool, g["page_indices"])
+    assert np.array_equal(back.double().cpu().numpy(), ref.decode_pages(host[low], d, None))
+    for rows, tab in ((slice(0, 179), small), (slice(49, 50), None)):
+        if tab is None:  # the first request's last token alone: a decode step
+            tab = {"qo_indptr": np.array([0, 1], np.int32), "kv_indptr": t["kv_indptr"][:2],
+                   "page_indices": low[:t["kv_indptr"][1]], "last_page_len": t["last_page_len"][:1]}
+        table = daa.PageTable.from_host(tab["qo_indptr"], tab["kv_indptr"], n - used + tab["page_indices"],
+                                        tab["last_page_len"], DEV)
+        lse = torch.empty(q[rows].shape[0], 2 * hkv, device=DEV)
+        out = daa.BatchAttentionQ4(table, 2 * hkv, pool).run(q[rows].to(DEV), lse=lse)
+        ref.check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(),
+                            ref.attention(q[rows].double().numpy(), host, tab, None, d, 1 / d ** 0.5), d)
+
+
+def test_two_streams_at_once(daa):
+    """Two batches with workspaces of their own, many runs under way at the same time."""
+    rng = np.random.default_rng(25)
+    made = [_attend(daa, rng, 8, 2, 128, [3000, 40, 900], [1, 5, 30]), _attend(daa, rng, 16, 1, 64, [5000, 7], [1, 1])]
+    streams = [torch.cuda.Stream() for _ in made]
+    torch.cuda.synchronize()
+    outs = []
+    for (attn, q, out, lse, want), s in zip(made, streams):
+        qd, o, l = q.to(DEV), torch.zeros_like(out), torch.zeros_like(lse)
+        torch.cuda.synchronize()
+        outs.append((attn, qd, o, l, s))
+    for _ in range(20):
+        for attn, qd, o, l, s in outs:
+            attn.run(qd, out=o, lse=l, stream=s)
+    torch.cuda.synchronize()
+    for (attn, q, out, lse, want), (_, _, o, l, _) in zip(made, outs):
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_step_in_a_graph(daa):
+    """Tables, append and attention of a step captured as one graph and replayed with new values."""
+    rng = np.random.default_rng(26)
+    hq, hkv, d = 8, 2, 128
+    slots, cached, new = [3, 0, 2], [100, 33, 700], [1, 2, 1]
+    st = _state(rng, 4, 60, 150, dict(zip(slots, cached)))
+    pool = _device_pool(daa, st, 150)
+    want = ref.step_table({**st, "free": list(st["free"]), "held": st["held"].copy(), "block_table": st["block_table"].copy()},
+                          slots, new, False)
+    ht = {x: np.array(want[x], np.int32) for x in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len")}
+    o = _outs(3, len(want["page_indices"]), 4)
+    table = daa.PageTable(o["qo_indptr"], o["kv_indptr"], o["page_indices"], o["last_page_len"], ht["qo_indptr"],
+                          ht["kv_indptr"], ht["last_page_len"])
+    cache = _dev(_pool(rng, 150, hkv, d))
+    first = cache.clone()
+    attn = daa.BatchAttentionQ4(table, hq, cache)
+    attn.plan()
+    q, k, v = (torch.zeros(4, h, d, dtype=torch.bfloat16, device=DEV) for h in (hq, hkv, hkv))
+    out, lse = torch.empty_like(q), torch.empty(4, hq, device=DEV)
+    s_dev, n_dev = _dev(np.array(slots, np.int32)), _dev(np.array(new, np.int32))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pool.build(s_dev, n_dev, **o)
+        attn.append(k, v)
+        attn.run(q, out=out, lse=lse)
+    for _ in range(3):
+        cache.copy_(first)
+        hq_, hk_, hv_ = _bf16(rng, q.shape), _bf16(rng, k.shape), _bf16(rng, v.shape)
+        q.copy_(hq_), k.copy_(hk_), v.copy_(hv_)
+        graph.replay()
+        torch.cuda.synchronize()
+        for name in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len", "slot_map", "positions"):
+            assert np.array_equal(o[name].cpu().numpy(), want[name]), name
+        host = first.cpu().numpy()
+        ref.append(host, hk_.double().numpy(), hv_.double().numpy(), ht, None)
+        assert np.array_equal(cache.cpu().numpy(), host)
+        ref.check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(),
+                            ref.attention(hq_.double().numpy(), host, ht, None, d, 1 / d ** 0.5), d)
+
+
+def test_traced_runs(daa):
+    """Under the tracer every kernel runs alone; the results are the same, and the kernels have names."""
+    rng = np.random.default_rng(27)
+    attn, q, out, lse, want = _attend(daa, rng, 12, 3, 128, [3000, 20, 64], [1, 1, 200])
+    qd, o2 = q.to(DEV), torch.zeros_like(out)
+    daa.trace_enable(64)
+    try:
+        attn.run(qd, out=o2)
+        daa.kv_dequant_q4(attn.kv_pages, attn.t.page_indices)
+        names = [n for n, _ in daa.trace_read()]
+    finally:
+        daa.trace_disable()
+    assert torch.equal(o2, out)
+    assert names[0] == "kv_dequant_q4" and names[-1] == "kv_dequant_q4" and "attention_q4" in names
+
+
+def test_append_after_other_kernels(daa):
+    """Launches overlap the kernel before them: values written just before are the ones that are used."""
+    rng = np.random.default_rng(28)
+    hkv, d = 2, 128
+    t, n = ref.make_table(rng, [0, 5], [300, 40])
+    g = {x: _dev(y) for x, y in t.items()}
+    src = [_bf16(rng, (340, hkv, d)).to(DEV) for _ in range(4)]
+    k = torch.empty_like(src[0])
+    pool = daa.new_q4_pool(n, hkv, d)
+    reads = []
+    for x in src:
+        k.copy_(x)
+        daa.kv_append_q4(k, k, pool, g["qo_indptr"], g["page_indices"], g["kv_indptr"], g["last_page_len"])
+        reads.append(daa.kv_dequant_q4(pool, g["page_indices"]))
+    for x, r in zip(src, reads):
+        host = np.zeros((n, hkv, 2, 9 * d), np.uint8)
+        ref.append(host, x.double().cpu().numpy(), x.double().cpu().numpy(), t, None)
+        assert np.array_equal(r.double().cpu().numpy(), ref.decode_pages(host[t["page_indices"]], d, None))

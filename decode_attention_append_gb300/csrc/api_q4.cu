@@ -180,7 +180,8 @@ daa_status daa_kv_dequant_q4(const void* kv_pages, const int32_t* kv_exp, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return traced(kKernelDequantQ4, s, [&] {
            return launch_kv_dequant_q4(kv_pages, kv_exp, page_ids, nullptr, n_pages, dims.num_kv_heads,
-                                       dims.head_dim, dims.num_pages, out, device_error_word(), !tracer_on(), s);
+                                       dims.head_dim, dims.num_pages, out, device_sms(), device_error_word(),
+                                       !tracer_on(), s);
          }) == cudaSuccess
              ? DAA_OK
              : DAA_ERR_CUDA;
@@ -276,7 +277,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     cudaError_t e = traced(kKernelDequantQ4, s, [&] {
       return launch_kv_dequant_q4(kv_pages, kv_exp, page_indices,
                                   reinterpret_cast<const int32_t*>(ws + lay.off_src), lay.n_scratch,
-                                  dims.num_kv_heads, dims.head_dim, dims.num_pages, ws + lay.off_pool,
+                                  dims.num_kv_heads, dims.head_dim, dims.num_pages, ws + lay.off_pool, device_sms(),
                                   device_error_word(), !tracer_on(), s);
     });
     if (e != cudaSuccess) return DAA_ERR_CUDA;

@@ -8,12 +8,14 @@
 // an infinity as the block's largest value: the cache holds finite numbers only,
 // so a key that a mask hides can never spoil a sum with 0 * NaN.
 //
-// Rounding y / s without a division per value: y has the 8 significant bits of
-// a bf16 and every midpoint of two e2m1 values times s has at most 7, so y / s
-// is either exactly a midpoint or at least 2^-9 (relative) away from one.
-// y * (1 / s) is off by at most 2^-23, so rounding it to fp16 (11 bits, a half
-// step of 2^-11 at most) lands on the midpoint exactly when y / s does, and the
-// conversion's tie rule then applies to the exact quotient.
+// Rounding a quotient without a division: y has the 8 significant bits of a bf16
+// and every midpoint of two e2m1 values times s has at most 7, so y / s is either
+// exactly a midpoint or at least 2^-9 (relative) away from one.  y * (1 / s), with
+// an approximate reciprocal, is off by less than 2^-21, so rounding it to fp16
+// (11 bits, a half step of 2^-11 at most) lands on the midpoint exactly when y / s
+// does, and the conversion's tie rule then applies to the exact quotient.  max|y| / 6
+// is rounded to e4m3 the same way: 6 times a midpoint of two e4m3 values (5
+// significant bits) has at most 7.
 //
 // Bound: HBM (2 + 9/16 bytes a value); about four instructions a value (widen,
 // scale, the maximum taken on packed bits, two conversions a pair).
@@ -39,6 +41,14 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   return v;
 }
 
+// 32 bytes at once, where the address allows it: the two 16-byte loads of a block
+// would each ask for half of every 32-byte sector of the warp's kilobyte.
+__device__ __forceinline__ void ld_stream_32(const uint4* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 // The largest |value| of 16 bf16 values as bits, taken two at a time: without a
 // sign bf16 values are ordered as their bits, and NaN is above infinity.
 __device__ __forceinline__ uint32_t max_abs_bits(const uint32_t (&w)[8]) {
@@ -62,10 +72,9 @@ __device__ __forceinline__ uint2 quantise_block(const uint4& a, const uint4& b, 
     top = max_abs_bits(w);
   }
   const float amax = __uint_as_float(top << 16);
-  // clamp(max|y| / 6): a true division, so that its ties are ties
-  const float s6 = fminf(fmaxf(__fdiv_rn(amax * two_to_minus_e, 6.f), 0.001953125f), 448.f);
-  const uint16_t sb = f32x2_to_e4m3x2(s6, 0.f);
-  const float r = __fdiv_rn(1.f, f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x) * two_to_minus_e;
+  const float s6 = fminf(fmaxf(amax * two_to_minus_e * (1.f / 6.f), 0.001953125f), 448.f);
+  const uint16_t sb = f16x2_to_e4m3x2(f32x2_to_f16x2(s6, 0.f));
+  const float r = rcp_approx(f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x) * two_to_minus_e;
   scale = (uint8_t)(sb & 0xFFu);
   uint32_t h[8];
 #pragma unroll
@@ -84,7 +93,7 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
                     const int32_t* __restrict__ append_indptr,
                     const int32_t* __restrict__ page_indices, const int32_t* __restrict__ kv_indptr,
                     const int32_t* __restrict__ last_page_len, int batch, int nnz_new, int Hkv,
-                    int64_t num_pages, int* err) {
+                    int step_rows, int step_blocks, int64_t num_pages, int* err) {
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
   constexpr int kAppendSpan = kThreads * kAppendU;
   constexpr int kMaxRows = kAppendSpan / NB + 2;  // rows a CTA touches (a row has NB blocks or more)
@@ -100,16 +109,24 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
   const int64_t last = min(first + kAppendSpan, total);
   const int row0 = (int)(first / per_row);
   const int in_row0 = (int)(first - (int64_t)row0 * per_row);
-  const int nrows = (int)((last - 1) / per_row) - row0 + 1;
+  const int nrows = (in_row0 + (int)(last - first) - 1) / per_row + 1;
   // the values do not depend on the page table: load them first
   const uint4* src = kv == 0 ? k_new : v_new;
   uint4 a[kAppendU], b[kAppendU];
+  if (reinterpret_cast<uintptr_t>(src) % 32 == 0) {
 #pragma unroll
-  for (int u = 0; u < kAppendU; ++u) {
-    const int64_t i = first + u * kThreads + threadIdx.x;
-    if (i < last) {
-      a[u] = ld_stream(src + 2 * i);
-      b[u] = ld_stream(src + 2 * i + 1);
+    for (int u = 0; u < kAppendU; ++u) {
+      const int64_t i = first + u * kThreads + threadIdx.x;
+      if (i < last) ld_stream_32(src + 2 * i, a[u], b[u]);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kAppendU; ++u) {
+      const int64_t i = first + u * kThreads + threadIdx.x;
+      if (i < last) {
+        a[u] = ld_stream(src + 2 * i);
+        b[u] = ld_stream(src + 2 * i + 1);
+      }
     }
   }
   // the search for a row's request is a chain of loads: in shared memory where the
@@ -146,13 +163,20 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
     s_slot[t] = slot;
   }
   __syncthreads();
+  // a thread's blocks are kThreads = step_rows * per_row + step_blocks apart
+  int next_row = (in_row0 + (int)threadIdx.x) / per_row;
+  int next_hb = in_row0 + (int)threadIdx.x - next_row * per_row;
 #pragma unroll
   for (int u = 0; u < kAppendU; ++u) {
-    const int64_t i = first + u * kThreads + threadIdx.x;
-    if (i >= last) continue;
-    const unsigned rel = (unsigned)(in_row0 + u * kThreads + threadIdx.x);
-    const unsigned row = rel / (unsigned)per_row, hb = rel - row * (unsigned)per_row;
-    const int h = (int)(hb / NB), blk = (int)(hb % NB);
+    const int row = next_row, hb = next_hb;
+    next_row += step_rows;
+    next_hb += step_blocks;
+    if (next_hb >= per_row) {
+      next_hb -= per_row;
+      ++next_row;
+    }
+    if (first + u * kThreads + threadIdx.x >= last) continue;
+    const int h = (int)((unsigned)hb / NB), blk = (int)((unsigned)hb % NB);
     const int64_t page = s_page[row];
     if (page < 0) continue;
     const int slot = s_slot[row];
@@ -165,12 +189,13 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
   }
 }
 
-// Pages -> bf16: a thread takes one (token, block of 16 dims) of a slice, kDeqU
-// slices at a time.  Scratch page i comes from pool page ids[src ? src[i] : i].
-constexpr int kDeqU = 4;
+// Pages -> bf16: a thread takes 8 dims of tokens tok and tok + 8 of a slice (so that
+// a warp's 16-byte stores lie side by side), kDeqU slices at a time.  Scratch page i
+// comes from pool page ids[src ? src[i] : i].
+constexpr int kDeqSmallU = 2, kDeqLargeU = 4;
 
-template <int D>
-__global__ void __launch_bounds__(kQ4Page * (D / kQ4Block))
+template <int D, int kDeqU>
+__global__ void __launch_bounds__(D, 2048 / D)
 kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ kv_exp,
                      const int32_t* __restrict__ ids, const int32_t* __restrict__ src,
                      int64_t n_slices, int Hkv, int64_t num_pages, uint16_t* __restrict__ out,
@@ -178,52 +203,70 @@ kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
   grid_dep_launch();
   grid_dep_wait();
-  const int tok = threadIdx.x / NB, blk = threadIdx.x % NB;
+  const int tok = threadIdx.x / (D / 8), chunk = threadIdx.x % (D / 8), blk = chunk / 2;
+  // slice s0 = blockIdx.x * kDeqU is slice `rem` of page i (32-bit divisions only)
+  const int per_page = 2 * Hkv;
   const int64_t s0 = (int64_t)blockIdx.x * kDeqU;
-  uint2 codes[kDeqU];
-  uint8_t sc[kDeqU];
-  float two_e[kDeqU];
+  const int n = (int)min((int64_t)kDeqU, n_slices - s0);
+  const unsigned groups = blockIdx.x / (unsigned)per_page;
+  const unsigned in_group = (blockIdx.x - groups * per_page) * kDeqU;
+  int i = (int)(groups * kDeqU + in_group / (unsigned)per_page);
+  int rem = (int)(in_group % (unsigned)per_page);
+  // rounds of loads, each of all slices at once: page ids (by way of src), codes
+  int page[kDeqU], at[kDeqU];  // at: K (0) or V (Hkv) plus head
 #pragma unroll
   for (int u = 0; u < kDeqU; ++u) {
-    const int64_t s = s0 + u;
-    codes[u] = make_uint2(0u, 0u);
-    sc[u] = 0;
-    two_e[u] = 1.f;
-    if (s < n_slices) {
-      const int64_t i = s / (2 * Hkv);
-      const int rem = (int)(s - i * (2 * Hkv));
-      const int kv = rem / Hkv, h = rem - kv * Hkv;
-      const int64_t page = __ldg(ids + (src ? (int64_t)__ldg(src + i) : i));
-      if (page < 0 || page >= num_pages) {
-        if (threadIdx.x == 0) set_device_error(err, kDevErrPageRange);  // the page reads as zeros
-      } else {
-        const uint8_t* slice = pool + ((page * Hkv + h) * 2 + kv) * SLICE;
-        codes[u] = __ldg(reinterpret_cast<const uint2*>(slice + tok * (D / 2) + blk * 8));
-        sc[u] = __ldg(slice + P * (D / 2) + (kv == 0 ? tok * NB + blk : blk * P + tok));
-        if (kv_exp) two_e[u] = q4_pow2(__ldg(kv_exp + kv * Hkv + h));
-      }
+    at[u] = rem;
+    page[u] = i;
+    if (++rem == per_page) {
+      rem = 0;
+      ++i;
+    }
+  }
+  if (src) {
+#pragma unroll
+    for (int u = 0; u < kDeqU; ++u)
+      if (u < n) page[u] = __ldg(src + page[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kDeqU; ++u)
+    if (u < n) page[u] = __ldg(ids + page[u]);
+  uint32_t codes[kDeqU][2];
+  uint32_t sc[kDeqU];
+#pragma unroll
+  for (int u = 0; u < kDeqU; ++u) {
+    codes[u][0] = codes[u][1] = sc[u] = 0;
+    if (u >= n) continue;
+    if ((uint32_t)page[u] < (uint64_t)num_pages) {  // another one reads as zeros
+      const int kv = at[u] >= Hkv, h = kv ? at[u] - Hkv : at[u];
+      const uint8_t* slice = pool + (((int64_t)page[u] * Hkv + h) * 2 + kv) * SLICE;
+      const uint8_t* row = slice + tok * (D / 2) + chunk * 4;
+      codes[u][0] = __ldg(reinterpret_cast<const uint32_t*>(row));
+      codes[u][1] = __ldg(reinterpret_cast<const uint32_t*>(row + 8 * (D / 2)));
+      const uint8_t* s8 = slice + P * (D / 2) + (kv == 0 ? tok * NB + blk : blk * P + tok);
+      sc[u] = __ldg(s8) | (uint32_t)__ldg(s8 + (kv == 0 ? 8 * NB : 8)) << 8;
+    } else if (threadIdx.x == 0) {
+      set_device_error(err, kDevErrPageRange);
     }
   }
 #pragma unroll
   for (int u = 0; u < kDeqU; ++u) {
-    const int64_t s = s0 + u;
-    if (s >= n_slices) break;
-    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(sc[u] * 0x0101u));
-    uint4 o[2];
-    uint32_t* ow = reinterpret_cast<uint32_t*>(o);
+    if (u >= n) break;
+    const float two_e = kv_exp ? q4_pow2(__ldg(kv_exp + at[u])) : 1.f;
+    const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)sc[u]);
+    uint4* dst = reinterpret_cast<uint4*>(out + ((s0 + u) * P + tok) * D + chunk * 8);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t h[4];
-      e2m1x8_to_f16x2(half == 0 ? codes[u].x : codes[u].y, h);
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t sj = __byte_perm(s2, s2, j == 0 ? 0x1010 : 0x3232);
+      uint32_t h[4], o[4];
+      e2m1x8_to_f16x2(codes[u][j], h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = f16x2_to_f32x2(mul_f16x2(h[j], s2));
-        ow[4 * half + j] = pack_bf16x2(f.x * two_e[u], f.y * two_e[u]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = f16x2_to_f32x2(mul_f16x2(h[k], sj));
+        o[k] = pack_bf16x2(f.x * two_e, f.y * two_e);
       }
+      dst[j * D] = make_uint4(o[0], o[1], o[2], o[3]);  // 8 rows of D / 8 uint4
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + (s * P + tok) * D + blk * kQ4Block);
-    dst[0] = o[0];
-    dst[1] = o[1];
   }
 }
 
@@ -245,19 +288,24 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                               : (large ? kv_append_q4_kernel<64, kLargeU> : kv_append_q4_kernel<64, kSmallU>);
   return launch_kernel(kern, dim3((unsigned)grid, 2), dim3(kThreads), 0, stream, programmatic,
                        (const uint4*)k_new, (const uint4*)v_new, (uint8_t*)pool, kv_exp, append_indptr,
-                       page_indices, kv_indptr, last_page_len, batch, nnz_new, Hkv, num_pages, err);
+                       page_indices, kv_indptr, last_page_len, batch, nnz_new, Hkv,
+                       kThreads / (Hkv * (head_dim / kQ4Block)), kThreads % (Hkv * (head_dim / kQ4Block)),
+                       num_pages, err);
 }
 
 cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
-                                 int64_t num_pages, void* out, int* err, bool programmatic,
+                                 int64_t num_pages, void* out, int sms, int* err, bool programmatic,
                                  cudaStream_t stream) {
   if (n_pages <= 0) return cudaSuccess;
   const int64_t n_slices = n_pages * 2 * Hkv;
-  const int64_t grid = (n_slices + kDeqU - 1) / kDeqU;
+  const bool large = n_slices * head_dim >= (int64_t)sms * 2048 * kDeqSmallU;
+  const int per_cta = large ? kDeqLargeU : kDeqSmallU;
+  const int64_t grid = (n_slices + per_cta - 1) / per_cta;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  auto kern = head_dim == 128 ? kv_dequant_q4_kernel<128> : kv_dequant_q4_kernel<64>;
-  return launch_kernel(kern, dim3((unsigned)grid), dim3(kQ4Page * (head_dim / kQ4Block)), 0, stream,
+  auto kern = head_dim == 128 ? (large ? kv_dequant_q4_kernel<128, kDeqLargeU> : kv_dequant_q4_kernel<128, kDeqSmallU>)
+                              : (large ? kv_dequant_q4_kernel<64, kDeqLargeU> : kv_dequant_q4_kernel<64, kDeqSmallU>);
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(head_dim), 0, stream,
                        programmatic, (const uint8_t*)pool, kv_exp, ids, src, n_slices, Hkv, num_pages,
                        (uint16_t*)out, err);
 }

@@ -36,6 +36,7 @@
 // through its own ring with one bulk copy a page (K and V of a head are side by
 // side), over the ends of requests, and writes its own parts; nothing in a CTA
 // is synchronised.
+#include <cfloat>
 #include <climits>
 
 #include "launch.h"
@@ -60,8 +61,10 @@ struct Shape {
   static constexpr int PAIRS = (NT == 1 ? 2 : 3) * (D == 128 ? 1 : 2);  // ring, in pairs of pages
   static constexpr int STAGE = 2 * PAGE;
   static constexpr int TILES = D / 16;                 // 16-dim tiles of O^T
-  static constexpr int KSTEPS = D / 16;
-  static constexpr int OFF_BAR = kWarps * PAIRS * STAGE;
+  static constexpr int KWORDS = D / 32;                // code words of a thread per key row
+  static constexpr int Q_WARP = NT * KWORDS * 32 * 16; // Q^T fragments of a warp
+  static constexpr int OFF_Q = kWarps * PAIRS * STAGE;
+  static constexpr int OFF_BAR = OFF_Q + kWarps * Q_WARP;
   static constexpr int SMEM = OFF_BAR + kWarps * PAIRS * 8;
   static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory of the CTAs of an SM");
 };
@@ -103,6 +106,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   const int r = lane >> 2, c = lane & 3;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * S::PAIRS;
   uint8_t* ring = smem + warp * (S::PAIRS * S::STAGE);
+  uint4* q_frag = reinterpret_cast<uint4*>(smem + S::OFF_Q + warp * S::Q_WARP);
 
   // The next kernel may start its CTAs, but not before this one may read: the next
   // class's launch does not wait by itself.
@@ -186,7 +190,6 @@ attention_q4_kernel(const AttentionQ4Args a) {
   const int n_pages = pages_of(u);
 
   // Q^T fragments: rows n = 8 t + r, this thread's dims [c * D/4, (c + 1) * D/4)
-  uint32_t qf[NT][S::KSTEPS][2];
   float fs[NT][2];       // score factor of rows 8 t + 2 c, + 1
   int lim[NT][2];        // keys of those rows: [0, lim)
   int lim_min = INT_MAX;
@@ -219,10 +222,12 @@ attention_q4_kernel(const AttentionQ4Args a) {
     const int ex = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126) : 0;
     const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-    for (int j = 0; j < S::KSTEPS; ++j) {
-      qf[t][j][0] = pack_f16x2(x[4 * j] * down, x[4 * j + 1] * down);
-      qf[t][j][1] = pack_f16x2(x[4 * j + 2] * down, x[4 * j + 3] * down);
-    }
+    for (int w = 0; w < S::KWORDS; ++w)  // a lane reads what it writes here
+      q_frag[(t * S::KWORDS + w) * 32 + lane] =
+          make_uint4(pack_f16x2(x[8 * w] * down, x[8 * w + 1] * down),
+                     pack_f16x2(x[8 * w + 2] * down, x[8 * w + 3] * down),
+                     pack_f16x2(x[8 * w + 4] * down, x[8 * w + 5] * down),
+                     pack_f16x2(x[8 * w + 6] * down, x[8 * w + 7] * down));
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int m = 8 * t + 2 * c + b;
@@ -265,52 +270,57 @@ attention_q4_kernel(const AttentionQ4Args a) {
 
     // ---- S^T of the two pages
     float s[2][NT][4];
+    constexpr int W = S::KWORDS;
+    uint32_t kw[2][2][W];              // [page][key rows r, r + 8]
+    uint32_t ks[2][2][2];              // block scales of the thread's dims
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[p][t][e] = 0.f;
-      constexpr int W = D / 32;  // code words of a thread per key row
-      uint32_t w0[W], w1[W];
-      uint32_t sc0[2], sc1[2];   // block scales of the thread's dims, key rows r and r + 8
       const uint8_t* kb = stage + p * S::PAGE + k_off;
-      if constexpr (D == 128) {
-        const uint4 x0 = *reinterpret_cast<const uint4*>(kb);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(kb + 8 * 64);
-        w0[0] = x0.x; w0[1] = x0.y; w0[2] = x0.z; w0[3] = x0.w;
-        w1[0] = x1.x; w1[1] = x1.y; w1[2] = x1.z; w1[3] = x1.w;
-        const uint8_t* sb = stage + p * S::PAGE + 1024 + key_r * 8 + 2 * c;
-        const uint32_t y0 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb));
-        const uint32_t y1 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb + 64));
-        sc0[0] = __byte_perm(y0, y0, 0x1010); sc0[1] = __byte_perm(y0, y0, 0x3232);
-        sc1[0] = __byte_perm(y1, y1, 0x1010); sc1[1] = __byte_perm(y1, y1, 0x3232);
-      } else {
-        const uint2 x0 = *reinterpret_cast<const uint2*>(kb);
-        const uint2 x1 = *reinterpret_cast<const uint2*>(kb + 8 * 32);
-        w0[0] = x0.x; w0[1] = x0.y;
-        w1[0] = x1.x; w1[1] = x1.y;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kb + h * (8 * 64));
+          kw[p][h][0] = x.x; kw[p][h][1] = x.y; kw[p][h][2] = x.z; kw[p][h][3] = x.w;
+          const uint8_t* sb = stage + p * S::PAGE + 1024 + key_r * 8 + 2 * c;
+          const uint32_t y = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sb + 64 * h));
+          ks[p][h][0] = __byte_perm(y, y, 0x1010);
+          ks[p][h][1] = __byte_perm(y, y, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(kb + h * (8 * 32));
+          kw[p][h][0] = x.x; kw[p][h][1] = x.y;
+        }
+      }
+      if constexpr (D == 64) {
         // one block a thread: key rows r and r + 8 in one conversion
         const uint8_t* sb = stage + p * S::PAGE + 512 + key_r * 4 + c;
         const uint32_t y = e4m3x2_to_f16x2((uint16_t)(sb[0] | (sb[32] << 8)));
-        sc0[0] = sc0[1] = __byte_perm(y, y, 0x1010);
-        sc1[0] = sc1[1] = __byte_perm(y, y, 0x3232);
+        ks[p][0][0] = ks[p][0][1] = __byte_perm(y, y, 0x1010);
+        ks[p][1][0] = ks[p][1][1] = __byte_perm(y, y, 0x3232);
       }
+    }
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+    for (int w = 0; w < W; ++w) {
+      uint4 qw[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) qw[t] = q_frag[(t * W + w) * 32 + lane];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
         uint32_t h0[4], h1[4];
-        e2m1x8_to_f16x2(w0[w], h0);
-        e2m1x8_to_f16x2(w1[w], h1);
-        const uint32_t z0 = sc0[(2 * w) / W], z1 = sc1[(2 * w) / W];
+        e2m1x8_to_f16x2(kw[p][0][w], h0);
+        e2m1x8_to_f16x2(kw[p][1][w], h1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          h0[i] = mul_f16x2(h0[i], z0);
-          h1[i] = mul_f16x2(h1[i], z1);
+          h0[i] = mul_f16x2(h0[i], ks[p][0][(2 * w) / W]);
+          h1[i] = mul_f16x2(h1[i], ks[p][1][(2 * w) / W]);
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          mma_f16(s[p][t], h0[0], h1[0], h0[1], h1[1], qf[t][2 * w][0], qf[t][2 * w][1]);
-          mma_f16(s[p][t], h0[2], h1[2], h0[3], h1[3], qf[t][2 * w + 1][0], qf[t][2 * w + 1][1]);
+          mma_f16(s[p][t], h0[0], h1[0], h0[1], h1[1], qw[t].x, qw[t].y);
+          mma_f16(s[p][t], h0[2], h1[2], h0[3], h1[3], qw[t].z, qw[t].w);
         }
       }
     }
@@ -490,14 +500,14 @@ attention_q4_kernel(const AttentionQ4Args a) {
 // (GB300, decode of 128 requests, 12 heads, 15 parts on average and 47 at most:
 // 16 us with one, 11 with four; 160 tokens, 32 heads, 6 parts: 7 us and 12).
 constexpr int kMergeWarps = 4;
-constexpr int kMergeLoads = 4;
+constexpr int kMergeLoads = 6;
 constexpr int kMergeWideParts = 10;  // parts of a token, on average, from which four warps share it
 
 template <int D, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeArgs a) {
   constexpr int EPL = D / 32;  // dims of a lane
   __shared__ float s_acc[W > 1 ? W : 1][W > 1 ? D : 1];
-  __shared__ float s_sum[W];
+  __shared__ float s_sum[W], s_max[W];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const MergeItem it = a.items[blockIdx.x];
   const int hq = blockIdx.y * (kMergeWarps / W) + warp / W;
@@ -507,11 +517,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeA
   const float* part = a.part_o + ((int64_t)it.part_begin * a.Hq + hq) * D + lane * EPL;
   const int64_t stride = (int64_t)a.Hq * D;
   grid_dep_wait();  // the parts come from the kernel launched before
-  float M = -INFINITY;
-  for (int p = lane; p < it.n_parts; p += 32) M = fmaxf(M, lse[(int64_t)p * a.Hq]);
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, m));
-  float acc[EPL], sum = 0.f;
+  // a share's weights are relative to its own maximum, M, raised as it goes
+  float acc[EPL], sum = 0.f, M = -FLT_MAX;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
   for (int p0 = share; p0 < it.n_parts; p0 += W * kMergeLoads) {
@@ -532,6 +539,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeA
         }
       }
     }
+    float raised = M;
+#pragma unroll
+    for (int i = 0; i < kMergeLoads; ++i) raised = fmaxf(raised, w[i]);
+    const float alpha = ex2_approx(M - raised);
+    M = raised;
+    sum *= alpha;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] *= alpha;
 #pragma unroll
     for (int i = 0; i < kMergeLoads; ++i) {
       const float x = ex2_approx(w[i] - M);
@@ -543,14 +558,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_q4_kernel(const MergeA
   if constexpr (W > 1) {
 #pragma unroll
     for (int e = 0; e < EPL; ++e) s_acc[warp][lane * EPL + e] = acc[e];
-    if (lane == 0) s_sum[warp] = sum;
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_max[warp] = M;
+    }
     __syncthreads();
     if (warp > 0) return;
+    const float M0 = M;
+#pragma unroll
+    for (int w = 1; w < W; ++w) M = fmaxf(M, s_max[w]);
+    const float alpha = ex2_approx(M0 - M);
+    sum *= alpha;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) acc[e] *= alpha;
 #pragma unroll
     for (int w = 1; w < W; ++w) {
-      sum += s_sum[w];
+      const float x = ex2_approx(s_max[w] - M);
+      sum = fmaf(x, s_sum[w], sum);
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) acc[e] += s_acc[w][lane * EPL + e];
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(x, s_acc[w][lane * EPL + e], acc[e]);
     }
   }
   const float inv = 1.f / sum;

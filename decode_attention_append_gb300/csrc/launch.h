@@ -201,7 +201,7 @@ cudaError_t launch_kv_append_q4(const void* k_new, const void* v_new, void* pool
                                 bool programmatic, cudaStream_t stream);
 cudaError_t launch_kv_dequant_q4(const void* pool, const int32_t* kv_exp, const int32_t* ids,
                                  const int32_t* src, int64_t n_pages, int Hkv, int head_dim,
-                                 int64_t num_pages, void* out, int* err, bool programmatic,
+                                 int64_t num_pages, void* out, int sms, int* err, bool programmatic,
                                  cudaStream_t stream);
 
 // Attention over the 4-bit pages (decode_q4.cu); n_ranges per class, in order.

@@ -59,10 +59,17 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t h) {
   return f;
 }
 
-// Two floats -> e4m3 bytes, nearest, ties to even, cut at 448 (lo in the low byte).
-__device__ __forceinline__ uint16_t f32x2_to_e4m3x2(float lo, float hi) {
+// An fp16 pair -> e4m3 bytes, nearest, ties to even, cut at 448 (low half in the low byte).
+__device__ __forceinline__ uint16_t f16x2_to_e4m3x2(uint32_t h) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+
+// 1 / x, off by 2^-23 (relative) at most.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 

@@ -16,9 +16,8 @@
 // Bound: 8 bytes per page id and 12 per new row; a launch and three dependent
 // loads for all but the longest batches.  Each CTA does the sums over the whole
 // batch itself (a few KB from L2) instead of waiting for another kernel, then
-// takes its share of the pages and rows; the CTA that finishes last (a ticket)
-// writes the lengths, page counts and free count back, when no other CTA still
-// reads them.  Nothing is changed when the step cannot be made (a bad or doubled
+// takes its share of the pages and rows; the CTA that is the last to have read the
+// batch (a ticket) writes the lengths, page counts and free count back.  Nothing is changed when the step cannot be made (a bad or doubled
 // slot, lengths past a row, more pages or rows than the buffers hold or the pool
 // has): the tables then describe an empty step and the error word says why.
 #include <algorithm>
@@ -122,8 +121,8 @@ __device__ __forceinline__ int find_owner(const int* s, int n, int i) {
 // slot are those it holds, and there are no rows.  Returns the error code that
 // every CTA works out alike (0: none).
 template <bool RELEASE, bool W>
-__device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l) {
-  const int free_count = a.counters[0];
+__device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l, int& free_count) {
+  free_count = a.counters[0];
   for (int i = threadIdx.x; i < l.words; i += kThreads) s.seen[i] = 0;
   __syncthreads();
   Sums<W> sum{0, 0, 0};
@@ -174,20 +173,28 @@ __device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l
     s.qo[a.batch] = (int)sum.rows;
     s.tp[a.batch] = (int)sum.take;
   }
+  bad |= free_count < 0 || free_count > a.num_pages;
   if (__syncthreads_or(bad)) return kDevErrShape;
-  if (free_count < 0 || free_count > a.num_pages) return kDevErrShape;
   if (RELEASE) return sum.pages > a.num_pages - free_count ? kDevErrShape : 0;
   if (sum.pages > a.page_capacity || sum.rows > a.row_capacity) return kDevErrShape;
   return sum.take > free_count ? kDevErrNoPages : 0;
 }
 
-// True in every thread of the CTA that reaches this point last.
-__device__ __forceinline__ bool last_cta(int* ticket) {
+// Thread 0, once the CTA has read all it needs of the lengths and counts (each
+// value is used before read_batch's last barrier): its number among the CTAs.  The
+// answer is asked for at the end only, so the atomic runs beside the page work.
+__device__ __forceinline__ int take_ticket(int* ticket) {
+  if (threadIdx.x != 0 || gridDim.x == 1) return 0;
+  __threadfence();
+  return atomicAdd(ticket, 1);
+}
+
+// True in every thread of the CTA whose ticket is the last: no CTA reads the lengths
+// and counts any more.
+__device__ __forceinline__ bool is_last(int ticket) {
   __shared__ int s_last;
-  __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    s_last = gridDim.x == 1 || atomicAdd(ticket, 1) == (int)gridDim.x - 1;
+    s_last = ticket == (int)gridDim.x - 1;
     __threadfence();
   }
   __syncthreads();
@@ -201,7 +208,8 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
   const Smem s(smem, l);
   grid_dep_launch();
   grid_dep_wait();
-  const int err = read_batch<false, W>(a, s, l);
+  int free_count;
+  const int err = read_batch<false, W>(a, s, l, free_count);
   const int n = a.batch;
   if (err != 0) {
     if (blockIdx.x == 0) {
@@ -214,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
     }
     return;
   }
-  const int free_count = a.counters[0];
+  const int ticket = take_ticket(a.counters + 1);
   auto fresh_page = [&](int r, int p) {
     return __ldg(a.free_pages + (free_count - 1 - (s.tp[r] + p - s.held[r])));
   };
@@ -234,26 +242,40 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
   // pages also enter their row of the block table
   const int n_pages = s.kp[n], n_rows = s.qo[n];
   const int stride = (int)gridDim.x * kThreads;
+  const bool wide_store = reinterpret_cast<uintptr_t>(a.page_indices) % 16 == 0;
   for (int64_t p0 = 4ll * (blockIdx.x * kThreads + threadIdx.x); p0 < n_pages; p0 += 4ll * stride) {
     int r = find_owner(s.kp, n, (int)p0);
-    int id[4], row_r[4], row_p[4];
+    int id[4];
+    const int p = (int)p0 - s.kp[r];
+    if (p0 + 4 <= s.kp[r + 1] && p + 4 <= s.held[r]) {  // one request's, all held
+      const int* row = a.block_table + (int64_t)s.slot[r] * a.max_pages + p;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = p0 + u;
-      row_r[u] = -1;
-      if (i < n_pages) {
-        while (i >= s.kp[r + 1]) ++r;
-        const int p = (int)i - s.kp[r];
-        const bool old = p < s.held[r];
-        id[u] = old ? a.block_table[(int64_t)s.slot[r] * a.max_pages + p] : fresh_page(r, p);
-        row_r[u] = old ? -1 : r;
-        row_p[u] = p;
+      for (int u = 0; u < 4; ++u) id[u] = row[u];
+    } else {
+      int row_r[4], row_p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t i = p0 + u;
+        row_r[u] = -1;
+        id[u] = 0;
+        if (i < n_pages) {
+          while (i >= s.kp[r + 1]) ++r;
+          row_p[u] = (int)i - s.kp[r];
+          const bool old = row_p[u] < s.held[r];
+          id[u] = old ? a.block_table[(int64_t)s.slot[r] * a.max_pages + row_p[u]] : fresh_page(r, row_p[u]);
+          row_r[u] = old ? -1 : r;
+        }
       }
-    }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (p0 + u < n_pages) a.page_indices[p0 + u] = id[u];
-      if (row_r[u] >= 0) a.block_table[(int64_t)s.slot[row_r[u]] * a.max_pages + row_p[u]] = id[u];
+      for (int u = 0; u < 4; ++u)
+        if (row_r[u] >= 0) a.block_table[(int64_t)s.slot[row_r[u]] * a.max_pages + row_p[u]] = id[u];
+    }
+    if (wide_store && p0 + 4 <= n_pages) {
+      *reinterpret_cast<int4*>(a.page_indices + p0) = make_int4(id[0], id[1], id[2], id[3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p0 + u < n_pages) a.page_indices[p0 + u] = id[u];
     }
   }
   if (a.slot_map || a.positions) {
@@ -268,7 +290,7 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
       }
     }
   }
-  if (!last_cta(a.counters + 1)) return;
+  if (!is_last(ticket)) return;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int pages = s.kp[i + 1] - s.kp[i];
     if (pages > s.held[i]) a.held[s.slot[i]] = pages;
@@ -290,19 +312,21 @@ __global__ void __launch_bounds__(kThreads) release_pages_kernel(const StepTable
   const Smem s(smem, l);
   grid_dep_launch();
   grid_dep_wait();
-  const int err = read_batch<true, W>(a, s, l);
+  int free_count;
+  const int err = read_batch<true, W>(a, s, l, free_count);
   if (err != 0) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_device_error(a.err, err);
     return;
   }
-  const int n = a.batch, n_pages = s.kp[n], free_count = a.counters[0];
+  const int ticket = take_ticket(a.counters + 1);
+  const int n = a.batch, n_pages = s.kp[n];
   const int stride = (int)gridDim.x * kThreads;
   for (int64_t i = blockIdx.x * kThreads + threadIdx.x; i < n_pages; i += stride) {
     const int r = find_owner(s.kp, n, (int)i);
     a.free_pages[free_count + n_pages - 1 - i] =
         a.block_table[(int64_t)s.slot[r] * a.max_pages + ((int)i - s.kp[r])];
   }
-  if (!last_cta(a.counters + 1)) return;
+  if (!is_last(ticket)) return;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     a.held[s.slot[i]] = 0;
     a.seq_len[s.slot[i]] = 0;

@@ -29,13 +29,24 @@
 // is raised only when a score passes it by 8) P is at most 2^15.  Sums, maxima
 // and O are fp32.
 //
-// Bound: HBM.  A (page, head) is 18 d bytes; at the measured 6.7 TB/s an SM gets
-// one of d = 128 every 52 ns (about 99 clocks), in which it can issue about 400
-// warp instructions.  Warps work alone: each streams a range of pages of its own
-// (the units of one kv head, cut so that every resident warp has the same cost)
-// through its own ring with one bulk copy a page (K and V of a head are side by
-// side), over the ends of requests, and writes its own parts; nothing in a CTA
-// is synchronised.
+// Bound: HBM for 8 rows, instructions for more.  A (page, head) is 18 d bytes; at
+// the measured 6.7 TB/s an SM gets one of d = 128 every 52 ns (about 99 clocks), in
+// which it can issue 400 warp instructions.  A page takes about 290 of them with 8
+// rows and 310 with 16: 64 conversions and 64 products of the codes, 16 mma for
+// every 8 rows, the rest loads, scales, exponents and the ring.  Measured (GB300, a
+// page on an SM): 59 ns with 8 rows (32 requests of 0.5k to 4k tokens, 32 heads on 32:
+// 56 us, 6.0 TB/s), 94 with 16 (128 of 1k to 32k, 12 heads on 1: 48 us, 3.8 TB/s) and
+// 144 with 24 (verify of 5 tokens, 32 heads on 8: 39.5 us, 2.4 TB/s); issue slots used
+// 65, 47 and 37 %.  The loads alone take 49, 34 and 26 us.
+//
+// Warps work alone: each streams a range of pages of its own (the units of one kv
+// head, cut so that every resident warp has the same cost) through its own ring with
+// one bulk copy a page (K and V of a head are side by side), over the ends of
+// requests, and writes its own parts; nothing in a CTA is synchronised.  Measured and
+// not faster: two warps to a range that share its pages and split the dims, so that
+// 16 and 24 rows have 16 warps an SM, too (58 and 51 us: 460 instructions a page); 12
+// warps of 168 registers for 16 rows (51 us); tcgen05 with the codes converted into
+// TMEM and shared memory (79 us for 48).
 #include <cfloat>
 #include <climits>
 
@@ -57,8 +68,10 @@ template <int D, int NT>
 struct Shape {
   static constexpr int SLICE = q4_slice_bytes(D);
   static constexpr int PAGE = 2 * SLICE;               // K and V of one (page, head)
-  static constexpr int CTAS = NT == 1 ? 4 : 2;  // meant to share an SM
-  static constexpr int PAIRS = (NT == 1 ? 2 : 3) * (D == 128 ? 1 : 2);  // ring, in pairs of pages
+  static constexpr int CTAS = NT == 1 ? 4 : 2;         // meant to share an SM: 128 and 255 registers
+  // Ring, in pairs of pages.  Deeper ones measured slower: at the start every warp's
+  // further pages queue in front of other warps' first ones.
+  static constexpr int PAIRS = (NT == 1 ? 2 : 3) * (D == 128 ? 1 : 2);
   static constexpr int STAGE = 2 * PAGE;
   static constexpr int TILES = D / 16;                 // 16-dim tiles of O^T
   static constexpr int KWORDS = D / 32;                // code words of a thread per key row
@@ -492,13 +505,13 @@ attention_q4_kernel(const AttentionQ4Args a) {
   if (blockIdx.x == 0) grid_dep_wait();
 }
 
-// softmax_merge of the parts of a (token, query head): M = max lse, weights
-// 2^(lse - M), their sum and the weighted sum of the parts (lse in the log2
-// domain).  Bound: latency (a load of lse, then one of the parts for every
-// kMergeLoads of them).  W warps share a row: one where rows have few parts, so
-// that a wave of CTAs holds as many rows as it can; four where they have many
-// (GB300, decode of 128 requests, 12 heads, 15 parts on average and 47 at most:
-// 16 us with one, 11 with four; 160 tokens, 32 heads, 6 parts: 7 us and 12).
+// softmax_merge of the parts of a (token, query head): weights 2^(lse - M) with M the
+// running maximum of lse, their sum and the weighted sum of the parts (lse in the
+// log2 domain).  Bound: latency (a part and its lse are loaded together, kMergeLoads
+// parts at a time).  W warps share a row: one where rows have few parts, so that a
+// wave of CTAs holds as many rows as it can; four where they have many (GB300, decode
+// of 128 requests, 12 heads, 15 parts on average and 47 at most: 12.5 us with one, 7
+// with four; 160 tokens, 32 heads, 6 parts: 7 us and 10).
 constexpr int kMergeWarps = 4;
 constexpr int kMergeLoads = 6;
 constexpr int kMergeWideParts = 10;  // parts of a token, on average, from which four warps share it

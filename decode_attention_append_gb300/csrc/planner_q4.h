@@ -21,10 +21,11 @@
 namespace daa {
 
 // GB300, 8 kv heads, d = 128, 32 requests of 2500 keys, 4 and 8 heads a kv head: 96
-// rows 140 us from the 4-bit pages and 167 by way of bf16, 128 rows 206 and 172.
+// rows 140 us from the 4-bit pages and 157 to 164 by way of bf16, 128 rows 206 and 161
+// to 168.
 constexpr int kQ4NativeRows = 96;
 // Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
-// page on an SM: 62, 90 and 153 ns with 8, 16 and 24 rows).  Where all units of 8
+// page on an SM: 59, 94 and 144 ns with 8, 16 and 24 rows).  Where all units of 8
 // rows find a free warp, smaller ones end sooner.
 constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
 constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages

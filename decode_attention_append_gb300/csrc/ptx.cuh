@@ -19,7 +19,6 @@ enum DeviceError : int {
   kDevErrPageRange = 1,     // page id outside [0, num_pages)
   kDevErrBarrierTimeout = 2,  // an mbarrier wait ran out of polls
   kDevErrShape = 3,         // a request's lengths are inconsistent
-  kDevErrNoPages = 4,       // a step needs more pages than the pool has free
 };
 
 __device__ __forceinline__ void set_device_error(int* err, int code) {

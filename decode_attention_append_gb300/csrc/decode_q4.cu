@@ -31,13 +31,13 @@
 //
 // Bound: HBM for 8 rows, instructions for more.  A (page, head) is 18 d bytes; at
 // the measured 6.7 TB/s an SM gets one of d = 128 every 52 ns (about 99 clocks), in
-// which it can issue 400 warp instructions.  A page takes about 290 of them with 8
-// rows and 310 with 16: 64 conversions and 64 products of the codes, 16 mma for
+// which it can issue 400 warp instructions.  A page takes 279 of them with 8 rows, 313
+// with 16 and 393 with 24: 64 conversions and 64 products of the codes, 16 mma for
 // every 8 rows, the rest loads, scales, exponents and the ring.  Measured (GB300, a
-// page on an SM): 59 ns with 8 rows (32 requests of 0.5k to 4k tokens, 32 heads on 32:
-// 56 us, 6.0 TB/s), 94 with 16 (128 of 1k to 32k, 12 heads on 1: 48 us, 3.8 TB/s) and
-// 144 with 24 (verify of 5 tokens, 32 heads on 8: 39.5 us, 2.4 TB/s); issue slots used
-// 65, 47 and 37 %.  The loads alone take 49, 34 and 26 us.
+// page on an SM): 60 ns with 8 rows (32 requests of 0.5k to 4k tokens, 32 heads on 32:
+// 56 us, 5.7 TB/s), 95 with 16 (128 of 1k to 32k, 12 heads on 1: 48 us, 3.7 TB/s) and
+// 140 with 24 (verify of 5 tokens, 32 heads on 8: 39.5 us, 2.5 TB/s); issue slots used
+// 63, 47 and 41 %.  The loads alone take 49, 34 and 26 us.
 //
 // Warps work alone: each streams a range of pages of its own (the units of one kv
 // head, cut so that every resident warp has the same cost) through its own ring with

@@ -25,7 +25,7 @@ namespace daa {
 // to 168.
 constexpr int kQ4NativeRows = 96;
 // Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
-// page on an SM: 59, 94 and 144 ns with 8, 16 and 24 rows).  Where all units of 8
+// page on an SM: 60, 95 and 140 ns with 8, 16 and 24 rows).  Where all units of 8
 // rows find a free warp, smaller ones end sooner.
 constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
 constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages

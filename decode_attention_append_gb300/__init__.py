@@ -980,7 +980,8 @@ def kv_dequant_q4(kv_pages, page_ids, kv_exp=None, out=None, stream=None):
     ids, n = _addr(page_ids, "page_ids", torch.int32, dev), page_ids.numel()
     shape = (n, 2, dims.num_kv_heads, dims.page_size, dims.head_dim)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+        with _use_stream(stream):
+            out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
     o = _addr(out, "out", torch.bfloat16, dev)
     if out.shape != shape:
         raise ValueError("out must be [n_pages, 2, Hkv, 16, head_dim]")
@@ -1014,6 +1015,11 @@ class BatchAttentionQ4:
         self.dev, _, _, self.dims = _q4_pool(kv_pages, kv_exp, num_qo_heads)
         for n in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len"):
             _addr(getattr(table, n), n, torch.int32, self.dev)
+        batch = len(table.h_qo_indptr) - 1
+        if len(table.h_kv_indptr) != batch + 1 or len(table.h_last_page_len) != batch or \
+                table.page_indices.numel() < int(table.h_kv_indptr[-1]):
+            raise ValueError("the table's host arrays have batch + 1, batch + 1 and batch entries, and "
+                             "page_indices has an entry for every page of them")
         self.causal = int(bool(causal))
         self.sm_scale = float(sm_scale if sm_scale is not None else 1.0 / float(self.dims.head_dim) ** 0.5)
         d = self.dims
@@ -1045,7 +1051,8 @@ class BatchAttentionQ4:
         if q.shape != self.shape:
             raise ValueError("q must be [nnz_qo, Hq, head_dim] of the planned table")
         if out is None:
-            out = torch.empty_like(q)
+            with _use_stream(stream):
+                out = torch.empty_like(q)
         po = _addr(out, "out", bf16, dev)
         if out.shape != self.shape:
             raise ValueError("out must have the shape of q")

@@ -615,3 +615,76 @@ def test_append_after_other_kernels(daa):
         host = np.zeros((n, hkv, 2, 9 * d), np.uint8)
         ref.append(host, x.double().cpu().numpy(), x.double().cpu().numpy(), t, None)
         assert np.array_equal(r.double().cpu().numpy(), ref.decode_pages(host[t["page_indices"]], d, None))
+
+
+@pytest.mark.parametrize("e", [0, -3])
+def test_append_every_block_maximum(daa, e):
+    """Every finite bf16 as a block's largest value, the rest of the block on and
+    beside the midpoints between codes: bit by bit as the exact quotients round."""
+    rng = np.random.default_rng(30)
+    top = torch.arange(0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)  # 0 .. the largest
+    rows = -(-len(top) // 8)
+    top = torch.cat([top, top[:8 * rows - len(top)]])
+    t, n = ref.make_table(rng, [0], [rows], spare=0)
+    g = {x: _dev(y) for x, y in t.items()}
+    scale = ref.E4M3[ref.quantise(top.double().numpy()[:, None].repeat(16, 1), np.full(len(top), e))[1][:, 0]]
+    mid = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * scale[:, None] * 2.0 ** e  # 7 bits at most: exact where normal
+    on = torch.from_numpy(np.clip(mid, 0, 3e38)).bfloat16()
+    bits = on.view(torch.int16)
+    block = torch.cat([top[:, None], on, (bits + 1).view(torch.bfloat16), (bits - 1).clamp(min=0).view(torch.bfloat16)[:, :1]], 1)
+    block = torch.where(block.abs() > top[:, None].abs(), top[:, None], block)
+    block = block * torch.from_numpy(rng.choice([-1.0, 1.0], (len(top), 16))).bfloat16()
+    k = block.reshape(rows, 1, 128)
+    exps = np.full((2, 1), e, np.int32)
+    pool = np.zeros((n, 1, 2, 9 * 128), np.uint8)
+    gpool = _dev(pool)
+    daa.kv_append_q4(k.to(DEV), k.to(DEV), gpool, g["qo_indptr"], g["page_indices"], g["kv_indptr"], g["last_page_len"],
+                     kv_exp=_dev(exps))
+    ref.append(pool, k.double().numpy(), k.double().numpy(), t, exps)
+    assert np.array_equal(gpool.cpu().numpy(), pool)
+
+
+def test_append_many_requests_and_offset_rows(daa):
+    """More requests than a CTA keeps in shared memory; K on a 16-byte boundary that is none of 32."""
+    rng = np.random.default_rng(31)
+    hkv, d = 2, 64
+    t, n = ref.make_table(rng, rng.integers(0, 20, 1400), rng.integers(0, 3, 1400))
+    rows = int(t["qo_indptr"][-1])
+    k, v = _bf16(rng, (rows, hkv, d)), _bf16(rng, (rows, hkv, d))
+    room = torch.zeros(k.numel() + 8, dtype=torch.bfloat16, device=DEV)
+    kd = room[8:].view(rows, hkv, d)
+    kd.copy_(k)
+    assert kd.data_ptr() % 32 == 16
+    g = {x: _dev(y) for x, y in t.items()}
+    gpool = daa.new_q4_pool(n, hkv, d)
+    daa.kv_append_q4(kd, v.to(DEV), gpool, g["qo_indptr"], g["page_indices"], g["kv_indptr"], g["last_page_len"])
+    pool = np.zeros((n, hkv, 2, 9 * d), np.uint8)
+    ref.append(pool, k.double().numpy(), v.double().numpy(), t, None)
+    assert np.array_equal(gpool.cpu().numpy(), pool)
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+def test_step_table_into_a_buffer_at_any_place(daa, off):
+    rng = np.random.default_rng(32)
+    lens = {i: int(x) for i, x in enumerate(rng.integers(0, 700, 40))}
+    st = _state(rng, 40, 60, 2400, lens)
+    pool = _device_pool(daa, st, 2400)
+    new = rng.integers(0, 60, 40)
+    want = ref.step_table(st, list(range(40)), new, True)
+    pages = len(want["page_indices"])
+    out = _outs(40, pages + 9, len(want["positions"]))
+    buf = out["page_indices"]
+    out["page_indices"] = buf[off:off + pages]
+    pool.build(_dev(np.arange(40, dtype=np.int32)), _dev(new.astype(np.int32)), advance=True, **out)
+    for name, w in want.items():
+        assert np.array_equal(out[name].cpu().numpy(), w), name
+    assert (buf[:off] == -7).all() and (buf[off + pages:] == -7).all()
+    _same_state(pool, st)
+
+
+def test_attention_refuses_a_short_page_list(daa):
+    t, n = ref.make_table(np.random.default_rng(33), [40, 3], [1, 1])
+    table = daa.PageTable.from_host(*(t[x] for x in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len")), DEV)
+    table.page_indices = table.page_indices[:-1]
+    with pytest.raises(ValueError):
+        daa.BatchAttentionQ4(table, 2, daa.new_q4_pool(n, 2, 64))

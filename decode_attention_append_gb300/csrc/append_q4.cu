@@ -17,11 +17,11 @@
 // is rounded to e4m3 the same way: 6 times a midpoint of two e4m3 values (5
 // significant bits) has at most 7.
 //
-// Bound: HBM (2 + 9/16 bytes a value), which the 11 instructions a value (widen,
-// scale, the maximum taken on packed bits, two conversions a pair, addresses) keep it
-// from reaching: 36,760 tokens of 8 heads of 128 dims 37 us on GB300, 5.2 TB/s, 60 %
-// of the issue slots; without the stores 35.  A step of 128 single tokens is latency:
-// 5.4 us with the launch.
+// Bound: HBM (2 + 9/16 bytes a value) and the 11 instructions a value (widen, scale,
+// the maximum taken on packed bits, two conversions a pair, addresses): 36,760 tokens
+// of 8 heads of 128 dims 37 us on GB300, launch and ramp among them, 5.2 TB/s, 60 % of
+// the issue slots; without the stores 35, without the arithmetic 36.  A step of 128
+// single tokens is latency: 5.4 us with the launch.
 //
 // The read-back moves 9/16 + 2 bytes a value at 6.4 TB/s: 8,192 pages of 8
 // heads of 128 dims in 106.8 us (with a thread's 16 dims stored side by side, half a
@@ -37,7 +37,8 @@ constexpr int kThreads = 128;
 // Blocks of 16 dims per thread in flight: two for small appends (a CTA's chain of
 // loads is what they wait for, so they are cut fine: a step of 128 tokens 8.3 us with
 // its read-back, 10.3 with six), six once the CTAs fill the GPU more than once
-// (36,760 tokens, with the read-back 72.2 us; with two 74.2, with eight 75.5).
+// (36,760 tokens, with the read-back 70.7 us; with two 74.2, with eight 75.5; CTAs that
+// stay and load the next chunk while they quantise one: 72.4).
 constexpr int kSmallU = 2, kLargeU = 6;
 constexpr int kMaxBatch = 1023;                 // requests whose indptr a CTA holds
 
@@ -107,7 +108,7 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
   constexpr int kMaxRows = kAppendSpan / NB + 2;  // rows a CTA touches (a row has NB blocks or more)
   __shared__ int64_t s_page[kMaxRows];  // page * Hkv of the row, -1: not written
   __shared__ int s_slot[kMaxRows];
-  __shared__ int s_indptr[kMaxBatch + 1];
+  __shared__ int s_indptr[kMaxBatch + 1], s_kv[kMaxBatch + 1], s_last[kMaxBatch + 1];
   grid_dep_launch();
   grid_dep_wait();
   const int kv = blockIdx.y;
@@ -137,13 +138,19 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
       }
     }
   }
-  // the search for a row's request is a chain of loads: in shared memory where the
-  // array fits, so that a small append waits for memory three times and not ten
-  const int32_t* indptr = append_indptr;
+  // the search for a row's request and its lengths are a chain of loads: in shared
+  // memory where the arrays fit, so that a CTA waits for memory twice and not ten times
+  const int32_t *indptr = append_indptr, *kv_begin = kv_indptr, *last_lens = last_page_len;
   if (batch <= kMaxBatch) {
-    for (int t = threadIdx.x; t <= batch; t += kThreads) s_indptr[t] = __ldg(append_indptr + t);
+    for (int t = threadIdx.x; t <= batch; t += kThreads) {
+      s_indptr[t] = __ldg(append_indptr + t);
+      s_kv[t] = __ldg(kv_indptr + t);
+      s_last[t] = t < batch ? __ldg(last_page_len + t) : 0;
+    }
     __syncthreads();
     indptr = s_indptr;
+    kv_begin = s_kv;
+    last_lens = s_last;
   }
   for (int t = threadIdx.x; t < nrows; t += kThreads) {
     const int row = row0 + t;
@@ -153,8 +160,8 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
       if (indptr[mid] <= row) lo = mid; else hi = mid - 1;
     }
     const int a0 = indptr[lo], a1 = indptr[lo + 1];
-    const int p0 = __ldg(kv_indptr + lo), np = __ldg(kv_indptr + lo + 1) - p0;
-    const int last_len = np > 0 ? __ldg(last_page_len + lo) : 0;
+    const int p0 = kv_begin[lo], np = kv_begin[lo + 1] - p0;
+    const int last_len = np > 0 ? last_lens[lo] : 0;
     const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * P + last_len : 0;
     int64_t at = -1;
     int slot = 0;

@@ -5,8 +5,9 @@
 // the K/V bytes.  A request whose packed (token, query head) rows are more than
 // kQ4NativeRows reads every key many times, so its pages are turned into bf16
 // once, in the workspace, and it runs on the bf16 kernels (their plan, on the
-// batch of these requests alone); the others are read from the 4-bit pages by
-// the attention_q4 kernel.
+// batch of these requests alone), unless there are so few of them that those
+// kernels would leave most of the GPU idle (few_chunks_q4); the others are read
+// from the 4-bit pages by the attention_q4 kernel.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -30,6 +31,20 @@ constexpr int kQ4NativeRows = 96;
 constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
 constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages
 constexpr int kQ4MinPages = 4;    // pages of a range at least
+
+// Whether a batch's long requests are better read from the 4-bit pages, too: few_chunks
+// of `warps` (units of kQ4UnitRows rows, times kv heads) over up to `keys` keys.  The
+// bf16 kernels give a long chunk's rows to few SMs, each of which walks all keys (11 to
+// 13 ns a key); 24-row units read the pages again for every 24 rows, but on every SM.
+// Requests of two 128-row tiles at most (`split`) have their keys cut there, too.
+// Measured on GB300 at 274 points (rows 128 to 2048, keys 100 to 16000, 1 to 32 kv
+// heads, 1 to 8 chunks, with and without decode beside them): taken at 170 of them, 1.7
+// times as fast on average there, 7.6 at best (252 rows, 1 kv head, 16000 keys: 27 us and
+// 205) and 0.9 at worst (2048 rows, 2 kv heads, 1256 keys: 32 and 29).
+inline bool few_chunks_q4(int64_t warps, int64_t keys, bool split, int sms) {
+  if (5 * warps <= 3 * (int64_t)sms) return !split || warps * keys <= 150000;
+  return !split && warps <= 2 * (int64_t)sms - 160000 / keys;
+}
 
 inline int q4_class(int rows) { return (rows - 1) / 8; }  // up to 8, 16, 24 rows
 // Warps of the class's kernel on an SM (its shared memory and registers).
@@ -115,7 +130,8 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
   };
   thread_local std::vector<Stream> streams[kQ4Classes];
   for (auto& v : streams) v.clear();
-  int64_t small_pages = 0;  // pages that units of few rows would read
+  int64_t chunk_warps = 0, chunk_keys = 1;  // of requests past kQ4NativeRows
+  bool chunk_split = false;
   for (int r = 0; r < batch; ++r) {
     const int64_t nq = (int64_t)qo[r + 1] - qo[r];
     const int64_t np = (int64_t)kv[r + 1] - kv[r];
@@ -124,6 +140,16 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     const int64_t kv_len = np > 0 ? (np - 1) * P + last[r] : 0;
     if (nq > kv_len || kv_len > INT32_MAX / 2) return DAA_ERR_SHAPE;
     if (nq * g > kQ4NativeRows) {
+      chunk_warps += units_of(nq, kQ4UnitRows) * d.num_kv_heads;
+      chunk_keys = std::max(chunk_keys, kv_len);
+      chunk_split |= nq <= 2 * (kPrefillTileRows / g);
+    }
+  }
+  const int64_t native_rows = few_chunks_q4(chunk_warps, chunk_keys, chunk_split, sms) ? INT64_MAX : kQ4NativeRows;
+  int64_t small_pages = 0;  // pages that units of few rows would read
+  for (int r = 0; r < batch; ++r) {
+    const int64_t nq = qo[r + 1] - qo[r], np = kv[r + 1] - kv[r];
+    if (nq * g > native_rows) {
       if ((int64_t)pl.src.size() + np > INT32_MAX / (2 * d.num_kv_heads)) return DAA_ERR_UNSUPPORTED;
       pl.req.push_back(r);
       pl.sub_qo.push_back(pl.sub_qo.back() + (int32_t)nq);
@@ -138,7 +164,7 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
   const int unit_rows = small_pages <= free_warps * kQ4MinPages ? kQ4SmallUnitRows : kQ4UnitRows;
   for (int r = 0; r < batch; ++r) {
     const int nq = qo[r + 1] - qo[r];
-    if (nq == 0 || nq * g > kQ4NativeRows) continue;
+    if (nq == 0 || (int64_t)nq * g > native_rows) continue;
     const int n_units = (int)units_of(nq, unit_rows);
     for (int i = 0, t0 = 0; i < n_units; ++i) {  // as equal as they come
       const int n = (nq - t0 + n_units - i - 1) / (n_units - i);

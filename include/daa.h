@@ -615,8 +615,9 @@ daa_status daa_release_pages(const daa_page_pool* pool, const int32_t* slots, in
  * daa_batch_attention on the pool's values in bf16, up to fp32 rounding order
  * and the rounding of the softmax weights.  Slots past a request's last token
  * may hold anything.  Requests of up to 96 packed (token, query head) rows are
- * read from the 4-bit pages; the pages of longer chunks are written to the
- * workspace in bf16 first (2 * Hkv * head_dim * 32 bytes a page), each once.
+ * read from the 4-bit pages, and longer chunks where a batch has few of them;
+ * else their pages are written to the workspace in bf16 first (2 * Hkv *
+ * head_dim * 32 bytes a page), each once.
  *  plan: host arrays of daa_batch_attention; the workspace (at least
  *        daa_batch_attention_q4_workspace_size bytes, 256-byte aligned); `info`.
  *        It copies from host memory, so it cannot be captured into a CUDA graph

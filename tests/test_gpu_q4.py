@@ -479,7 +479,7 @@ def test_serving_steps_together(daa, hq, hkv, d, exps):
 
 @pytest.mark.parametrize("hq,hkv,new", [(8, 1, [12]), (8, 1, [13]), (4, 1, [24, 25]), (16, 1, [6, 7, 1])])
 def test_attention_around_the_row_threshold(daa, hq, hkv, new):
-    """The largest requests read from the 4-bit pages and the smallest that go by way of bf16 ones."""
+    """Around the rows from which a request counts as a long chunk."""
     _check(daa, np.random.default_rng(21), hq, hkv, 128, [333] * len(new), new)
     _check(daa, np.random.default_rng(22), hq, hkv, 64, [90] * len(new), new, causal=False)
 
@@ -688,3 +688,26 @@ def test_attention_refuses_a_short_page_list(daa):
     table.page_indices = table.page_indices[:-1]
     with pytest.raises(ValueError):
         daa.BatchAttentionQ4(table, 2, daa.new_q4_pool(n, 2, 64))
+
+
+@pytest.mark.parametrize("hq,hkv,d,cached,new,causal,exps,bf16", [
+    (32, 8, 128, [300, 20, 0], [512, 1, 0], True, True, True),       # four-tile items, a decode beside
+    (32, 8, 64, [77, 900], [500, 6], True, False, True),
+    (16, 16, 128, [100, 0], [260, 259], False, True, True),
+    (8, 8, 64, [5, 700, 3], [700, 1, 1], False, False, True),
+    (24, 8, 128, [2500, 40], [85, 1], True, False, False),           # a token more than two tiles of 42
+    (24, 8, 128, [2500, 40], [84, 1], True, False, True),            # two tiles, keys cut
+    (7, 1, 64, [3860, 40], [108, 1], True, True, False), (4, 1, 128, [1500], [512], True, False, False),
+    (8, 2, 128, [1000, 9, 100], [128, 1, 30], False, True, False), (1, 1, 64, [0], [1500], True, False, False),
+])
+def test_attention_long_chunks(daa, hq, hkv, d, cached, new, causal, exps, bf16):
+    """Chunks by way of bf16 pages, and few ones that are read from the 4-bit pages."""
+    attn, q, out, _, _ = _check(daa, np.random.default_rng(34), hq, hkv, d, cached, new, causal=causal, exps=exps)
+    daa.trace_enable(16)
+    try:
+        again = attn.run(q.to(DEV))
+        names = [n for n, _ in daa.trace_read()]
+    finally:
+        daa.trace_disable()
+    assert ("kv_dequant_q4" in names) == bf16
+    assert torch.equal(again, out)

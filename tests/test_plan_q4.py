@@ -45,19 +45,34 @@ def _plan(exe, hq, hkv, d, sms, cached, new):
     return got, qo, kp, kv
 
 
+def _few(long, new, kv, g, hkv, sms):
+    """Whether the long requests' 24-row units are few for the GPU (units times kv heads,
+    against their longest key range)."""
+    warps = hkv * sum(-(-new[r] // max(1, 24 // g)) for r in long)
+    keys = max(int(kv[r]) for r in long)
+    split = any(new[r] <= 2 * (128 // g) for r in long)
+    if warps <= 0.6 * sms:
+        return not split or warps * keys <= 150000
+    return not split and warps <= 2 * sms - 160000 // keys
+
+
 @pytest.mark.parametrize("hq,hkv,d,cached,new", [
     (32, 32, 128, [500] * 7 + [4000] * 5, [1] * 12), (12, 1, 128, [100, 30000, 9000, 0], [1, 1, 1, 1]),
     (32, 8, 128, [1000, 50, 0, 7], [5, 0, 1, 3]), (16, 1, 64, [400, 8000], [4, 1]),
     (8, 2, 64, [3, 0, 900], [24, 25, 1]), (4, 2, 64, [48, 39, 72], [16, 1, 1]), (3, 3, 128, [0] * 700, [1] * 700),
     (40, 8, 128, [2000, 100, 33, 64], [1, 20, 19, 300]), (1, 1, 64, [], []), (2, 1, 128, [5, 6], [0, 0]),
     (16, 16, 128, list(range(0, 3000, 37)), [1 + i % 9 for i in range(82)]), (7, 1, 128, [100000], [1]),
+    (7, 1, 64, [3860, 40], [108, 1]), (4, 1, 128, [16000], [512]), (8, 2, 128, [4000, 9, 100], [128, 1, 30]),
 ])
 @pytest.mark.parametrize("sms", [152, 3])
 def test_units_cover_every_token_and_page_once(harness, hq, hkv, d, cached, new, sms):
     got, qo, kp, kv = _plan(harness, hq, hkv, d, sms, cached, new)
     g = hq // hkv
-    native = [r for r in range(len(new)) if 0 < new[r] * g <= NATIVE]
     long = [r for r in range(len(new)) if new[r] * g > NATIVE]
+    if not got["X"]:  # none, or so few that the 4-bit pages are better for them, too
+        assert not long or _few(long, new, kv, g, hkv, sms)
+        long = []
+    native = [r for r in range(len(new)) if 0 < new[r] and r not in long]
     seen = {(r, t): np.zeros(kp[r + 1] - kp[r], int) for r in native for t in range(new[r])}
     slots = {}
     owner = {int(qo[r] + t): (r, t) for r in native for t in range(new[r])}
@@ -105,3 +120,15 @@ def test_units_cover_every_token_and_page_once(harness, hq, hkv, d, cached, new,
         covered |= {row0 + tok0 + t for t in range(n)}
     assert covered == set(rows)
     assert got["L"][0][1] == len(got["X"])
+
+
+@pytest.mark.parametrize("hq,hkv,cached,new,native", [
+    (7, 1, [3860], [108], True),              # one chunk, one kv head: seven SMs' worth of tiles
+    (32, 8, [1536], [512], False),            # tiles for 64 SMs, 688 units
+    (32, 8, [1536, 900], [64, 1], True), (32, 8, [16000], [64], False),
+    (64, 8, [8192, 8192], [8192, 8192], False), (12, 1, [16000, 5], [170, 1], True),
+    (12, 1, [16000, 16000, 16000, 16000, 16000], [170] * 5, False),
+])
+def test_few_long_chunks_stay_on_the_4_bit_pages(harness, hq, hkv, cached, new, native):
+    got, *_ = _plan(harness, hq, hkv, 128, 152, cached, new)
+    assert (not got["X"]) == native and bool(got["U"]) == (native or 1 in new)

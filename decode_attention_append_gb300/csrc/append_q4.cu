@@ -44,7 +44,7 @@ constexpr int kMaxBatch = 1023;                 // requests whose indptr a CTA h
 
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
   return v;
@@ -53,7 +53,7 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
 // 32 bytes at once, where the address allows it: the two 16-byte loads of a block
 // would each ask for half of every 32-byte sector of the warp's kilobyte.
 __device__ __forceinline__ void ld_stream_32(const uint4* p, uint4& a, uint4& b) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
                : "l"(p));
 }
@@ -97,11 +97,11 @@ __device__ __forceinline__ uint2 quantise_block(const uint4& a, const uint4& b, 
 // touches is found once by binary search.
 template <int D, int kAppendU>
 __global__ void __launch_bounds__(kThreads)
-kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new,
-                    uint8_t* __restrict__ pool, const int32_t* __restrict__ kv_exp,
-                    const int32_t* __restrict__ append_indptr,
-                    const int32_t* __restrict__ page_indices, const int32_t* __restrict__ kv_indptr,
-                    const int32_t* __restrict__ last_page_len, int batch, int nnz_new, int Hkv,
+kv_append_q4_kernel(const uint4* k_new, const uint4* v_new,
+                    uint8_t* __restrict__ pool, const int32_t* kv_exp,
+                    const int32_t* append_indptr,
+                    const int32_t* page_indices, const int32_t* kv_indptr,
+                    const int32_t* last_page_len, int batch, int nnz_new, int Hkv,
                     int step_rows, int step_blocks, int64_t num_pages, int* err) {
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
   constexpr int kAppendSpan = kThreads * kAppendU;
@@ -143,9 +143,9 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
   const int32_t *indptr = append_indptr, *kv_begin = kv_indptr, *last_lens = last_page_len;
   if (batch <= kMaxBatch) {
     for (int t = threadIdx.x; t <= batch; t += kThreads) {
-      s_indptr[t] = __ldg(append_indptr + t);
-      s_kv[t] = __ldg(kv_indptr + t);
-      s_last[t] = t < batch ? __ldg(last_page_len + t) : 0;
+      s_indptr[t] = ld_word(append_indptr + t);
+      s_kv[t] = ld_word(kv_indptr + t);
+      s_last[t] = t < batch ? ld_word(last_page_len + t) : 0;
     }
     __syncthreads();
     indptr = s_indptr;
@@ -169,7 +169,7 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
       set_device_error(err, kDevErrShape);
     } else {
       const int64_t pos = kv_len - (a1 - a0) + (row - a0);
-      const int64_t page = __ldg(page_indices + p0 + pos / P);
+      const int64_t page = ld_word(page_indices + p0 + pos / P);
       slot = (int)(pos % P);
       if (page < 0 || page >= num_pages) set_device_error(err, kDevErrPageRange);
       else at = page * Hkv;
@@ -195,7 +195,7 @@ kv_append_q4_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v
     const int64_t page = s_page[row];
     if (page < 0) continue;
     const int slot = s_slot[row];
-    const float me = kv_exp ? q4_pow2(-__ldg(kv_exp + kv * Hkv + h)) : 1.f;
+    const float me = kv_exp ? q4_pow2(-ld_word(kv_exp + kv * Hkv + h)) : 1.f;
     uint8_t sc;
     const uint2 codes = quantise_block(a[u], b[u], me, sc);
     uint8_t* slice = pool + ((page + h) * 2 + kv) * (int64_t)SLICE;
@@ -213,8 +213,8 @@ constexpr int kDeqSmallU = 2, kDeqLargeU = 4;
 
 template <int D, int kDeqU>
 __global__ void __launch_bounds__(D, 2048 / D)
-kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ kv_exp,
-                     const int32_t* __restrict__ ids, const int32_t* __restrict__ src,
+kv_dequant_q4_kernel(const uint8_t* pool, const int32_t* kv_exp,
+                     const int32_t* ids, const int32_t* src,
                      int64_t n_slices, int Hkv, int64_t num_pages, uint16_t* __restrict__ out,
                      int* err) {
   constexpr int P = kQ4Page, NB = D / kQ4Block, SLICE = q4_slice_bytes(D);
@@ -243,11 +243,11 @@ kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict
   if (src) {
 #pragma unroll
     for (int u = 0; u < kDeqU; ++u)
-      if (u < n) page[u] = __ldg(src + page[u]);
+      if (u < n) page[u] = ld_word(src + page[u]);
   }
 #pragma unroll
   for (int u = 0; u < kDeqU; ++u)
-    if (u < n) page[u] = __ldg(ids + page[u]);
+    if (u < n) page[u] = ld_word(ids + page[u]);
   uint32_t codes[kDeqU][2];
   uint32_t sc[kDeqU];
 #pragma unroll
@@ -258,10 +258,10 @@ kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict
       const int kv = at[u] >= Hkv, h = kv ? at[u] - Hkv : at[u];
       const uint8_t* slice = pool + (((int64_t)page[u] * Hkv + h) * 2 + kv) * SLICE;
       const uint8_t* row = slice + tok * (D / 2) + chunk * 4;
-      codes[u][0] = __ldg(reinterpret_cast<const uint32_t*>(row));
-      codes[u][1] = __ldg(reinterpret_cast<const uint32_t*>(row + 8 * (D / 2)));
+      codes[u][0] = (uint32_t)ld_word(row);
+      codes[u][1] = (uint32_t)ld_word(row + 8 * (D / 2));
       const uint8_t* s8 = slice + P * (D / 2) + (kv == 0 ? tok * NB + blk : blk * P + tok);
-      sc[u] = __ldg(s8) | (uint32_t)__ldg(s8 + (kv == 0 ? 8 * NB : 8)) << 8;
+      sc[u] = ld_byte(s8) | ld_byte(s8 + (kv == 0 ? 8 * NB : 8)) << 8;
     } else if (threadIdx.x == 0) {
       set_device_error(err, kDevErrPageRange);
     }
@@ -269,7 +269,7 @@ kv_dequant_q4_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict
 #pragma unroll
   for (int u = 0; u < kDeqU; ++u) {
     if (u >= n) break;
-    const float two_e = kv_exp ? q4_pow2(__ldg(kv_exp + at[u])) : 1.f;
+    const float two_e = kv_exp ? q4_pow2(ld_word(kv_exp + at[u])) : 1.f;
     const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)sc[u]);
     uint4* dst = reinterpret_cast<uint4*>(out + ((s0 + u) * P + tok) * D + chunk * 8);
 #pragma unroll

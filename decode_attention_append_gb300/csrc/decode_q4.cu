@@ -121,29 +121,28 @@ attention_q4_kernel(const AttentionQ4Args a) {
   uint8_t* ring = smem + warp * (S::PAIRS * S::STAGE);
   uint4* q_frag = reinterpret_cast<uint4*>(smem + S::OFF_Q + warp * S::Q_WARP);
 
-  // The next kernel may start its CTAs, but not before this one may read: the next
-  // class's launch does not wait by itself.
-  if (a.wait_first) grid_dep_wait();
-  grid_dep_launch();
   // the heads of a range in warps side by side: their slices of a page are, too
   const int64_t id = (int64_t)blockIdx.x * kWarps + warp;
   const int range = (int)(id / a.Hkv);
   if (range >= a.n_ranges) return;
   const int kvh = (int)(id - (int64_t)range * a.Hkv);
   const int g = a.group;
-  const Q4Range rec = a.ranges[range];
-  const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(__ldg(a.kv_exp + kvh)) : 1.f);
-  const float f_v = a.kv_exp ? q4_pow2(__ldg(a.kv_exp + a.Hkv + kvh)) : 1.f;
-  auto pages_of = [&](const Q4Unit& u) {
-    const int key_end = a.causal ? min(u.tok_end, u.pos0 + u.n_tok) : u.tok_end;
-    return max(0, (key_end + kP - 1) / kP - u.tok_begin / kP);
-  };
-
+  const Q4Range rec = a.ranges[range];  // of the plan: copied long before the kernel ahead of this one
   if (lane == 0) {
     for (int i = 0; i < S::PAIRS; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   __syncwarp();
+  // The next kernel may start its CTAs, but not before this one may read: the next
+  // class's launch does not wait by itself.
+  if (a.wait_first) grid_dep_wait();
+  grid_dep_launch();
+  const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(ld_word(a.kv_exp + kvh)) : 1.f);
+  const float f_v = a.kv_exp ? q4_pow2(ld_word(a.kv_exp + a.Hkv + kvh)) : 1.f;
+  auto pages_of = [&](const Q4Unit& u) {
+    const int key_end = a.causal ? min(u.tok_end, u.pos0 + u.n_tok) : u.tok_end;
+    return max(0, (key_end + kP - 1) / kP - u.tok_begin / kP);
+  };
 
   // The loads run ahead of the products by the ring's depth, over the end of a
   // unit into the next ones: in_unit, in_j, in_n are the unit, page and page count
@@ -154,7 +153,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   const uint8_t* head = a.pool + (int64_t)kvh * S::PAGE;
   const uint32_t page_stride = (uint32_t)a.Hkv * S::PAGE;
   auto load_ids = [&]() {
-    ids = in_j + lane < in_n ? __ldg(in_ids + in_j + lane) : 0;
+    ids = in_j + lane < in_n ? ld_word(in_ids + in_j + lane) : 0;
     if (ids < 0 || ids >= a.num_pages) {
       set_device_error(a.err, kDevErrPageRange);
       ids = 0;  // a valid page instead; the output is undefined anyway
@@ -206,30 +205,32 @@ attention_q4_kernel(const AttentionQ4Args a) {
   float fs[NT][2];       // score factor of rows 8 t + 2 c, + 1
   int lim[NT][2];        // keys of those rows: [0, lim)
   int lim_min = INT_MAX;
+  uint4 q_row[NT][D / 32];  // all loads at once; a row past the last is another one, set to zero
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int n = 8 * t + r;
+    const int n = min(8 * t + r, rows - 1), tok = n / g;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        a.q + ((int64_t)(u.q_row + tok) * a.Hq + kvh * g + (n - tok * g)) * D + c * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) q_row[t][i] = ld_16(src + i);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
     float x[D / 4];
     float mx = 0.f;
-    if (n < rows) {
-      const int tok = n / g;
-      const uint16_t* src = a.q + ((int64_t)(u.q_row + tok) * a.Hq + kvh * g + (n - tok * g)) * D + c * (D / 4);
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 w = q_row[t][i];
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          x[8 * i + 2 * j] = bf16lo_to_f32(ww[j]);
-          x[8 * i + 2 * j + 1] = bf16hi_to_f32(ww[j]);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v = 8 * t + r < rows ? ww[j] : 0u;
+        x[8 * i + 2 * j] = bf16lo_to_f32(v);
+        x[8 * i + 2 * j + 1] = bf16hi_to_f32(v);
       }
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
-    } else {
-#pragma unroll
-      for (int i = 0; i < D / 4; ++i) x[i] = 0.f;
     }
+#pragma unroll
+    for (int i = 0; i < D / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const int ex = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126) : 0;

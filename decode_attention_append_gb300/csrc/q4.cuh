@@ -25,6 +25,25 @@ constexpr int kQ4MaxExp = 32;  // |kv_exp| is cut to this, so powers of two stay
 
 __host__ __device__ constexpr int q4_slice_bytes(int d) { return 9 * d; }
 
+// Loads of what the kernel ahead may have written.  These kernels are launched
+// programmatically and start before that one has ended, so its results are no
+// constants of theirs: not ld.global.nc (__ldg), and volatile, to stay behind the wait.
+__device__ __forceinline__ int32_t ld_word(const void* p) {
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_byte(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // Eight e2m1 codes (one 32-bit word, lowest nibble first) -> four fp16 pairs.
 __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"

@@ -28,6 +28,7 @@
 
 #include "launch.h"
 #include "ptx.cuh"
+#include "q4.cuh"
 
 namespace daa {
 namespace {
@@ -136,8 +137,8 @@ __device__ int read_batch(const StepTableArgs& a, const Smem& s, const Layout& l
     Sums<W> v{0, 0, 0};
     int slot = -1, held = 0, len = 0;
     if (i < a.batch) {
-      slot = __ldg(a.slots + i);
-      const int n = RELEASE ? 0 : __ldg(a.new_len + i);
+      slot = ld_word(a.slots + i);
+      const int n = RELEASE ? 0 : ld_word(a.new_len + i);
       if (slot < 0 || slot >= a.num_slots || n < 0) {
         bad = 1;
         slot = 0;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) step_table_kernel(const StepTableArg
   }
   const int ticket = take_ticket(a.counters + 1);
   auto fresh_page = [&](int r, int p) {
-    return __ldg(a.free_pages + (free_count - 1 - (s.tp[r] + p - s.held[r])));
+    return ld_word(a.free_pages + (free_count - 1 - (s.tp[r] + p - s.held[r])));
   };
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= n; i += kThreads) {

@@ -127,6 +127,8 @@ attention_q4_kernel(const AttentionQ4Args a) {
   if (range >= a.n_ranges) return;
   const int kvh = (int)(id - (int64_t)range * a.Hkv);
   const int g = a.group;
+  const uint32_t inv_g = 65536u / (uint32_t)g + 1;  // n / g = n * inv_g >> 16, a row's token (n < 64)
+  auto token_of = [&](int n) { return (int)((uint32_t)n * inv_g >> 16); };
   const Q4Range rec = a.ranges[range];  // of the plan: copied long before the kernel ahead of this one
   if (lane == 0) {
     for (int i = 0; i < S::PAIRS; ++i) mbar_init(&full[i], 1);
@@ -208,7 +210,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   uint4 q_row[NT][D / 32];  // all loads at once; a row past the last is another one, set to zero
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int n = min(8 * t + r, rows - 1), tok = n / g;
+    const int n = min(8 * t + r, rows - 1), tok = token_of(n);
     const uint4* src = reinterpret_cast<const uint4*>(
         a.q + ((int64_t)(u.q_row + tok) * a.Hq + kvh * g + (n - tok * g)) * D + c * (D / 4));
 #pragma unroll
@@ -247,7 +249,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
       const int m = 8 * t + 2 * c + b;
       const int e = __shfl_sync(0xffffffffu, ex, 4 * (2 * c + b));  // row m's, held by lanes 4 (m % 8) ..
       fs[t][b] = f_k * __uint_as_float((uint32_t)(127 + e) << 23);
-      lim[t][b] = a.causal && m < rows ? min(u.pos0 + m / g + 1, u.kv_len) : u.kv_len;
+      lim[t][b] = a.causal && m < rows ? min(u.pos0 + token_of(m) + 1, u.kv_len) : u.kv_len;
       lim_min = min(lim_min, lim[t][b]);
     }
   }
@@ -475,7 +477,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
       if (n >= rows) continue;
       const float inv = L > 0.f || L != L ? f_v / L : 0.f;  // no visible key: zero, lse -inf
       const float lse2 = off[t][b] + __log2f(L);            // a weight is 2^(s - off)
-      const int tok = n / g;
+      const int tok = token_of(n);
       const int hq = kvh * g + (n - tok * g);
       if (u.part < 0) {
         const int64_t row = (int64_t)(u.q_row + tok) * a.Hq + hq;

@@ -29,8 +29,11 @@ constexpr int kQ4NativeRows = 96;
 // page on an SM: 60, 95 and 140 ns with 8, 16 and 24 rows).  Where all units of 8
 // rows find a free warp, smaller ones end sooner.
 constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
-constexpr int kQ4UnitPages = 3;   // what a unit costs beside its pages, in pages
 constexpr int kQ4MinPages = 4;    // pages of a range at least
+// What a unit costs beside its pages, in pages, by class (GB300: with 3 for all a second
+// unit made 16- and 24-row warps end 2 us after the others; decode of 128 requests of 12
+// heads 53.3 us with 3 and 51.4 with 7, verify of 5 tokens 44.4 and 42.7).
+constexpr int kQ4UnitPages[kQ4Classes] = {5, 7, 7};
 
 // Whether a batch's long requests are better read from the 4-bit pages, too: few_chunks
 // of `warps` (units of kQ4UnitRows rows, times kv heads) over up to `keys` keys.  The
@@ -196,9 +199,10 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     int64_t left_streams = (int64_t)ss.size();
     // cost of the next range: what is left over the ranges left (each but the last
     // may cut a stream, which costs a unit more)
+    const int unit_pages = kQ4UnitPages[cls];
     auto share = [&] {
       const int64_t left = first_range + n_ranges - (int64_t)(pl.seg_begin.size() - 1);
-      return (left_pages + kQ4UnitPages * (left_streams + left - 1) + left - 1) / left;
+      return (left_pages + unit_pages * (left_streams + left - 1) + left - 1) / left;
     };
     int64_t room = share();  // of the open range
     for (Stream& s : ss) {
@@ -206,19 +210,19 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
       for (int at = 0; at < s.pages;) {
         const int left = s.pages - at;
         const bool last_range = (int)pl.seg_begin.size() - first_range == (int)n_ranges;
-        if (!last_range && room < std::min<int64_t>(left, kQ4MinPages / 2) + kQ4UnitPages &&
+        if (!last_range && room < std::min<int64_t>(left, kQ4MinPages / 2) + unit_pages &&
             (int)pl.units.size() > pl.seg_begin.back()) {
           pl.seg_begin.push_back((int32_t)pl.units.size());
           room = share();
           continue;
         }
-        int n = last_range ? left : (int)std::max<int64_t>(1, std::min<int64_t>(left, room - kQ4UnitPages));
+        int n = last_range ? left : (int)std::max<int64_t>(1, std::min<int64_t>(left, room - unit_pages));
         if (left - n < kQ4MinPages / 2) n = left;  // no small rest
         Q4Unit u{};
         u.tok_begin = at * P;
         u.tok_end = (at + n) * P;
         if (!pl.units.push_back(u)) return DAA_ERR_WORKSPACE;
-        room -= n + kQ4UnitPages;
+        room -= n + unit_pages;
         left_pages -= n;
         at += n;
       }

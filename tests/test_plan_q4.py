@@ -103,7 +103,7 @@ def test_units_cover_every_token_and_page_once(harness, hq, hkv, d, cached, new,
         assert all((8 * c < u[1] * g <= 8 * c + 8) for u in got["U"][b:e])
     assert at == len(got["U"])
     for c in range(3):
-        cost = [sum(-(-(u[6] - u[5]) // P) + 3 for u in got["U"][b:e]) for b, e, k in got["R"] if k == c]
+        cost = [sum(-(-(u[6] - u[5]) // P) + (5, 7, 7)[c] for u in got["U"][b:e]) for b, e, k in got["R"] if k == c]
         assert len(cost) <= sms * (16 if c == 0 else 8) * (2 if long else 1)
         if len(cost) > 1 and len(cost) > 4:
             assert max(cost) <= np.mean(cost) + 8

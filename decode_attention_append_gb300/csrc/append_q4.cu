@@ -37,7 +37,7 @@ constexpr int kThreads = 128;
 // Blocks of 16 dims per thread in flight: two for small appends (a CTA's chain of
 // loads is what they wait for, so they are cut fine: a step of 128 tokens 8.3 us with
 // its read-back, 10.3 with six), six once the CTAs fill the GPU more than once
-// (36,760 tokens, with the read-back 70.7 us; with two 74.2, with eight 75.5; CTAs that
+// (36,760 tokens, with the read-back 70.4 us; with two 74.2, with eight 75.5; CTAs that
 // stay and load the next chunk while they quantise one: 72.4).
 constexpr int kSmallU = 2, kLargeU = 6;
 constexpr int kMaxBatch = 1023;                 // requests whose indptr a CTA holds

@@ -31,22 +31,26 @@
 //
 // Bound: HBM for 8 rows, instructions for more.  A (page, head) is 18 d bytes; at
 // the measured 6.7 TB/s an SM gets one of d = 128 every 52 ns (about 99 clocks), in
-// which it can issue 400 warp instructions.  A page takes 279 of them with 8 rows, 313
-// with 16 and 393 with 24: 64 conversions and 64 products of the codes, 16 mma for
-// every 8 rows, the rest loads, scales, exponents and the ring.  Measured (GB300, a
-// page on an SM): 60 ns with 8 rows (32 requests of 0.5k to 4k tokens, 32 heads on 32:
-// 56 us, 5.7 TB/s), 95 with 16 (128 of 1k to 32k, 12 heads on 1: 48 us, 3.7 TB/s) and
-// 140 with 24 (verify of 5 tokens, 32 heads on 8: 39.5 us, 2.5 TB/s); issue slots used
-// 63, 47 and 41 %.  The loads alone take 49, 34 and 26 us.
+// which it can issue 400 warp instructions.  A page takes 280 of them with 8 rows, 309
+// with 16 and 389 with 24: 64 conversions and 64 products of the codes, 16 mma for
+// every 8 rows, the rest loads, scales, exponents and the ring.  Measured (GB300): each
+// further page of long contexts takes an SM 52 ns with 8 rows (the bytes' time), 74 with
+// 16 and 92 with 24; about 3.5 us go by before the first pages are there, and 0.5 to 2
+// for writing a range's last unit.  Kernels: 32 requests of 0.5k to 4k tokens, 32 heads
+// on 32, 56 us (5.7 TB/s); 128 of 1k to 32k, 12 heads on 1, 45.5 us (3.9 TB/s); verify of
+// 5 tokens, 32 heads on 8, 37 us (2.7 TB/s); issue slots used 64, 49 and 43 %.  The loads
+// alone take 49, 34 and 26 us.
 //
 // Warps work alone: each streams a range of pages of its own (the units of one kv
 // head, cut so that every resident warp has the same cost) through its own ring with
 // one bulk copy a page (K and V of a head are side by side), over the ends of
 // requests, and writes its own parts; nothing in a CTA is synchronised.  Measured and
 // not faster: two warps to a range that share its pages and split the dims, so that
-// 16 and 24 rows have 16 warps an SM, too (58 and 51 us: 460 instructions a page); 12
-// warps of 168 registers for 16 rows (51 us); tcgen05 with the codes converted into
-// TMEM and shared memory (79 us for 48).
+// 16 and 24 rows have 16 warps an SM, too (58 us for 48 and 51 for 39.5: 460
+// instructions a page); 12 warps of 168 registers for 16 rows (51 for 48); the scores of a
+// pair beside the products of the one before it (52 for 48); tcgen05 with the codes
+// converted into TMEM and shared memory (79 for 47); a unit's rows written by way of
+// shared memory (47 us for 44.9 with the merge).
 #include <cfloat>
 #include <climits>
 

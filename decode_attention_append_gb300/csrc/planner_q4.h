@@ -26,7 +26,7 @@ namespace daa {
 // to 168.
 constexpr int kQ4NativeRows = 96;
 // Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
-// page on an SM: 60, 95 and 140 ns with 8, 16 and 24 rows).  Where all units of 8
+// further page on an SM: 52, 74 and 92 ns with 8, 16 and 24 rows).  Where all units of 8
 // rows find a free warp, smaller ones end sooner.
 constexpr int kQ4UnitRows = 24, kQ4SmallUnitRows = 8;
 constexpr int kQ4MinPages = 4;    // pages of a range at least

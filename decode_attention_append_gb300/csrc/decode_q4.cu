@@ -114,6 +114,14 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+// A sector at once (p on a 32-byte boundary).
+__device__ __forceinline__ void st_32(float* p, float a, float b, float c, float d, float e, float f, float g,
+                                      float h) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d),
+               "f"(e), "f"(f), "f"(g), "f"(h)
+               : "memory");
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kWarps, Shape<D, NT>::CTAS)
 attention_q4_kernel(const AttentionQ4Args a) {
@@ -498,11 +506,12 @@ attention_q4_kernel(const AttentionQ4Args a) {
         if (r == 0 && a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
       } else {
         const int64_t row = ((int64_t)u.part + (int64_t)tok * u.part_stride) * a.Hq + hq;
-        float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + r * (D / 8));
+        float* dst = a.part_o + row * D + r * (D / 8);
 #pragma unroll
-        for (int i = 0; i < S::TILES; i += 2)
-          dst[i / 2] = make_float4(o[t][i][b] * inv, o[t][i][b + 2] * inv, o[t][i + 1][b] * inv,
-                                   o[t][i + 1][b + 2] * inv);
+        for (int i = 0; i < S::TILES; i += 4)
+          st_32(dst + 2 * i, o[t][i][b] * inv, o[t][i][b + 2] * inv, o[t][i + 1][b] * inv,
+                o[t][i + 1][b + 2] * inv, o[t][i + 2][b] * inv, o[t][i + 2][b + 2] * inv,
+                o[t][i + 3][b] * inv, o[t][i + 3][b + 2] * inv);
         if (r == 0) a.part_lse[row] = lse2;
       }
     }

@@ -37,8 +37,8 @@
 // further page of long contexts takes an SM 52 ns with 8 rows (the bytes' time), 74 with
 // 16 and 92 with 24; about 3.5 us go by before the first pages are there, and 0.5 to 2
 // for writing a range's last unit.  Kernels: 32 requests of 0.5k to 4k tokens, 32 heads
-// on 32, 56 us (5.7 TB/s); 128 of 1k to 32k, 12 heads on 1, 45.5 us (3.9 TB/s); verify of
-// 5 tokens, 32 heads on 8, 37 us (2.7 TB/s); issue slots used 64, 49 and 43 %.  The loads
+// on 32, 56 us (5.7 TB/s); 128 of 1k to 32k, 12 heads on 1, 44.7 us (4.0 TB/s); verify of
+// 5 tokens, 32 heads on 8, 35 us (2.8 TB/s); issue slots used 64, 49 and 43 %.  The loads
 // alone take 49, 34 and 26 us.
 //
 // Warps work alone: each streams a range of pages of its own (the units of one kv
@@ -74,8 +74,9 @@ struct Shape {
   static constexpr int PAGE = 2 * SLICE;               // K and V of one (page, head)
   static constexpr int CTAS = NT == 1 ? 4 : 2;         // meant to share an SM: 128 and 255 registers
   // Ring, in pairs of pages.  Deeper ones measured slower: at the start every warp's
-  // further pages queue in front of other warps' first ones.
-  static constexpr int PAIRS = (NT == 1 ? 2 : 3) * (D == 128 ? 1 : 2);
+  // further pages queue in front of other warps' first ones (24 rows, contexts of 4k:
+  // 53.8 us with two, 55.4 with three; 16 rows 50.9 and 50.4).
+  static constexpr int PAIRS = (NT == 2 ? 3 : 2) * (D == 128 ? 1 : 2);
   static constexpr int STAGE = 2 * PAGE;
   static constexpr int TILES = D / 16;                 // 16-dim tiles of O^T
   static constexpr int KWORDS = D / 32;                // code words of a thread per key row
@@ -114,7 +115,8 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t lo, uint32_t hi) {
   return d;
 }
 
-// A sector at once (p on a 32-byte boundary).
+// A sector at once (p on a 32-byte boundary): with 16-byte stores, half a sector each,
+// the parts of 24-row units cost 1.5 us more (verify of 5 tokens 42.8 us, 41.3).
 __device__ __forceinline__ void st_32(float* p, float a, float b, float c, float d, float e, float f, float g,
                                       float h) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d),

@@ -807,7 +807,8 @@ class PagePool:
     @classmethod
     def from_tensors(cls, seq_len, held, block_table, free_pages, counters):
         """A pool on the caller's tensors (see ``daa_page_pool``).  Its host
-        copies of the lengths are read from the device by the first ``step``."""
+        copies of the lengths are read from the device by the first ``step``,
+        ``set_lengths`` or ``release``, on that call's stream."""
         self = cls.__new__(cls)
         self._init(seq_len, held, block_table, free_pages, counters)
         self.h_len = self.h_held = self.h_free = None
@@ -829,11 +830,13 @@ class PagePool:
         self._pool = _Pool(*ptrs, seq_len.shape[0], block_table.shape[1], free_pages.shape[0], self.PAGE_SIZE)
         self._pool_ref = ctypes.byref(self._pool)
 
-    def _mirror(self):
+    def _mirror(self, stream):
+        """The host copies, read once behind what the call's stream holds (it may be
+        what fills the arrays)."""
         if self.h_len is None:
-            self.h_len = self.seq_len.cpu().numpy().astype(np.int64)
-            self.h_held = self.held.cpu().numpy().astype(np.int64)
-            self.h_free = int(self.counters[0])
+            with torch.cuda.device(self.dev), _use_stream(stream):
+                n, held, free = (x.cpu().numpy() for x in (self.seq_len, self.held, self.counters))
+            self.h_len, self.h_held, self.h_free = n.astype(np.int64), held.astype(np.int64), int(free[0])
 
     def build(self, slots, new_len, qo_indptr, kv_indptr, page_indices, last_page_len, slot_map=None,
               positions=None, advance=False, stream=None):
@@ -863,7 +866,7 @@ class PagePool:
         """The page table of a step that brings ``new_lens[i]`` tokens to slot
         ``slots[i]`` (host sequences).  With ``advance`` the lengths grow by them;
         otherwise call ``set_lengths`` once it is known how many were kept."""
-        self._mirror()
+        self._mirror(stream)
         sl, nl = (np.asarray(x, np.int64).reshape(-1) for x in (slots, new_lens))
         self._check_slots(sl)
         if len(nl) != len(sl) or (nl < 0).any():
@@ -900,7 +903,7 @@ class PagePool:
     def set_lengths(self, slots, lens, stream=None):
         """Set the cached lengths of slots (the tokens kept of a step that did
         not advance, or a request cut back).  Pages stay with their slots."""
-        self._mirror()
+        self._mirror(stream)
         sl, ln = (np.asarray(x, np.int64).reshape(-1) for x in (slots, lens))
         self._check_slots(sl)
         if len(ln) != len(sl) or (ln < 0).any() or (-(-ln // self.PAGE_SIZE) > self.h_held[sl]).any():
@@ -912,7 +915,7 @@ class PagePool:
 
     def release(self, slots, stream=None):
         """Give the pages of slots back (``daa_release_pages``); their lengths become 0."""
-        self._mirror()
+        self._mirror(stream)
         sl = np.asarray(slots, np.int64).reshape(-1)
         self._check_slots(sl)
         with torch.cuda.device(self.dev), _use_stream(stream):

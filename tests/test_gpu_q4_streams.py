@@ -1,0 +1,82 @@
+"""The 4-bit cache and the page pool on streams of the caller's: what a call reads,
+and the memory it uses, belong to the stream that it names."""
+import numpy as np
+import pytest
+import torch
+
+import q4_support as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BUSY = 200_000_000  # clock cycles, about 0.1 s: what is queued behind them has not run when the test goes on
+
+
+@pytest.fixture(scope="module")
+def daa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import decode_attention_append_gb300 as m
+    m.device_error(reset=True)
+    return m
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(daa):
+    yield
+    assert daa.device_error(reset=True) == 0
+
+
+def _dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _late_pool(daa, s):
+    """A pool of 6 slots whose arrays are filled on stream s, behind other work; its state."""
+    lens = [30, 16, 1, 0, 100, 0]
+    st = {"seq_len": np.array(lens, np.int32), "held": np.array([-(-x // 16) for x in lens], np.int32),
+          "block_table": np.full((6, 10), -1, np.int32)}
+    free = list(range(39, -1, -1))
+    for i, h in enumerate(st["held"]):
+        st["block_table"][i, :h] = [free.pop() for _ in range(h)]
+    st["free"] = free
+    stack = np.full(40, -1, np.int32)
+    stack[:len(free)] = free
+    src = [_dev(x) for x in (st["seq_len"], st["held"], st["block_table"], stack, np.array([len(free), 0], np.int32))]
+    dst = [torch.zeros_like(x) for x in src]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+        for d, x in zip(dst, src):
+            d.copy_(x)
+    return daa.PagePool.from_tensors(*dst), st
+
+
+def _same_host(pool, st):
+    assert np.array_equal(pool.h_len, st["seq_len"]) and np.array_equal(pool.h_held, st["held"])
+    assert pool.h_free == len(st["free"])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_lengths_are_read_on_the_stream_of_the_call(daa, raw):
+    s = torch.cuda.Stream()
+    name = s.cuda_stream if raw else s
+    pool, st = _late_pool(daa, s)
+    slots, new = [4, 0, 3], [1, 40, 17]
+    t = pool.step(slots, new, stream=name)
+    want = ref.step_table(st, slots, new, True)
+    torch.cuda.synchronize()
+    for n, w in want.items():
+        assert np.array_equal(getattr(t, n).cpu().numpy(), w), n
+    _same_host(pool, st)
+    pool, st = _late_pool(daa, s)
+    pool.set_lengths([0, 4], [17, 100], stream=name)
+    st["seq_len"][[0, 4]] = [17, 100]
+    torch.cuda.synchronize()
+    assert np.array_equal(pool.seq_len.cpu().numpy(), st["seq_len"])
+    _same_host(pool, st)
+    pool, st = _late_pool(daa, s)
+    pool.release([0, 4], stream=name)
+    torch.cuda.synchronize()
+    assert pool.counters.tolist() == [pool.h_free, 0] and pool.h_free == len(st["free"]) + 9

@@ -42,10 +42,12 @@ constexpr int kDevErrNoPages = 4;  // beside ptx.cuh's codes: a step needs more 
 // held, cached length; the scan's warp sums; the bitmap of the slots seen.
 struct Layout {
   int batch, words;
-  __host__ __device__ size_t bytes() const {
+  __host__ __device__ constexpr size_t bytes() const {
     return 8 * (size_t)(3 * kWarps) + 4 * ((size_t)6 * batch + 3 + words);
   }
 };
+
+constexpr size_t kMaxSmem = Layout{DAA_STEP_MAX_BATCH, DAA_STEP_MAX_SLOTS / 32}.bytes();
 
 struct Smem {
   long long* warp_sums;  // [3][kWarps]
@@ -353,8 +355,11 @@ cudaError_t launch_step_table(const StepTableArgs& a, bool release, int sms, boo
   const bool wide = (int64_t)a.batch * a.max_pages * kP > INT32_MAX;
   auto kern = release ? (wide ? release_pages_kernel<true> : release_pages_kernel<false>)
                       : (wide ? step_table_kernel<true> : step_table_kernel<false>);
+  // The kernel's limit, always the same one: with each call's own size, a smaller step
+  // prepared in another thread could lower it between this call and the launch.
+  static_assert(kMaxSmem <= 227 * 1024, "a step's shared memory");
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   // the host knows only upper bounds of the work: a CTA per 2048 pages or 512

@@ -80,3 +80,32 @@ def test_lengths_are_read_on_the_stream_of_the_call(daa, raw):
     pool.release([0, 4], stream=name)
     torch.cuda.synchronize()
     assert pool.counters.tolist() == [pool.h_free, 0] and pool.h_free == len(st["free"]) + 9
+
+
+def test_steps_of_two_pools_in_two_threads(daa):
+    """Steps of different sizes prepared at the same time: neither changes what the other is launched with."""
+    import threading
+    failed, go = [], threading.Barrier(2)
+
+    def work(batch):
+        try:
+            s = torch.cuda.Stream()
+            pool = daa.PagePool(2 * batch, batch, 4)
+            i32 = dict(dtype=torch.int32, device=DEV)
+            a = (torch.arange(batch, **i32), torch.ones(batch, **i32), torch.empty(batch + 1, **i32),
+                 torch.empty(batch + 1, **i32), torch.empty(batch, **i32), torch.empty(batch, **i32))
+            torch.cuda.synchronize()
+            go.wait()
+            for _ in range(3000):
+                pool.build(*a, stream=s)
+            s.synchronize()
+            assert a[3][-1] == batch
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(b,)) for b in (2500, 8000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed

@@ -312,7 +312,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
     a.head_dim = dims.head_dim;
     a.num_pages = dims.num_pages;
     a.causal = causal ? 1 : 0;
-    a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+    a.sm_scale = sm_scale;
     a.out = static_cast<uint16_t*>(out);
     a.lse_out = lse_out;
     a.part_o = reinterpret_cast<float*>(ws + lay.off_part_o);

@@ -115,6 +115,16 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+// sm_scale * log2(e) * 2^e for |e| <= 158, cut to fp32's normal numbers: a factor of zero (or
+// infinity) would turn the -inf of a hidden key (or the score 0) into NaN.  2^e comes in two
+// halves, so nothing on the way is out of range when the result is not.  Below FLT_MIN every
+// weight is 1 to within 2^-100 (before it a score is under 2^20) and the cut changes nothing.
+__device__ __forceinline__ float score_factor(float sm_scale, int e) {
+  const int half = e / 2;
+  const float f = sm_scale * __int_as_float((127 + half) << 23) * __int_as_float((127 + e - half) << 23);
+  return fminf(fmaxf(f * 1.4426950408889634f, FLT_MIN), FLT_MAX);
+}
+
 // A sector at once (p on a 32-byte boundary): with 16-byte stores, half a sector each,
 // the parts of 24-row units cost 1.5 us more (verify of 5 tokens 42.8 us, 41.3).
 __device__ __forceinline__ void st_32(float* p, float a, float b, float c, float d, float e, float f, float g,
@@ -153,7 +163,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
   // class's launch does not wait by itself.
   if (a.wait_first) grid_dep_wait();
   grid_dep_launch();
-  const float f_k = a.sm_scale_log2 * (a.kv_exp ? q4_pow2(ld_word(a.kv_exp + kvh)) : 1.f);
+  const int e_k = a.kv_exp ? q4_exp(ld_word(a.kv_exp + kvh)) : 0;
   const float f_v = a.kv_exp ? q4_pow2(ld_word(a.kv_exp + a.Hkv + kvh)) : 1.f;
   auto pages_of = [&](const Q4Unit& u) {
     const int key_end = a.causal ? min(u.tok_end, u.pos0 + u.n_tok) : u.tok_end;
@@ -262,7 +272,7 @@ attention_q4_kernel(const AttentionQ4Args a) {
     for (int b = 0; b < 2; ++b) {
       const int m = 8 * t + 2 * c + b;
       const int e = __shfl_sync(0xffffffffu, ex, 4 * (2 * c + b));  // row m's, held by lanes 4 (m % 8) ..
-      fs[t][b] = f_k * __uint_as_float((uint32_t)(127 + e) << 23);
+      fs[t][b] = score_factor(a.sm_scale, e + e_k);
       lim[t][b] = a.causal && m < rows ? min(u.pos0 + token_of(m) + 1, u.kv_len) : u.kv_len;
       lim_min = min(lim_min, lim[t][b]);
     }

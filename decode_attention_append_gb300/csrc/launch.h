@@ -217,7 +217,7 @@ struct AttentionQ4Args {
   int Hq, Hkv, group, head_dim;
   int64_t num_pages;
   int causal;
-  float sm_scale_log2;     // sm_scale * log2(e)
+  float sm_scale;
   uint16_t* out;
   float* lse_out;          // or null
   float* part_o;           // [n_parts][Hq][d]

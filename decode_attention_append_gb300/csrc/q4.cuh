@@ -113,10 +113,8 @@ __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
   return r;
 }
 
-// 2^e, e cut to [-kQ4MaxExp, kQ4MaxExp].
-__device__ __forceinline__ float q4_pow2(int e) {
-  e = min(max(e, -kQ4MaxExp), kQ4MaxExp);
-  return __int_as_float((e + 127) << 23);
-}
+// A head's exponent, cut to [-kQ4MaxExp, kQ4MaxExp], and two to its power.
+__device__ __forceinline__ int q4_exp(int e) { return min(max(e, -kQ4MaxExp), kQ4MaxExp); }
+__device__ __forceinline__ float q4_pow2(int e) { return __int_as_float((q4_exp(e) + 127) << 23); }
 
 }  // namespace daa

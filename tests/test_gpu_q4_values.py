@@ -1,0 +1,68 @@
+"""Attention over the 4-bit cache where scales leave fp32's range."""
+import numpy as np
+import pytest
+import torch
+
+import q4_support as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def daa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import decode_attention_append_gb300 as m
+    m.device_error(reset=True)
+    return m
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(daa):
+    yield
+    assert daa.device_error(reset=True) == 0
+
+
+def _dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _pool(rng, n, hkv, d):
+    return np.concatenate([rng.integers(0, 256, (n, hkv, 2, 8 * d), dtype=np.uint8),
+                           rng.integers(40, 64, (n, hkv, 2, d), dtype=np.uint8)], -1)
+
+
+def _table(daa, t):
+    return daa.PageTable.from_host(*(t[x] for x in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len")), DEV)
+
+
+def _bf16(rng, shape, scale=1.0):
+    return torch.from_numpy(rng.standard_normal(shape) * scale).bfloat16()
+
+
+@pytest.mark.parametrize("size,scale,e,zero_keys", [
+    (-122, None, -32, False), (-30, 2.0 ** -100, -32, False), (126, 2.0 ** -126, -20, False), (110, 2.0 ** -120, 12, False),
+    (-100, 2.0 ** 100, -8, False), (-126, 2.9e38, -6, False), (100, 2.0 ** 20, 32, True), (120, 2.0 ** 120, 0, True),
+])
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (8, 1), (6, 1)])
+def test_scales_at_the_ends_of_their_range(daa, hq, hkv, size, scale, e, zero_keys):
+    """Queries, sm_scale and exponents whose product leaves fp32's range or its normal numbers, in part or as a whole, while
+    the scores themselves are ordinary or vanish."""
+    rng = np.random.default_rng(41)
+    d = 128
+    t, n = ref.make_table(rng, [37, 5, 130], [1, 4, 3])
+    pool = _pool(rng, n, hkv, d)
+    if zero_keys:
+        pool[:, :, 0, :8 * d] = 0
+    exps = np.stack([np.full(hkv, e), np.arange(hkv) - 1]).astype(np.int32)
+    q = _bf16(rng, (8, hq, d)).clamp(-1.9, 1.9).double() * 2.0 ** size
+    q = q.bfloat16()
+    attn = daa.BatchAttentionQ4(_table(daa, t), hq, _dev(pool), sm_scale=scale, kv_exp=_dev(exps))
+    lse = torch.empty(8, hq, device=DEV)
+    out = attn.run(q.to(DEV), lse=lse)
+    used = 1 / d ** 0.5 if scale is None else float(np.float32(scale))
+    want = ref.attention(q.double().numpy(), pool, t, exps, d, used)
+    ref.check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, d)

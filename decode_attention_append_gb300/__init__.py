@@ -248,13 +248,19 @@ def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
 
-def _use_stream(stream):
+def _torch_stream(stream, dev: int):
+    """A call's stream on CUDA device `dev` as torch's: a stream of torch's, or a
+    cudaStream_t (0 and 1 are the handles of the default stream)."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    if int(stream) in (0, 1):
+        return torch.cuda.default_stream(dev)
+    return torch.cuda.ExternalStream(int(stream), device=dev)
+
+
+def _use_stream(stream, dev: int):
     """torch's own work of a call on the stream that the call names."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-    return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
 
 
 def _dims(kv_pages: torch.Tensor, num_qo_heads: int) -> _Dims:
@@ -834,7 +840,7 @@ class PagePool:
         """The host copies, read once behind what the call's stream holds (it may be
         what fills the arrays)."""
         if self.h_len is None:
-            with torch.cuda.device(self.dev), _use_stream(stream):
+            with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
                 n, held, free = (x.cpu().numpy() for x in (self.seq_len, self.held, self.counters))
             self.h_len, self.h_held, self.h_free = n.astype(np.int64), held.astype(np.int64), int(free[0])
 
@@ -884,7 +890,7 @@ class PagePool:
             raise DaaError(-2, "PagePool.step: the step's rows and pages must fit 32 bits")
         hl = np.where(pages > 0, kv - (pages - 1) * self.PAGE_SIZE, 0)
         i32 = dict(dtype=torch.int32, device=self.device)
-        with torch.cuda.device(self.dev), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             up = torch.from_numpy(np.stack([sl, nl]).astype(np.int32)).to(self.device)
             n = len(sl)
             t = PageTable(torch.empty(n + 1, **i32), torch.empty(n + 1, **i32),
@@ -908,7 +914,7 @@ class PagePool:
         self._check_slots(sl)
         if len(ln) != len(sl) or (ln < 0).any() or (-(-ln // self.PAGE_SIZE) > self.h_held[sl]).any():
             raise ValueError("lens must have one entry per slot, within the pages the slot holds")
-        with torch.cuda.device(self.dev), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             at = torch.from_numpy(sl).to(self.device)
             self.seq_len.index_copy_(0, at, torch.from_numpy(ln.astype(np.int32)).to(self.device))
         self.h_len[sl] = ln
@@ -918,7 +924,7 @@ class PagePool:
         self._mirror(stream)
         sl = np.asarray(slots, np.int64).reshape(-1)
         self._check_slots(sl)
-        with torch.cuda.device(self.dev), _use_stream(stream):
+        with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             dev = torch.from_numpy(sl.astype(np.int32)).to(self.device)
             _call(load_library().daa_release_pages, "release_pages", self.dev, stream, self._pool_ref,
                   dev.data_ptr(), len(sl))
@@ -983,7 +989,7 @@ def kv_dequant_q4(kv_pages, page_ids, kv_exp=None, out=None, stream=None):
     ids, n = _addr(page_ids, "page_ids", torch.int32, dev), page_ids.numel()
     shape = (n, 2, dims.num_kv_heads, dims.page_size, dims.head_dim)
     if out is None:
-        with _use_stream(stream):
+        with _use_stream(stream, dev):
             out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
     o = _addr(out, "out", torch.bfloat16, dev)
     if out.shape != shape:
@@ -1054,7 +1060,7 @@ class BatchAttentionQ4:
         if q.shape != self.shape:
             raise ValueError("q must be [nnz_qo, Hq, head_dim] of the planned table")
         if out is None:
-            with _use_stream(stream):
+            with _use_stream(stream, dev):
                 out = torch.empty_like(q)
         po = _addr(out, "out", bf16, dev)
         if out.shape != self.shape:

@@ -34,6 +34,7 @@ import ctypes
 import functools
 import os
 import threading
+import weakref
 from dataclasses import dataclass
 
 import numpy as np
@@ -261,6 +262,54 @@ def _torch_stream(stream, dev: int):
 def _use_stream(stream, dev: int):
     """torch's own work of a call on the stream that the call names."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
+
+
+class _StreamUse:
+    """Memory that torch allocated on one stream and calls use on others.  The
+    first call on another stream waits for the allocating one, where the memory may
+    still be in use as what it was before; and memory freed while a call is under
+    way is not given away before that call has ended.  A stream of torch's is
+    recorded with the allocator.  One of the caller's may be gone by the time the
+    memory is freed: an event after each call stands for it, and the allocating
+    stream waits for that.  Captured calls run when their graph is replayed: whoever
+    replays it keeps the memory and the order."""
+
+    def __init__(self, dev: int, *tensors):
+        self.dev, self.tensors, self.home = dev, tensors, torch.cuda.current_stream(dev)
+        self.known, self.events = {self.home.cuda_stream}, {}
+
+    def begin(self, stream):
+        """Before a call on ``stream``; what it returns goes to ``end`` after it."""
+        if stream is None:
+            raw = _raw_stream(self.dev)
+        else:
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if raw in self.known:
+            return None
+        s = torch.cuda.current_stream(self.dev) if stream is None else _torch_stream(stream, self.dev)
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return None
+        if raw not in self.events:
+            s.wait_stream(self.home)
+            if s.cuda_stream == 0 or s.stream_id != s.cuda_stream:  # not the caller's: those go by their handle
+                for t in self.tensors:
+                    t.record_stream(s)
+                self.known.add(raw)
+                return None
+            if not self.events:
+                weakref.finalize(self, _wait_for, self.home, self.events).atexit = False
+            self.events[raw] = torch.cuda.Event()
+        return self.events[raw], s
+
+    def end(self, used):
+        if used is not None:
+            used[0].record(used[1])
+
+
+def _wait_for(stream, events):
+    for e in events.values():
+        stream.wait_event(e)
 
 
 def _dims(kv_pages: torch.Tensor, num_qo_heads: int) -> _Dims:
@@ -1015,7 +1064,8 @@ class BatchAttentionQ4:
     table's host copies, then append, run or step on it.  ``run`` plans first when
     ``plan`` has not been called.  Runs of one object share its workspace and must
     be ordered on the GPU; append and run can be captured into a CUDA graph, plan
-    cannot."""
+    cannot.  The object may be dropped while a run is under way; a graph that holds
+    one needs it until its last replay has ended."""
 
     def __init__(self, table: PageTable, num_qo_heads: int, kv_pages: torch.Tensor, causal=True,
                  sm_scale=None, kv_exp=None):
@@ -1037,14 +1087,19 @@ class BatchAttentionQ4:
                                                  d.head_dim, d.page_size, d.num_pages)
         self.shape = (int(table.h_qo_indptr[-1]), d.num_qo_heads, d.head_dim)
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=kv_pages.device)
+        self._use = _StreamUse(self.dev, self.workspace)
         self.info = None
 
     def plan(self, stream=None):
         """Upload the batch's plan; later runs (one per layer) reuse it."""
         t, info = self.t, PlanInfo()
-        _call(load_library().daa_batch_attention_q4_plan, "batch_attention_q4_plan", self.dev, stream,
-              _ptr(t.h_qo_indptr), _ptr(t.h_kv_indptr), _ptr(t.h_last_page_len), len(t.h_qo_indptr) - 1,
-              self.dims, self.workspace.data_ptr(), self.workspace.numel(), ctypes.byref(info))
+        used = self._use.begin(stream)
+        try:
+            _call(load_library().daa_batch_attention_q4_plan, "batch_attention_q4_plan", self.dev, stream,
+                  _ptr(t.h_qo_indptr), _ptr(t.h_kv_indptr), _ptr(t.h_last_page_len), len(t.h_qo_indptr) - 1,
+                  self.dims, self.workspace.data_ptr(), self.workspace.numel(), ctypes.byref(info))
+        finally:
+            self._use.end(used)
         self.info = info
         return info
 
@@ -1073,9 +1128,13 @@ class BatchAttentionQ4:
         if self.info is None:
             self.plan(stream)
         exp = None if self.kv_exp is None else self.kv_exp.data_ptr()
-        _call(load_library().daa_batch_attention_q4_run, "batch_attention_q4", dev, stream, pq,
-              self.kv_pages.data_ptr(), exp, self.t.page_indices.data_ptr(), self.info, self.causal, self.sm_scale,
-              po, pl, self.workspace.data_ptr(), self.workspace.numel(), d)
+        used = self._use.begin(stream)
+        try:
+            _call(load_library().daa_batch_attention_q4_run, "batch_attention_q4", dev, stream, pq,
+                  self.kv_pages.data_ptr(), exp, self.t.page_indices.data_ptr(), self.info, self.causal,
+                  self.sm_scale, po, pl, self.workspace.data_ptr(), self.workspace.numel(), d)
+        finally:
+            self._use.end(used)
         return out
 
     def step(self, k_new, v_new, q, out=None, lse=None, stream=None):

@@ -82,6 +82,67 @@ def test_lengths_are_read_on_the_stream_of_the_call(daa, raw):
     assert pool.counters.tolist() == [pool.h_free, 0] and pool.h_free == len(st["free"]) + 9
 
 
+def _chunk(daa, hq=32, hkv=8, d=128, cached=3001, new=700):
+    """A chunk whose workspace is large (its pages in bf16): more than 10 MB, so a block of its own."""
+    rng = np.random.default_rng(1)
+    t, n = ref.make_table(rng, [cached, 20], [new, 1])
+    pool = np.concatenate([rng.integers(0, 256, (n, hkv, 2, 8 * d), dtype=np.uint8),
+                           rng.integers(40, 64, (n, hkv, 2, d), dtype=np.uint8)], -1)
+    table = daa.PageTable.from_host(*(t[x] for x in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len")), DEV)
+    q = torch.from_numpy(rng.standard_normal((new + 1, hq, d))).bfloat16().to(DEV)
+    return table, _dev(pool), q
+
+
+def test_workspace_outlives_its_object(daa):
+    """An object dropped while its run is under way: its workspace is nobody else's until the run has ended."""
+    table, pages, q = _chunk(daa)
+    want = daa.BatchAttentionQ4(table, q.shape[1], pages).run(q)
+    out, s = torch.empty_like(want), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        attn = daa.BatchAttentionQ4(table, q.shape[1], pages)
+        n, at = attn.workspace.numel(), attn.workspace.data_ptr()
+        assert n > 10 << 20
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(BUSY)
+        attn.run(q, out=out, stream=stream)
+        pending = not s.query()
+        del attn
+        other = torch.empty(n, dtype=torch.uint8, device=DEV)  # never written
+        # not this memory, or on a stream that waits for the run
+        safe = other.data_ptr() != at or not torch.cuda.current_stream().query()
+        s.synchronize()
+        assert pending and safe
+        assert torch.equal(out, want)
+        del other
+        torch.cuda.synchronize()
+
+
+def test_workspace_waits_for_what_its_memory_was(daa):
+    """A workspace in memory that the constructor's stream still writes for a tensor freed before."""
+    table, pages, q = _chunk(daa)
+    attn = daa.BatchAttentionQ4(table, q.shape[1], pages)
+    want = attn.run(q)
+    n, head = attn.workspace.numel(), attn.workspace[:256].clone()  # of the plan
+    del attn
+    s = torch.cuda.Stream()
+    before = torch.empty(n, dtype=torch.uint8, device=DEV)
+    at = before.data_ptr()
+    before.fill_(7)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    before.fill_(7)
+    del before
+    attn = daa.BatchAttentionQ4(table, q.shape[1], pages)
+    assert attn.workspace.data_ptr() == at and not torch.cuda.current_stream().query()
+    attn.plan(stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(attn.workspace[:256], head)
+    out = attn.run(q, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_steps_of_two_pools_in_two_threads(daa):
     """Steps of different sizes prepared at the same time: neither changes what the other is launched with."""
     import threading

@@ -845,7 +845,9 @@ class PagePool:
     ``step`` is the call of a serving loop: it checks the lengths on the host,
     raises before anything is launched when they do not fit, and returns a
     ``PageTable``.  ``build`` is the kernel alone, on device arrays.  Calls on one
-    pool must be ordered on the GPU (one stream, or events between streams)."""
+    pool must be ordered on the GPU (one stream, or events between streams).  A pool
+    may be dropped while a call on its arrays is under way, but not while a graph
+    that holds one is still to be replayed."""
 
     PAGE_SIZE = 16
 
@@ -856,6 +858,7 @@ class PagePool:
         counters = torch.tensor([num_pages, 0], **i32)
         self._init(torch.zeros(num_slots, **i32), torch.zeros(num_slots, **i32),
                    torch.full((num_slots, max_pages), -1, **i32), free, counters)
+        self._use = _StreamUse(self.dev, self.seq_len, self.held, self.block_table, free, counters)
         self.h_len, self.h_held, self.h_free = (np.zeros(num_slots, np.int64), np.zeros(num_slots, np.int64),
                                                 int(num_pages))
 
@@ -884,6 +887,16 @@ class PagePool:
         self.free_pages, self.counters, self.device = free_pages, counters, seq_len.device
         self._pool = _Pool(*ptrs, seq_len.shape[0], block_table.shape[1], free_pages.shape[0], self.PAGE_SIZE)
         self._pool_ref = ctypes.byref(self._pool)
+        self._use = None  # the caller's arrays: theirs to keep and to order
+
+    def _on_pool(self, stream, fn):
+        """fn(), work on ``stream`` that reads or writes the pool's arrays."""
+        used = self._use.begin(stream) if self._use else None
+        try:
+            fn()
+        finally:
+            if used:
+                self._use.end(used)
 
     def _mirror(self, stream):
         """The host copies, read once behind what the call's stream holds (it may be
@@ -914,8 +927,9 @@ class PagePool:
             p_map, rows = _addr(slot_map, "slot_map", torch.int64, dev), slot_map.numel()
         if positions is not None:
             p_pos, rows = _addr(positions, "positions", i32, dev), min(rows, positions.numel())
-        _call(load_library().daa_step_table, "step_table", dev, stream, self._pool_ref, args[0], args[1], batch,
-              1 if advance else 0, args[2], args[3], args[4], page_indices.numel(), args[5], p_map, p_pos, rows)
+        self._on_pool(stream, lambda: _call(
+            load_library().daa_step_table, "step_table", dev, stream, self._pool_ref, args[0], args[1], batch,
+            1 if advance else 0, args[2], args[3], args[4], page_indices.numel(), args[5], p_map, p_pos, rows))
 
     def step(self, slots, new_lens, advance=True, stream=None) -> PageTable:
         """The page table of a step that brings ``new_lens[i]`` tokens to slot
@@ -965,7 +979,8 @@ class PagePool:
             raise ValueError("lens must have one entry per slot, within the pages the slot holds")
         with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             at = torch.from_numpy(sl).to(self.device)
-            self.seq_len.index_copy_(0, at, torch.from_numpy(ln.astype(np.int32)).to(self.device))
+            to = torch.from_numpy(ln.astype(np.int32)).to(self.device)
+            self._on_pool(stream, lambda: self.seq_len.index_copy_(0, at, to))
         self.h_len[sl] = ln
 
     def release(self, slots, stream=None):
@@ -975,8 +990,8 @@ class PagePool:
         self._check_slots(sl)
         with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             dev = torch.from_numpy(sl.astype(np.int32)).to(self.device)
-            _call(load_library().daa_release_pages, "release_pages", self.dev, stream, self._pool_ref,
-                  dev.data_ptr(), len(sl))
+            self._on_pool(stream, lambda: _call(load_library().daa_release_pages, "release_pages", self.dev, stream,
+                                                self._pool_ref, dev.data_ptr(), len(sl)))
         self.h_free += int(self.h_held[sl].sum())
         self.h_len[sl] = self.h_held[sl] = 0
 

@@ -143,6 +143,29 @@ def test_workspace_waits_for_what_its_memory_was(daa):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_pool_outlives_its_object(daa, raw):
+    """A pool dropped while a call on it is under way on another stream: its arrays are nobody else's until that has ended."""
+    s = torch.cuda.Stream()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    pool = daa.PagePool(1000, 50, 70_000)
+    n, at = pool.block_table.numel(), pool.block_table.data_ptr()
+    a = (torch.tensor([3], **i32), torch.tensor([20], **i32), *(torch.empty(2, **i32) for _ in range(3)), torch.empty(1, **i32))
+    for busy in (0, BUSY):  # a first kernel call may wait for the device
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(busy)
+        pool.build(*a, stream=s.cuda_stream if raw else s)
+    pending = not s.query()
+    del pool
+    other = torch.empty(n, **i32)  # never written
+    # not this memory, or on a stream that waits for the call
+    safe = other.data_ptr() != at or not torch.cuda.current_stream().query()
+    s.synchronize()
+    assert pending and safe
+    assert a[2].tolist() == [0, 20] and a[3].tolist() == [0, 2] and a[4].tolist() == [0, 1]
+
+
 def test_steps_of_two_pools_in_two_threads(daa):
     """Steps of different sizes prepared at the same time: neither changes what the other is launched with."""
     import threading

@@ -673,7 +673,10 @@ class PageTable:
 
 
 class BatchAttention:
-    """Plan-once / run-many wrapper for one batch shape (FlashInfer-style)."""
+    """Plan-once / run-many wrapper for one batch shape (FlashInfer-style).  Calls of
+    one object share its workspace and must be ordered on the GPU.  The object may be
+    dropped while one is under way; a graph that holds one needs it until its last
+    replay has ended."""
 
     def __init__(self, table: PageTable, num_qo_heads: int, kv_pages: torch.Tensor, causal=True,
                  sm_scale=None, prefix_groups=None):
@@ -692,15 +695,20 @@ class BatchAttention:
                                                 table.h_last_page_len, prefix_groups,
                                                 num_qo_heads, hkv, d, p, n)
         self.workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=kv_pages.device)
+        self._use = _StreamUse(self.workspace.get_device(), self.workspace)
         self.info = None  # set by plan(): run() and step() then launch the kernels only
 
     def plan(self, stream=None):
         """Upload the batch's plan once; later run() / step() calls (e.g. one per
         layer) reuse it until the next plan() or a tree-mask run."""
         t = self.t
-        self.info = batch_attention_plan(t.h_qo_indptr, t.h_kv_indptr, t.h_last_page_len, self.Hq,
-                                         self.kv_pages, self.workspace,
-                                         prefix_groups=self.prefix_groups, stream=stream)
+        used = self._use.begin(stream)
+        try:
+            self.info = batch_attention_plan(t.h_qo_indptr, t.h_kv_indptr, t.h_last_page_len, self.Hq,
+                                             self.kv_pages, self.workspace,
+                                             prefix_groups=self.prefix_groups, stream=stream)
+        finally:
+            self._use.end(used)
         return self.info
 
     def append(self, k_new, v_new, stream=None):
@@ -711,6 +719,13 @@ class BatchAttention:
     def step(self, k_new, v_new, q, out=None, lse=None, stream=None):
         """append + run in one call (``append_attention``, or ``append_attention_run``
         on the stored plan)."""
+        used = self._use.begin(stream)
+        try:
+            return self._step(k_new, v_new, q, out, lse, stream)
+        finally:
+            self._use.end(used)
+
+    def _step(self, k_new, v_new, q, out, lse, stream):
         t = self.t
         if self.info is not None:
             return append_attention_run(k_new, v_new, q, self.kv_pages, t.qo_indptr, t.kv_indptr,
@@ -725,6 +740,13 @@ class BatchAttention:
     def run(self, q, out=None, lse=None, stream=None, tree_mask=None):
         """Attention over the batch; with ``tree_mask``, under draft-tree masks
         (``batch_attention_tree``; the batch must be causal)."""
+        used = self._use.begin(stream)
+        try:
+            return self._run(q, out, lse, stream, tree_mask)
+        finally:
+            self._use.end(used)
+
+    def _run(self, q, out, lse, stream, tree_mask):
         t = self.t
         if tree_mask is None and self.info is not None:
             return batch_attention_run(q, self.kv_pages, t.qo_indptr, t.kv_indptr, t.page_indices,

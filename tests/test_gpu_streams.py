@@ -1,0 +1,69 @@
+"""Workspaces of the bf16 calls on streams of the caller's."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BUSY = 200_000_000  # clock cycles, about 0.1 s: what is queued behind them has not run when the test goes on
+
+
+@pytest.fixture(scope="module")
+def daa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import decode_attention_append_gb300 as m
+    m.device_error(reset=True)
+    return m
+
+
+@pytest.fixture(scope="module")
+def batch(daa):
+    """A decode batch whose keys are cut, so that its workspace is large: table, pool, new K, new V, q."""
+    rng = np.random.default_rng(1)
+    n, pages, hq, hkv, d = 64, 400, 32, 8, 128
+    table = daa.PageTable.from_host(np.arange(n + 1), pages * np.arange(n + 1),
+                                    rng.permutation(n * pages).astype(np.int32), np.full(n, 5), DEV)
+    gen = torch.Generator(DEV).manual_seed(1)
+    pool, k, v, q = (torch.randn(s, generator=gen, device=DEV, dtype=torch.bfloat16)
+                     for s in ((n * pages, 2, hkv, 16, d), (n, hkv, d), (n, hkv, d), (n, hq, d)))
+    return table, pool, k, v, q
+
+
+def _calls(attn, b, planned):
+    _, _, k, v, q = b
+    if planned:
+        attn.plan()
+    return {"run": lambda out, s: attn.run(q, out=out, stream=s), "step": lambda out, s: attn.step(k, v, q, out=out, stream=s)}
+
+
+@pytest.mark.parametrize("call", ["run", "step"])
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("raw", [False, True])
+def test_workspace_outlives_its_object(daa, batch, call, planned, raw):
+    """An object dropped while a call is under way: its workspace is nobody else's until that has ended."""
+    table, pool, _, _, q = batch
+    attn = daa.BatchAttention(table, q.shape[1], pool)
+    want = torch.empty_like(q)
+    _calls(attn, batch, planned)[call](want, None)
+    n = attn.workspace.numel()
+    assert n > 1 << 20  # a block of its own
+    del attn
+    s, out = torch.cuda.Stream(), torch.empty_like(q)
+    attn = daa.BatchAttention(table, q.shape[1], pool)
+    at = attn.workspace.data_ptr()
+    run = _calls(attn, batch, planned)[call]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    run(out, s.cuda_stream if raw else s)
+    pending = not s.query()
+    del attn, run
+    other = torch.empty(n, dtype=torch.uint8, device=DEV)  # never written
+    # not this memory, or on a stream that waits for the call
+    safe = other.data_ptr() != at or not torch.cuda.current_stream().query()
+    s.synchronize()
+    assert pending and safe
+    assert torch.equal(out, want) and daa.device_error(reset=True) == 0

@@ -397,7 +397,8 @@ def batch_attention(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_l
     ``host_indptr`` = (h_qo_indptr, h_kv_indptr, h_last_page_len) host copies of
     the page table used for planning; when omitted they are copied from the
     device (a synchronisation).  ``workspace`` (uint8 CUDA tensor) is allocated
-    by torch here when omitted; the library itself never allocates.
+    by torch here when omitted, like ``out`` for the call's stream; the library
+    itself never allocates.
 
     ``prefix_groups`` = (indptr, prefix_len), host int arrays: group i is
     requests [indptr[i], indptr[i+1]) whose first prefix_len[i] keys sit in the
@@ -419,14 +420,16 @@ def batch_attention(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_l
     hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
-        out = torch.empty_like(q)
+        with _use_stream(stream, q.get_device()):
+            out = torch.empty_like(q)
     _dev_bf16(out, "out")
     if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()):
         raise TypeError("lse must be a contiguous fp32 CUDA tensor")
     groups = None if prefix_groups is None else _host_groups(prefix_groups)
     need = _workspace_need(lib, hq, hk, hl, dims, groups, "batch_attention")
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        with _use_stream(stream, q.get_device()):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if groups is None:
         st = lib.daa_batch_attention(_ptr(q), _ptr(kv_pages), _ptr(qo_indptr), _ptr(kv_indptr),
@@ -473,7 +476,8 @@ def batch_attention_tree(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_p
     hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
-        out = torch.empty_like(q)
+        with _use_stream(stream, q.get_device()):
+            out = torch.empty_like(q)
     _dev_bf16(out, "out")
     if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()):
         raise TypeError("lse must be a contiguous fp32 CUDA tensor")
@@ -483,7 +487,8 @@ def batch_attention_tree(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_p
                                                       ctypes.byref(st))
         _check(st.value, "batch_attention_tree")
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            with _use_stream(stream, q.get_device()):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib.daa_batch_attention_tree(_ptr(q), _ptr(kv_pages), _ptr(qo_indptr), _ptr(kv_indptr),
                                         _ptr(page_indices), _ptr(last_page_len), _ptr(hq), _ptr(hk),
@@ -519,7 +524,8 @@ def append_attention(k_new, v_new, q, kv_pages, qo_indptr, kv_indptr, page_indic
     hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
-        out = torch.empty_like(q)
+        with _use_stream(stream, q.get_device()):
+            out = torch.empty_like(q)
     _dev_bf16(out, "out")
     if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()):
         raise TypeError("lse must be a contiguous fp32 CUDA tensor")
@@ -527,7 +533,8 @@ def append_attention(k_new, v_new, q, kv_pages, qo_indptr, kv_indptr, page_indic
     if workspace is None:
         need = _workspace_need(lib, hq, hk, hl, dims, groups, "append_attention")
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            with _use_stream(stream, q.get_device()):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if groups is None:
         st = lib.daa_append_attention(_ptr(k_new), _ptr(v_new), _ptr(q), _ptr(kv_pages),
@@ -565,7 +572,8 @@ def batch_attention_noalloc(q, kv_pages, qo_indptr, kv_indptr, page_indices, las
         sm_scale = 1.0 / float(d) ** 0.5
     hq, hk, hl = (_host_i32(x) for x in host_indptr)
     if out is None:
-        out = torch.empty_like(q)
+        with _use_stream(stream, q.get_device()):
+            out = torch.empty_like(q)
     _dev_bf16(out, "out")
     if out.shape != q.shape:
         raise ValueError("out must have the shape of q")
@@ -602,13 +610,14 @@ def batch_attention_plan(h_qo_indptr, h_kv_indptr, h_last_page_len, num_qo_heads
     return info
 
 
-def _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse):
+def _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse, stream):
     _dev_bf16(q, "q"), _dev_bf16(kv_pages, "kv_pages")
     for n, t in (("qo_indptr", qo_indptr), ("kv_indptr", kv_indptr), ("page_indices", page_indices),
                  ("last_page_len", last_page_len)):
         _dev_i32(t, n)
     if out is None:
-        out = torch.empty_like(q)
+        with _use_stream(stream, q.get_device()):
+            out = torch.empty_like(q)
     _dev_bf16(out, "out")
     if lse is not None and not (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()):
         raise TypeError("lse must be a contiguous fp32 CUDA tensor")
@@ -619,7 +628,7 @@ def batch_attention_run(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_pa
                         workspace, causal=True, sm_scale=None, out=None, lse=None, stream=None):
     """Attention on a plan made by ``batch_attention_plan`` (kernels only)."""
     lib = load_library()
-    out = _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse)
+    out = _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse, stream)
     if sm_scale is None:
         sm_scale = 1.0 / float(q.shape[2]) ** 0.5
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -637,7 +646,7 @@ def append_attention_run(k_new, v_new, q, kv_pages, qo_indptr, kv_indptr, page_i
     """``append_attention`` on a plan made by ``batch_attention_plan``."""
     lib = load_library()
     _dev_bf16(k_new, "k_new"), _dev_bf16(v_new, "v_new")
-    out = _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse)
+    out = _run_args(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_len, out, lse, stream)
     if sm_scale is None:
         sm_scale = 1.0 / float(q.shape[2]) ** 0.5
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

@@ -67,3 +67,35 @@ def test_workspace_outlives_its_object(daa, batch, call, planned, raw):
     s.synchronize()
     assert pending and safe
     assert torch.equal(out, want) and daa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("call", ["attention", "append", "tree", "run", "noalloc"])
+def test_what_a_call_allocates_is_its_streams(daa, batch, call):
+    """Output and workspace that a call makes are the named stream's memory: given back when the call returns, they are
+    nobody else's before the stream has come to it."""
+    table, pool, k, v, q = batch
+    host = (table.h_qo_indptr, table.h_kv_indptr, table.h_last_page_len)
+    dev = (table.qo_indptr, table.kv_indptr, table.page_indices, table.last_page_len)
+    attn = daa.BatchAttention(table, q.shape[1], pool)
+    need = attn.workspace.numel()
+    if call == "run":
+        attn.plan()
+    mask = torch.ones(q.shape[0], 1, dtype=torch.int32, device=DEV)
+    calls = {"attention": lambda s: daa.batch_attention(q, pool, *dev, host_indptr=host, stream=s),
+             "append": lambda s: daa.append_attention(k, v, q, pool, *dev, host_indptr=host, stream=s),
+             "tree": lambda s: daa.batch_attention_tree(q, pool, *dev, mask, host_indptr=host, stream=s),
+             "run": lambda s: attn.run(q, stream=s),
+             "noalloc": lambda s: daa.batch_attention_noalloc(q, pool, *dev, host, stream=s)}
+    want = calls[call](None)
+    torch.cuda.synchronize()
+    for raw in (False, True):
+        s = torch.cuda.Stream()
+        held = lambda: sum(x["total_size"] for x in torch.cuda.memory_snapshot() if x["stream"] == s.cuda_stream)  # noqa: E731
+        torch.cuda.empty_cache()
+        before = held()
+        out = calls[call](s.cuda_stream if raw else s)
+        made = held() - before
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        assert made >= out.numel() * 2 + (need if call in ("attention", "append", "tree") else 0)
+    assert daa.device_error(reset=True) == 0

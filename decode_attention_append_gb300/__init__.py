@@ -396,7 +396,7 @@ def batch_attention(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_l
 
     ``host_indptr`` = (h_qo_indptr, h_kv_indptr, h_last_page_len) host copies of
     the page table used for planning; when omitted they are copied from the
-    device (a synchronisation).  ``workspace`` (uint8 CUDA tensor) is allocated
+    device on the call's stream (a synchronisation).  ``workspace`` (uint8 CUDA tensor) is allocated
     by torch here when omitted, like ``out`` for the call's stream; the library
     itself never allocates.
 
@@ -417,7 +417,8 @@ def batch_attention(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_page_l
         sm_scale = 1.0 / float(d) ** 0.5
     if host_indptr is None:
         host_indptr = (qo_indptr, kv_indptr, last_page_len)
-    hq, hk, hl = (_host_i32(x) for x in host_indptr)
+    with _use_stream(stream, q.get_device()):
+        hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
         with _use_stream(stream, q.get_device()):
@@ -473,7 +474,8 @@ def batch_attention_tree(q, kv_pages, qo_indptr, kv_indptr, page_indices, last_p
         sm_scale = 1.0 / float(d) ** 0.5
     if host_indptr is None:
         host_indptr = (qo_indptr, kv_indptr, last_page_len)
-    hq, hk, hl = (_host_i32(x) for x in host_indptr)
+    with _use_stream(stream, q.get_device()):
+        hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
         with _use_stream(stream, q.get_device()):
@@ -521,7 +523,8 @@ def append_attention(k_new, v_new, q, kv_pages, qo_indptr, kv_indptr, page_indic
         sm_scale = 1.0 / float(d) ** 0.5
     if host_indptr is None:
         host_indptr = (qo_indptr, kv_indptr, last_page_len)
-    hq, hk, hl = (_host_i32(x) for x in host_indptr)
+    with _use_stream(stream, q.get_device()):
+        hq, hk, hl = (_host_i32(x) for x in host_indptr)
     batch = len(hq) - 1
     if out is None:
         with _use_stream(stream, q.get_device()):

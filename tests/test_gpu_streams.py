@@ -99,3 +99,24 @@ def test_what_a_call_allocates_is_its_streams(daa, batch, call):
         assert torch.equal(out, want)
         assert made >= out.numel() * 2 + (need if call in ("attention", "append", "tree") else 0)
     assert daa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("call", ["attention", "append", "tree"])
+@pytest.mark.parametrize("raw", [False, True])
+def test_lengths_are_read_on_the_stream_of_the_call(daa, batch, call, raw):
+    """Without host copies a call reads the table from the device: behind what its stream holds."""
+    table, pool, k, v, q = batch
+    src = (table.qo_indptr, table.kv_indptr, table.page_indices, table.last_page_len)
+    mask = torch.ones(q.shape[0], 1, dtype=torch.int32, device=DEV)
+    calls = {"attention": daa.batch_attention, "append": lambda *a, **kw: daa.append_attention(k, v, *a, **kw),
+             "tree": lambda *a, **kw: daa.batch_attention_tree(*a, mask, **kw)}
+    want = calls[call](q, pool, *src)
+    dst, s = [torch.zeros_like(x) for x in src], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+        for d, x in zip(dst, src):
+            d.copy_(x)
+    out = calls[call](q, pool, *dst, stream=s.cuda_stream if raw else s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and daa.device_error(reset=True) == 0

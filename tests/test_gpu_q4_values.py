@@ -1,8 +1,10 @@
-"""Attention over the 4-bit cache where scales leave fp32's range."""
+"""Attention over the 4-bit cache where wrong values are small next to a context, or scales
+leave fp32's range."""
 import numpy as np
 import pytest
 import torch
 
+import q4_bounds
 import q4_support as ref
 
 pytestmark = pytest.mark.gpu
@@ -41,6 +43,47 @@ def _table(daa, t):
 
 def _bf16(rng, shape, scale=1.0):
     return torch.from_numpy(rng.standard_normal(shape) * scale).bfloat16()
+
+
+@pytest.mark.parametrize("hq,hkv,d,cached,new,causal,bf16", [
+    (2, 2, 128, [5003], [1], True, False), (4, 1, 128, [9001, 4095], [1, 1], True, False),
+    (16, 1, 64, [3001], [4], True, False), (8, 1, 128, [2500], [3], True, False),
+    (12, 4, 64, [1500, 700, 0], [1, 5, 3], True, False), (8, 1, 128, [700], [12], False, False),
+    (7, 1, 64, [3860], [108], True, False),
+    (24, 8, 64, [1700], [84], True, True), (32, 8, 64, [77], [500], True, True), (16, 4, 128, [100], [300], True, True),
+])
+def test_every_v_page_counts_once(daa, hq, hkv, d, cached, new, causal, bf16):
+    """V zero but for one page, at every page in turn: left out, counted twice, negated or taken from elsewhere it is off
+    by more than the bounds, which are relative to that page."""
+    rng = np.random.default_rng(40 + hq)
+    t, n = ref.make_table(rng, cached, new)
+    pool = _pool(rng, n, hkv, d)
+    q = _bf16(rng, (int(t["qo_indptr"][-1]), hq, d))
+    scale = 1 / d ** 0.5
+    B = ref.attention(q.double().numpy(), pool, t, None, d, scale, causal)[3].max()
+    dev = _dev(pool)
+    scales = dev[:, :, 1, 8 * d:].clone()
+    dev[:, :, 1, 8 * d:] = 0
+    attn = daa.BatchAttentionQ4(_table(daa, t), hq, dev, causal=causal)
+    qd = q.to(DEV)
+    daa.trace_enable(16)
+    try:
+        attn.run(qd)
+        assert ("kv_dequant_q4" in [x for x, _ in daa.trace_read()]) == bf16
+    finally:
+        daa.trace_disable()
+    for r in range(len(new)):
+        rows = slice(t["qo_indptr"][r], t["qo_indptr"][r + 1])
+        outs = []
+        for page in t["page_indices"][t["kv_indptr"][r]:t["kv_indptr"][r + 1]].tolist():
+            dev[page, :, 1, 8 * d:] = scales[page]
+            out = attn.run(qd)
+            dev[page, :, 1, 8 * d:] = 0
+            outs.append(out[rows].clone())
+            out[rows] = 0
+            assert not out.any()  # nobody else's page
+        want = q4_bounds.by_page(q.double().numpy(), pool, t, r, d, scale, causal)
+        q4_bounds.check_by_page(torch.stack(outs).double().cpu().numpy(), want, B, d, q4_bounds.BF16 if bf16 else q4_bounds.FP16)
 
 
 @pytest.mark.parametrize("size,scale,e,zero_keys", [

@@ -1,5 +1,5 @@
 """Attention over the 4-bit cache where wrong values are small next to a context, or scales
-leave fp32's range."""
+leave fp32's range; and the places that step tables name, against what the append wrote there."""
 import numpy as np
 import pytest
 import torch
@@ -109,3 +109,24 @@ def test_scales_at_the_ends_of_their_range(daa, hq, hkv, size, scale, e, zero_ke
     used = 1 / d ** 0.5 if scale is None else float(np.float32(scale))
     want = ref.attention(q.double().numpy(), pool, t, exps, d, used)
     ref.check_attention(out.double().cpu().numpy(), lse.double().cpu().numpy(), want, d)
+
+
+def test_slot_map_names_the_appended_rows(daa):
+    """Every new token's quantised K and V at the page and slot that its step's table names."""
+    rng = np.random.default_rng(42)
+    hkv, d = 3, 64
+    pool, cache = daa.PagePool(90, 5, 30), daa.new_q4_pool(90, hkv, d)
+    exps = rng.integers(-3, 4, (2, hkv)).astype(np.int32)
+    for slots, new in (([2, 0], [37, 1]), ([0, 3, 2], [16, 50, 1]), ([3, 0], [1, 9])):
+        table = pool.step(slots, new)
+        rows = sum(new)
+        k, v = _bf16(rng, (rows, hkv, d)), _bf16(rng, (rows, hkv, d), 0.1)
+        daa.kv_append_q4(k.to(DEV), v.to(DEV), cache, table.qo_indptr, table.page_indices, table.kv_indptr,
+                         table.last_page_len, kv_exp=_dev(exps))
+        page, slot = np.divmod(table.slot_map.cpu().numpy(), 16)
+        got = daa.kv_dequant_q4(cache, _dev(page.astype(np.int32)), kv_exp=_dev(exps)).double().cpu().numpy()
+        got = got[np.arange(rows), :, :, slot]  # [rows, 2, Hkv, d]
+        for i, x in enumerate((k, v)):
+            code, sc = ref.quantise(x.double().numpy(), np.broadcast_to(exps[i], (rows, hkv)))
+            val = np.where(code >= 8, -1.0, 1.0) * ref.E2M1[code & 7] * np.repeat(ref.E4M3[sc], 16, -1) * 2.0 ** exps[i][:, None]
+            assert np.array_equal(got[:, i], val)

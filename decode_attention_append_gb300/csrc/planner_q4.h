@@ -257,6 +257,9 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     }
   }
   // the bf16 requests: their own plan, then its query rows moved to their place in the batch
+  // (tiles and merges: a request of more rows than a group has heads has several tokens, and
+  // those are never CUDA-core units)
+  static_assert(kQ4NativeRows >= 16, "the largest group");
   daa_dims sd = d;
   sd.num_pages = std::max<int64_t>(1, (int64_t)pl.src.size());
   st = plan_batch(pl.sub_qo.data(), pl.sub_kv.data(), pl.sub_last.data(), (int32_t)pl.req.size(), sd,
@@ -266,10 +269,6 @@ daa_status plan_batch_q4(const int32_t* qo, const int32_t* kv, const int32_t* la
     const int i = (int)(std::upper_bound(pl.sub_qo.begin(), pl.sub_qo.end(), row) - pl.sub_qo.begin()) - 1;
     return row + qo[pl.req[i]] - pl.sub_qo[i];
   };
-  for (size_t i = 0; i < pl.sub_units.size(); ++i) {
-    DecodeUnit& u = pl.sub_units.data()[i];
-    u.q_row = moved(u.q_row);
-  }
   for (size_t i = 0; i < pl.sub_merges.size(); ++i) {
     MergeItem& m = pl.sub_merges.data()[i];
     m.q_row = moved(m.q_row);

@@ -923,15 +923,6 @@ class PagePool:
         self._pool_ref = ctypes.byref(self._pool)
         self._use = None  # the caller's arrays: theirs to keep and to order
 
-    def _on_pool(self, stream, fn):
-        """fn(), work on ``stream`` that reads or writes the pool's arrays."""
-        used = self._use.begin(stream) if self._use else None
-        try:
-            fn()
-        finally:
-            if used:
-                self._use.end(used)
-
     def _mirror(self, stream):
         """The host copies, read once behind what the call's stream holds (it may be
         what fills the arrays)."""
@@ -961,9 +952,13 @@ class PagePool:
             p_map, rows = _addr(slot_map, "slot_map", torch.int64, dev), slot_map.numel()
         if positions is not None:
             p_pos, rows = _addr(positions, "positions", i32, dev), min(rows, positions.numel())
-        self._on_pool(stream, lambda: _call(
-            load_library().daa_step_table, "step_table", dev, stream, self._pool_ref, args[0], args[1], batch,
-            1 if advance else 0, args[2], args[3], args[4], page_indices.numel(), args[5], p_map, p_pos, rows))
+        used = self._use and self._use.begin(stream)
+        try:
+            _call(load_library().daa_step_table, "step_table", dev, stream, self._pool_ref, args[0], args[1], batch,
+                  1 if advance else 0, args[2], args[3], args[4], page_indices.numel(), args[5], p_map, p_pos, rows)
+        finally:
+            if used:
+                self._use.end(used)
 
     def step(self, slots, new_lens, advance=True, stream=None) -> PageTable:
         """The page table of a step that brings ``new_lens[i]`` tokens to slot
@@ -1014,7 +1009,12 @@ class PagePool:
         with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             at = torch.from_numpy(sl).to(self.device)
             to = torch.from_numpy(ln.astype(np.int32)).to(self.device)
-            self._on_pool(stream, lambda: self.seq_len.index_copy_(0, at, to))
+            used = self._use and self._use.begin(stream)
+            try:
+                self.seq_len.index_copy_(0, at, to)
+            finally:
+                if used:
+                    self._use.end(used)
         self.h_len[sl] = ln
 
     def release(self, slots, stream=None):
@@ -1024,8 +1024,13 @@ class PagePool:
         self._check_slots(sl)
         with torch.cuda.device(self.dev), _use_stream(stream, self.dev):
             dev = torch.from_numpy(sl.astype(np.int32)).to(self.device)
-            self._on_pool(stream, lambda: _call(load_library().daa_release_pages, "release_pages", self.dev, stream,
-                                                self._pool_ref, dev.data_ptr(), len(sl)))
+            used = self._use and self._use.begin(stream)
+            try:
+                _call(load_library().daa_release_pages, "release_pages", self.dev, stream, self._pool_ref,
+                      dev.data_ptr(), len(sl))
+            finally:
+                if used:
+                    self._use.end(used)
         self.h_free += int(self.h_held[sl].sum())
         self.h_len[sl] = self.h_held[sl] = 0
 

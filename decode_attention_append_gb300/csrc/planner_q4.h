@@ -22,8 +22,8 @@
 namespace daa {
 
 // GB300, 8 kv heads, d = 128, 32 requests of 2500 keys, 4 and 8 heads a kv head: 96
-// rows 140 us from the 4-bit pages and 157 to 164 by way of bf16, 128 rows 206 and 161
-// to 168.
+// rows 118 us from the 4-bit pages and 133 to 146 by way of bf16, 128 rows 165 to 168 and
+// 134 to 151.
 constexpr int kQ4NativeRows = 96;
 // Rows a unit holds at most: more would spill the register kernel's sums (GB300, a
 // further page on an SM: 52, 74 and 92 ns with 8, 16 and 24 rows).  Where all units of 8
@@ -41,9 +41,10 @@ constexpr int kQ4UnitPages[kQ4Classes] = {5, 7, 7};
 // 13 ns a key); 24-row units read the pages again for every 24 rows, but on every SM.
 // Requests of two 128-row tiles at most (`split`) have their keys cut there, too.
 // Measured on GB300 at 274 points (rows 128 to 2048, keys 100 to 16000, 1 to 32 kv
-// heads, 1 to 8 chunks, with and without decode beside them): taken at 170 of them, 1.7
-// times as fast on average there, 7.6 at best (252 rows, 1 kv head, 16000 keys: 27 us and
-// 205) and 0.9 at worst (2048 rows, 2 kv heads, 1256 keys: 32 and 29).
+// heads, 1 to 8 chunks, with and without decode beside them): taken at 170 of them, 1.83
+// times as fast on average there, 9.4 at best (252 rows, 1 kv head of 64 dims, 16000 keys:
+// 18.8 us and 176) and 1.01 at worst (126 rows, 5 kv heads, 118 keys: 10.4 and 10.5); 1.45
+// over all points.  Where it is not taken it would be 1.35 at best.
 inline bool few_chunks_q4(int64_t warps, int64_t keys, bool split, int sms) {
   if (5 * warps <= 3 * (int64_t)sms) return !split || warps * keys <= 150000;
   return !split && warps <= 2 * (int64_t)sms - 160000 / keys;

@@ -611,13 +611,23 @@ daa_status daa_release_pages(const daa_page_pool* pool, const int32_t* slots, in
  *
  * daa_batch_attention_q4_*: daa_batch_attention over a 4-bit pool, planned once
  * and run many times (see daa_batch_attention_plan and _run: same plan rules,
- * workspace, masks, outputs and errors).  The result is that of
- * daa_batch_attention on the pool's values in bf16, up to fp32 rounding order
- * and the rounding of the softmax weights.  Slots past a request's last token
- * may hold anything.  Requests of up to 96 packed (token, query head) rows are
- * read from the 4-bit pages, and longer chunks where a batch has few of them;
- * else their pages are written to the workspace in bf16 first (2 * Hkv *
- * head_dim * 32 bytes a page), each once.
+ * workspace, causal mask, outputs and errors).  Draft-tree masks and shared-prefix
+ * groups have no form of this; daa_kv_dequant_q4 gives pages that the bf16 calls
+ * take.  The result is that of daa_batch_attention on the pool's values in bf16,
+ * up to fp32 rounding order and the rounding of the softmax weights.  Slots past a
+ * request's last token may hold anything.
+ * Requests of up to 96 packed (token, query head) rows are read from the 4-bit
+ * pages, with weights rounded to fp16 (2^-11 of a weight), and so are longer
+ * chunks where a batch has few of them.  The pages of the other chunks are written
+ * to the workspace in bf16 by every run (2 * Hkv * head_dim * 32 bytes a page; a
+ * page that two such requests share is written for each), and their weights are
+ * rounded to bf16 (2^-8).  The plan decides from the whole batch, so a chunk's last
+ * bits may depend on what else is in it.
+ * What the cache gains is decode and verify speed: from about 64 rows a request on,
+ * a batch of many requests is slower than daa_batch_attention on bf16 pages
+ * (GB300, 32 requests of 2500 keys, 8 kv heads of 128 dims: 25.7 us and 62.2 at 4
+ * rows, 65 and 68 at 48, 91 and 71 at 64, 118 and 66 to 77 at 96, 150 and 83 at 256).
+ * Scores are fp32: a row with a scaled score past 2^26 in magnitude is undefined.
  *  plan: host arrays of daa_batch_attention; the workspace (at least
  *        daa_batch_attention_q4_workspace_size bytes, 256-byte aligned); `info`.
  *        It copies from host memory, so it cannot be captured into a CUDA graph

@@ -251,12 +251,12 @@ def _current_device() -> int:
 
 def _torch_stream(stream, dev: int):
     """A call's stream on CUDA device `dev` as torch's: a stream of torch's, or a
-    cudaStream_t (0 and 1 are the handles of the default stream)."""
-    if hasattr(stream, "cuda_stream"):
+    cudaStream_t, alone or as an object's ``cuda_stream`` (0 and 1 are the handles of
+    the default stream)."""
+    if isinstance(stream, torch.cuda.Stream):
         return stream
-    if int(stream) in (0, 1):
-        return torch.cuda.default_stream(dev)
-    return torch.cuda.ExternalStream(int(stream), device=dev)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.default_stream(dev) if raw in (0, 1) else torch.cuda.ExternalStream(raw, device=dev)
 
 
 def _use_stream(stream, dev: int):

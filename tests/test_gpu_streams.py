@@ -120,3 +120,21 @@ def test_lengths_are_read_on_the_stream_of_the_call(daa, batch, call, raw):
     out = calls[call](q, pool, *dst, stream=s.cuda_stream if raw else s)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and daa.device_error(reset=True) == 0
+
+
+def test_streams_of_other_libraries(daa, batch):
+    """An object with a cuda_stream handle is a stream, as an integer is."""
+    table, pool, k, v, q = batch
+    host = (table.h_qo_indptr, table.h_kv_indptr, table.h_last_page_len)
+    dev = (table.qo_indptr, table.kv_indptr, table.page_indices, table.last_page_len)
+    s = torch.cuda.Stream()
+
+    class Stream:
+        cuda_stream = s.cuda_stream
+    want = daa.batch_attention(q, pool, *dev, host_indptr=host)
+    attn, copy = daa.BatchAttention(table, q.shape[1], pool), pool.clone()
+    torch.cuda.synchronize()
+    outs = [daa.batch_attention(q, pool, *dev, stream=Stream()),
+            daa.append_attention(k, v, q, copy, *dev, host_indptr=host, stream=Stream()), attn.run(q, stream=Stream())]
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[2], want) and daa.device_error(reset=True) == 0

@@ -275,11 +275,14 @@ class _StreamUse:
     replays it keeps the memory and the order."""
 
     def __init__(self, dev: int, *tensors):
-        self.dev, self.tensors, self.home = dev, tensors, torch.cuda.current_stream(dev)
-        self.known, self.events = {self.home.cuda_stream}, {}
+        self.dev, self.tensors = dev, tensors
+        self.home = torch.cuda.current_stream(dev) if dev >= 0 else None
+        self.known, self.events = {self.home.cuda_stream if self.home else None}, {}
 
     def begin(self, stream):
         """Before a call on ``stream``; what it returns goes to ``end`` after it."""
+        if self.home is None:  # host memory: the call itself will refuse it
+            return None
         if stream is None:
             raw = _raw_stream(self.dev)
         else:
@@ -287,9 +290,8 @@ class _StreamUse:
         if raw in self.known:
             return None
         s = torch.cuda.current_stream(self.dev) if stream is None else _torch_stream(stream, self.dev)
-        with torch.cuda.stream(s):
-            if torch.cuda.is_current_stream_capturing():
-                return None
+        if _capturing(s):
+            return None
         if raw not in self.events:
             s.wait_stream(self.home)
             if s.cuda_stream == 0 or s.stream_id != s.cuda_stream:  # not the caller's: those go by their handle
@@ -298,7 +300,7 @@ class _StreamUse:
                 self.known.add(raw)
                 return None
             if not self.events:
-                weakref.finalize(self, _wait_for, self.home, self.events).atexit = False
+                weakref.finalize(self, _give_back, self.home, self.events, self.tensors).atexit = False
             self.events[raw] = torch.cuda.Event()
         return self.events[raw], s
 
@@ -307,9 +309,23 @@ class _StreamUse:
             used[0].record(used[1])
 
 
-def _wait_for(stream, events):
-    for e in events.values():
-        stream.wait_event(e)
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+_late: list = []  # memory dropped while its stream was being captured, which cannot wait then
+
+
+def _give_back(stream, events, tensors):
+    _late.append((stream, events, tensors))
+    held, _late[:] = _late[:], []
+    for item in held:
+        if _capturing(item[0]):
+            _late.append(item)
+            continue
+        for e in item[1].values():
+            item[0].wait_event(e)
 
 
 def _dims(kv_pages: torch.Tensor, num_qo_heads: int) -> _Dims:

@@ -138,3 +138,31 @@ def test_streams_of_other_libraries(daa, batch):
             daa.append_attention(k, v, q, copy, *dev, host_indptr=host, stream=Stream()), attn.run(q, stream=Stream())]
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want) and torch.equal(outs[2], want) and daa.device_error(reset=True) == 0
+
+
+def test_object_dropped_during_a_capture(daa, batch):
+    """An object that ran on the caller's stream, dropped while its own stream is being captured: the capture goes on, and the
+    memory is kept for later."""
+    table, pool, _, _, q = batch
+    home, s = torch.cuda.Stream(), torch.cuda.Stream()
+    want = daa.BatchAttention(table, q.shape[1], pool).run(q)
+    x = torch.zeros(4, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(home):
+        attn = daa.BatchAttention(table, q.shape[1], pool)
+    out = attn.run(q, stream=s.cuda_stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=home):
+        x.add_(1)
+        del attn
+        x.add_(1)
+    assert len(daa._late) == 1
+    with torch.cuda.stream(home):
+        other = daa.BatchAttention(table, q.shape[1], pool)
+    again = other.run(q, stream=s.cuda_stream)
+    del other
+    assert not daa._late
+    graph.replay()
+    torch.cuda.synchronize()
+    assert x.tolist() == [2.0] * 4
+    assert torch.equal(out, want) and torch.equal(again, want) and daa.device_error(reset=True) == 0

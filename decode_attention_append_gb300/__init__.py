@@ -293,7 +293,8 @@ class _StreamUse:
         if _capturing(s):
             return None
         if raw not in self.events:
-            s.wait_stream(self.home)
+            if not _capturing(self.home):  # s would become part of that capture
+                s.wait_stream(self.home)
             if s.cuda_stream == 0 or s.stream_id != s.cuda_stream:  # not the caller's: those go by their handle
                 for t in self.tensors:
                     t.record_stream(s)

@@ -166,3 +166,25 @@ def test_object_dropped_during_a_capture(daa, batch):
     torch.cuda.synchronize()
     assert x.tolist() == [2.0] * 4
     assert torch.equal(out, want) and torch.equal(again, want) and daa.device_error(reset=True) == 0
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_first_call_on_a_stream_beside_a_capture(daa, batch, raw):
+    """A call on a stream of its own while the constructor's stream is being captured stays out of the capture."""
+    table, pool, _, _, q = batch
+    home, s = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(home):
+        attn = daa.BatchAttention(table, q.shape[1], pool)
+        attn.plan()
+    want, out, x = attn.run(q, stream=home), torch.zeros_like(q), torch.zeros(4, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=home):
+        x.add_(1)
+        attn.run(q, out=out, stream=s.cuda_stream if raw else s)
+    s.synchronize()
+    assert torch.equal(out, want)  # it ran, and not as part of the graph
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not out.any() and x.tolist() == [1.0] * 4 and daa.device_error(reset=True) == 0

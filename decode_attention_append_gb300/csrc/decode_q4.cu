@@ -29,7 +29,8 @@
 // is raised only when a score passes it by 8) P is at most 2^15.  Sums, maxima
 // and O are fp32.
 //
-// Bound: HBM for 8 rows, instructions for more.  A (page, head) is 18 d bytes; at
+// Bound: HBM for 8 rows; for more, the instructions at the pace that two warps a scheduler
+// (221 and 255 registers) can issue them.  A (page, head) is 18 d bytes; at
 // the measured 6.7 TB/s an SM gets one of d = 128 every 52 ns (about 99 clocks), in
 // which it can issue 400 warp instructions.  A page takes 280 of them with 8 rows, 309
 // with 16 and 389 with 24: 64 conversions and 64 products of the codes, 16 mma for

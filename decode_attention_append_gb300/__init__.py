@@ -22,6 +22,8 @@ Entry points (same names as the C ABI, without the ``daa_`` prefix):
   table there from the requests' lengths, and takes pages back.
 * ``kv_append_q4``, ``kv_dequant_q4``, ``BatchAttentionQ4`` -- append, read-back
   and attention on a KV cache held in 4 bits (``new_q4_pool``).
+* ``Rope``, ``apply_rope``, ``append_rope``, ``append_rope_q4`` -- rotary positions:
+  query and key rows rotated, alone or on the way into either cache.
 
 Tensors: bf16 ``q [nnz_qo, Hq, d]``, ``k_new/v_new [nnz_new, Hkv, d]``, page
 pool ``kv_pages [num_pages, 2, Hkv, page_size, d]`` (K then V, HND inside a
@@ -33,12 +35,15 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 import threading
 import weakref
 from dataclasses import dataclass
 
 import numpy as np
 import torch
+
+from .rope import rope_frequencies
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libdaa.so")
@@ -49,7 +54,8 @@ DAA_OK = 0
 STATUS = {0: "ok", -1: "invalid argument", -2: "shape", -3: "page range", -4: "unsupported",
           -5: "CUDA error", -6: "workspace", -7: "alignment"}
 KERNEL_NAMES = {1: "kv_append", 2: "decode_splitkv", 3: "softmax_merge", 4: "prefill_tc", 5: "decode_tc",
-                6: "short_tc", 7: "step_table", 8: "kv_append_q4", 9: "kv_dequant_q4", 10: "attention_q4"}
+                6: "short_tc", 7: "step_table", 8: "kv_append_q4", 9: "kv_dequant_q4", 10: "attention_q4",
+                11: "rope", 12: "append_rope", 13: "append_rope_q4"}
 
 
 class DaaError(RuntimeError):
@@ -86,6 +92,12 @@ class _Pool(ctypes.Structure):
 class PlanInfo(ctypes.Structure):
     """daa_plan_info: the record of a plan uploaded by ``batch_attention_plan``."""
     _fields_ = [("words", ctypes.c_int64 * 24)]
+
+
+class _Rope(ctypes.Structure):
+    """daa_rope: the frequencies of a rotation."""
+    _fields_ = [("turns", ctypes.c_uint64 * 64), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
 
 
 def library_path() -> str:
@@ -160,6 +172,14 @@ def load_library():
         lib.daa_batch_attention_q4_plan.argtypes = [vp, vp, vp, i32, _Dims, vp, sz, pinfo, vp]
         lib.daa_batch_attention_q4_run.restype = i32
         lib.daa_batch_attention_q4_run.argtypes = [vp, vp, vp, vp, pinfo, i32, f32, vp, vp, vp, sz, _Dims, vp]
+        lib.daa_rope_init.restype = i32
+        lib.daa_rope_init.argtypes = [vp, i32, i32, i32, vp, ctypes.c_double]
+        lib.daa_apply_rope.restype = i32
+        lib.daa_apply_rope.argtypes = [vp, vp, i32, i32, vp]
+        lib.daa_append_rope.restype = i32
+        lib.daa_append_rope.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, _Dims, vp]
+        lib.daa_append_rope_q4.restype = i32
+        lib.daa_append_rope_q4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, _Dims, vp]
         lib.daa_set_prefill_append_fusion.restype = i32
         lib.daa_set_prefill_append_fusion.argtypes = [i32]
         lib.daa_prefill_append_fusion.restype = i32
@@ -745,6 +765,19 @@ class BatchAttention:
         kv_append(k_new, v_new, self.kv_pages, t.qo_indptr, t.page_indices, t.kv_indptr,
                   t.last_page_len, stream=stream)
 
+    def append_rope(self, q, k_new, v_new, rope, positions=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6,
+                    stream=None):
+        """``append_rope`` on this table and pool; returns the rotated q for ``run``."""
+        t = self.t
+        return append_rope(q, k_new, v_new, self.kv_pages, t.qo_indptr, t.page_indices, t.kv_indptr, t.last_page_len,
+                           rope, positions, q_out, q_norm, k_norm, eps, stream)
+
+    def step_rope(self, q, k_new, v_new, rope, positions=None, q_norm=None, k_norm=None, eps=1e-6, out=None, lse=None,
+                  stream=None, tree_mask=None):
+        """append_rope, then run: a step on the projections' rows as they are."""
+        q = self.append_rope(q, k_new, v_new, rope, positions, None, q_norm, k_norm, eps, stream)
+        return self.run(q, out=out, lse=lse, stream=stream, tree_mask=tree_mask)
+
     def step(self, k_new, v_new, q, out=None, lse=None, stream=None):
         """append + run in one call (``append_attention``, or ``append_attention_run``
         on the stored plan)."""
@@ -1179,6 +1212,19 @@ class BatchAttentionQ4:
         kv_append_q4(k_new, v_new, self.kv_pages, t.qo_indptr, t.page_indices, t.kv_indptr,
                      t.last_page_len, kv_exp=self.kv_exp, stream=stream)
 
+    def append_rope(self, q, k_new, v_new, rope, positions=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6,
+                    stream=None):
+        """``append_rope_q4`` on this table and pool; returns the rotated q for ``run``."""
+        t = self.t
+        return append_rope_q4(q, k_new, v_new, self.kv_pages, t.qo_indptr, t.page_indices, t.kv_indptr,
+                              t.last_page_len, rope, positions, self.kv_exp, q_out, q_norm, k_norm, eps, stream)
+
+    def step_rope(self, q, k_new, v_new, rope, positions=None, q_norm=None, k_norm=None, eps=1e-6, out=None, lse=None,
+                  stream=None):
+        """append_rope, then run: a step on the projections' rows as they are."""
+        q = self.append_rope(q, k_new, v_new, rope, positions, None, q_norm, k_norm, eps, stream)
+        return self.run(q, out=out, lse=lse, stream=stream)
+
     def run(self, q, out=None, lse=None, stream=None):
         """Attention of q [nnz_qo, Hq, head_dim]; returns ``out`` and fills ``lse``."""
         d, dev, bf16 = self.dims, self.dev, torch.bfloat16
@@ -1212,6 +1258,195 @@ class BatchAttentionQ4:
         """append, then run."""
         self.append(k_new, v_new, stream)
         return self.run(q, out=out, lse=lse, stream=stream)
+
+
+class Rope:
+    """A rotation of heads by their tokens' positions (``daa_rope``): pair i of the
+    first ``rotary_dim`` dims (all of ``head_dim`` without one; a multiple of 16) turns
+    by position * ``frequencies[i]`` and is multiplied by ``magnitude``.  Pairs are dims
+    (i, i + rotary_dim / 2), or (2i, 2i + 1) when ``interleaved``.  The frequencies are
+    those of ``base`` and ``scaling`` (``rope_frequencies``), or given as
+    ``frequencies`` (radians a token, rotary_dim / 2 of them).  Host data, for every
+    device and layer."""
+
+    def __init__(self, head_dim, base=10000.0, rotary_dim=None, interleaved=False, scaling=None, frequencies=None,
+                 magnitude=None):
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        self.interleaved = bool(interleaved)
+        if frequencies is None:
+            f, m = rope_frequencies(self.rotary_dim, base, scaling)
+        elif scaling is not None:
+            raise ValueError("a scaling changes the base's frequencies: give one of scaling and frequencies")
+        else:
+            f, m = np.array(frequencies, np.float64), 1.0
+        if f.shape != (self.rotary_dim // 2,) or not np.isfinite(f).all():
+            raise ValueError("frequencies must be rotary_dim / 2 finite numbers")
+        self.frequencies = f = np.ascontiguousarray(f)
+        self.magnitude = float(m if magnitude is None else magnitude)
+        self._rope = _Rope()
+        _check(load_library().daa_rope_init(ctypes.byref(self._rope), self.head_dim, self.rotary_dim,
+                                            int(self.interleaved), _ptr(f), self.magnitude), "Rope")
+        self._addr = ctypes.addressof(self._rope)
+
+
+_rope_rows = struct.Struct("@PqqPqqPqqPqqPqqiPPPf0P").pack  # daa_rope_rows
+
+
+def _heads(t, name, dev: int, rows: int, d: int):
+    """(address, row stride, head stride, heads) of bf16 rows [rows, heads, d] on device `dev`, any strides but d's."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a bf16 CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != d:
+        raise ValueError(f"{name} must be [{rows}, heads, {d}]")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}'s head_dim values must be side by side")
+    return t.data_ptr(), s[0], s[1], shape[1]
+
+
+def _norm_addr(w, name, dev, d):
+    if w is None:
+        return 0
+    p = _addr(w, name, torch.bfloat16, dev)
+    if w.shape != (d,):
+        raise ValueError(f"{name} must be [{d}]")
+    return p
+
+
+def _rope_of(rope):
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    return rope.head_dim
+
+
+def _new_rows(x, rows, heads, d, dev, stream):
+    with _use_stream(stream, dev):
+        return torch.empty(rows, heads, d, dtype=torch.bfloat16, device=x.device)
+
+
+_NONE = (0, 0, 0)
+
+
+def apply_rope(q, k, positions, rope, q_out=None, k_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """q [rows, Hq, head_dim] and k [rows, Hkv, head_dim] (or None) rotated by ``positions``
+    (int32 [rows]): (q_out, k_out), new contiguous tensors unless given; q_out=q is in
+    place.  Rows may have any strides of whole 16 bytes (views of a projection's
+    output).  With ``q_norm`` / ``k_norm`` (bf16 [head_dim]) heads are divided by their root
+    mean square (with ``eps``) and multiplied by these first.  No autograd: the
+    gradients of the inputs are this call on those of the outputs at negated
+    positions (without norms)."""
+    d = _rope_of(rope)
+    dev = q.get_device() if isinstance(q, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError("q must be a bf16 CUDA tensor")
+    rows = q.shape[0] if q.dim() == 3 else 0
+    pq = _heads(q, "q", dev, rows, d)
+    p_pos = _addr(positions, "positions", torch.int32, dev)
+    if positions.shape != (rows,):
+        raise ValueError("positions must be [rows]")
+    if q_out is None:
+        q_out = _new_rows(q, rows, pq[3], d, dev, stream)
+    po = _heads(q_out, "q_out", dev, rows, d)
+    if po[3] != pq[3]:
+        raise ValueError("q_out must have the shape of q")
+    pk, pko, hk = _NONE, _NONE, 0
+    if k is not None:
+        *pk, hk = _heads(k, "k", dev, rows, d)
+        if k_out is None:
+            k_out = _new_rows(q, rows, hk, d, dev, stream)
+        *pko, ho = _heads(k_out, "k_out", dev, rows, d)
+        if ho != hk:
+            raise ValueError("k_out must have the shape of k")
+    elif k_out is not None or k_norm is not None:
+        raise ValueError("k_out and k_norm go with k")
+    io = _rope_rows(*pq[:3], *pk, *_NONE, *po[:3], *pko, rows, p_pos, _norm_addr(q_norm, "q_norm", dev, d),
+                    _norm_addr(k_norm, "k_norm", dev, d), eps)
+    _call(load_library().daa_apply_rope, "apply_rope", dev, stream, rope._addr, io, pq[3], hk)
+    return q_out, k_out
+
+
+def _append_rope_args(q, k_new, v_new, dev, dims, table, rope, positions, q_out, q_norm, k_norm, eps, stream):
+    """(q_out, rows record, table addresses, batch) of an append with rotation."""
+    d = _rope_of(rope)
+    if d != dims.head_dim:
+        raise ValueError(f"rope is of head_dim {d}, the pool of {dims.head_dim}")
+    i32 = torch.int32
+    rows = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else 0
+    *pk, hk = _heads(k_new, "k_new", dev, rows, d)
+    *pv, hv = _heads(v_new, "v_new", dev, rows, d)
+    if hk != dims.num_kv_heads or hv != hk:
+        raise ValueError("k_new and v_new must be [nnz_new, Hkv, head_dim]")
+    pq, po = _NONE, _NONE
+    if q is not None:
+        *pq, hq = _heads(q, "q", dev, rows, d)
+        if q_out is None:
+            q_out = _new_rows(q, rows, hq, d, dev, stream)
+        *po, ho = _heads(q_out, "q_out", dev, rows, d)
+        if ho != hq:
+            raise ValueError("q_out must have the shape of q")
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm go with q")
+    p_pos = 0
+    if positions is not None:
+        p_pos = _addr(positions, "positions", i32, dev)
+        if positions.shape != (rows,):
+            raise ValueError("positions must be [nnz_new]")
+    append_indptr, page_indices, kv_indptr, last_page_len = table
+    at = (_addr(append_indptr, "append_indptr", i32, dev), _addr(page_indices, "page_indices", i32, dev),
+          _addr(kv_indptr, "kv_indptr", i32, dev), _addr(last_page_len, "last_page_len", i32, dev))
+    batch = append_indptr.numel() - 1
+    if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
+        raise ValueError("append_indptr and kv_indptr have batch + 1 entries, last_page_len batch")
+    io = _rope_rows(*pq, *pk, *pv, *po, *_NONE, rows, p_pos, _norm_addr(q_norm, "q_norm", dev, d),
+                    _norm_addr(k_norm, "k_norm", dev, d), eps)
+    return q_out, io, at, batch
+
+
+@functools.lru_cache(maxsize=64)
+def _dims_of(shape, num_qo_heads) -> _Dims:
+    if len(shape) != 5 or shape[1] != 2:
+        raise ValueError("kv_pages must be [num_pages, 2, Hkv, page_size, head_dim]")
+    n, _, hkv, p, d = shape
+    return _Dims(hkv if num_qo_heads is None else num_qo_heads, hkv, d, p, n)
+
+
+def append_rope(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len, rope,
+                positions=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """``kv_append`` of rotated keys: k_new [nnz_new, Hkv, head_dim] rotated and written with
+    v_new into their page slots, and q [nnz_new, Hq, head_dim] (or None) rotated into
+    ``q_out`` (a new contiguous tensor without one), which is returned.  A token's
+    position is its place in its request; ``positions`` (int32 [nnz_new]) gives others,
+    as the depths of draft trees.  Rows behind the last request (nnz_new more than
+    append_indptr[batch]) are padding: nothing is written for them.  Strides, norms and
+    in-place as ``apply_rope``."""
+    dev = kv_pages.get_device() if isinstance(kv_pages, torch.Tensor) else -1
+    if dev < 0:
+        raise TypeError("kv_pages must be a contiguous bf16 CUDA tensor")
+    pool = _addr(kv_pages, "kv_pages", torch.bfloat16, dev)
+    dims = _dims_of(kv_pages.shape, q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else None)
+    q_out, io, at, batch = _append_rope_args(q, k_new, v_new, dev, dims,
+                                             (append_indptr, page_indices, kv_indptr, last_page_len), rope, positions,
+                                             q_out, q_norm, k_norm, eps, stream)
+    _call(load_library().daa_append_rope, "append_rope", dev, stream, rope._addr, io, pool, *at, batch, dims)
+    return q_out
+
+
+def append_rope_q4(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len, rope,
+                   positions=None, kv_exp=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
+    """``append_rope`` into a 4-bit pool: the rotated keys (in bf16) and v_new are quantised
+    as ``kv_append_q4`` does."""
+    dev, pool, exp, dims = _q4_pool(kv_pages, kv_exp,
+                                    q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else None)
+    q_out, io, at, batch = _append_rope_args(q, k_new, v_new, dev, dims,
+                                             (append_indptr, page_indices, kv_indptr, last_page_len), rope, positions,
+                                             q_out, q_norm, k_norm, eps, stream)
+    _call(load_library().daa_append_rope_q4, "append_rope_q4", dev, stream, rope._addr, io, pool, exp, *at, batch,
+          dims)
+    return q_out
 
 
 def set_prefill_append_fusion(enable: bool) -> None:

@@ -6,16 +6,8 @@
 //   y = x * 2^-e,  s = e4m3(clamp(max|y| / 6, 2^-9, 448)),  q = e2m1(y / s),
 // both roundings to the nearest value, ties to even.  NaN is stored as zero and
 // an infinity as the block's largest value: the cache holds finite numbers only,
-// so a key that a mask hides can never spoil a sum with 0 * NaN.
-//
-// Rounding a quotient without a division: y has the 8 significant bits of a bf16
-// and every midpoint of two e2m1 values times s has at most 7, so y / s is either
-// exactly a midpoint or at least 2^-9 (relative) away from one.  y * (1 / s), with
-// an approximate reciprocal, is off by less than 2^-21, so rounding it to fp16
-// (11 bits, a half step of 2^-11 at most) lands on the midpoint exactly when y / s
-// does, and the conversion's tie rule then applies to the exact quotient.  max|y| / 6
-// is rounded to e4m3 the same way: 6 times a midpoint of two e4m3 values (5
-// significant bits) has at most 7.
+// so a key that a mask hides can never spoil a sum with 0 * NaN.  quantise_block
+// (q4.cuh) rounds; the append with rotation uses it too.
 //
 // Bound: HBM (2 + 9/16 bytes a value) and the 11 instructions a value (widen, scale,
 // the maximum taken on packed bits, two conversions a pair, addresses): 36,760 tokens
@@ -56,40 +48,6 @@ __device__ __forceinline__ void ld_stream_32(const uint4* p, uint4& a, uint4& b)
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
                : "l"(p));
-}
-
-// The largest |value| of 16 bf16 values as bits, taken two at a time: without a
-// sign bf16 values are ordered as their bits, and NaN is above infinity.
-__device__ __forceinline__ uint32_t max_abs_bits(const uint32_t (&w)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
-  return max(m & 0xFFFFu, m >> 16);
-}
-
-// One block of 16 bf16 values -> 8 code bytes and the scale byte.
-__device__ __forceinline__ uint2 quantise_block(const uint4& a, const uint4& b, float two_to_minus_e,
-                                                uint8_t& scale) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t top = max_abs_bits(w);
-  if (top > 0x7F80u) {  // a NaN: they count as zeros
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((w[i] & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFF0000u;
-      if ((w[i] & 0x7FFF0000u) > 0x7F800000u) w[i] &= 0x0000FFFFu;
-    }
-    top = max_abs_bits(w);
-  }
-  const float amax = __uint_as_float(top << 16);
-  const float s6 = fminf(fmaxf(amax * two_to_minus_e * (1.f / 6.f), 0.001953125f), 448.f);
-  const uint16_t sb = f16x2_to_e4m3x2(f32x2_to_f16x2(s6, 0.f));
-  const float r = rcp_approx(f16x2_to_f32x2(e4m3x2_to_f16x2(sb)).x) * two_to_minus_e;
-  scale = (uint8_t)(sb & 0xFFu);
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = f32x2_to_f16x2(bf16lo_to_f32(w[i]) * r, bf16hi_to_f32(w[i]) * r);
-  const uint32_t lo[4] = {h[0], h[1], h[2], h[3]}, hi[4] = {h[4], h[5], h[6], h[7]};
-  return make_uint2(f16x8_to_e2m1x8(lo), f16x8_to_e2m1x8(hi));
 }
 
 // Flat blocks (row, head, block of 16 dims) of K (blockIdx.y 0) or V (1), cut

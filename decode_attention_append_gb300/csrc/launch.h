@@ -230,6 +230,33 @@ cudaError_t launch_attention_q4(const AttentionQ4Args& a, const int (&n_ranges)[
 // softmax_merge of its n_parts parts (items without a prefix part).
 cudaError_t launch_merge_q4(const MergeArgs& a, int n_parts, bool programmatic, cudaStream_t stream);
 
+// ------------------------------------------------------- rotary positions (rope.cu)
+// Launched programmatically like the kernels above.  Rows of bf16 heads, strides in
+// elements.
+struct RopeRows {
+  uint16_t* p;  // null: there are none
+  int64_t row, head;
+};
+enum RopeTarget { kRopeRows = 0, kRopePages = 1, kRopePagesQ4 = 2 };
+struct RopeArgs {
+  uint64_t turns[64];      // of pair i: turns a token, in 2^-64 of a turn, modulo one
+  RopeRows q, k, v, q_out, k_out;  // v: appends only; k_out: kRopeRows only
+  int n_rows, Hq, Hk;      // Hq 0: no query rows; Hk: kv heads
+  int rotary_dim, interleaved;
+  float magnitude, eps;
+  const uint16_t *q_norm, *k_norm;  // [head_dim] or null
+  const int32_t* positions;         // [n_rows]; null: those of the page table
+  uint8_t* pool;           // bf16 or 4-bit pages
+  const int32_t* kv_exp;   // [2][Hk] or null (4-bit)
+  const int32_t *append_indptr, *page_indices, *kv_indptr, *last_page_len;
+  int batch;
+  int64_t num_pages;
+  int* err;
+  int per_cta, max_rows, step_rows, step_heads;  // set by the launch
+};
+cudaError_t launch_rope(RopeArgs a, int head_dim, RopeTarget target, int sms, bool programmatic,
+                        cudaStream_t stream);
+
 // SMs of the current device, and a launch between the tracer's events (api.cu).
 int device_sms();
 bool tracer_on();

@@ -111,6 +111,9 @@ enum KernelId : int32_t {
   kKernelAppendQ4 = 8,
   kKernelDequantQ4 = 9,
   kKernelAttentionQ4 = 10,
+  kKernelRope = 11,           // rows rotated
+  kKernelAppendRope = 12,     // rotated and appended to bf16 pages
+  kKernelAppendRopeQ4 = 13,   // and to 4-bit pages
 };
 
 }  // namespace daa

@@ -662,6 +662,107 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
                                       void* stream);
 
 /*
+ * Rotary positions ("Chunked prefill", #correctness: a chunk's new k, v vectors
+ * join the cache at their absolute positions).  The other calls of this header
+ * take q and k whose heads are rotated by their tokens' positions already; these
+ * apply the rotation, alone or on the way into the cache.
+ *
+ * Of a head x[0 .. head_dim) of a token at position p, the first rotary_dim dims
+ * form pairs (a, b): (x[i], x[i + rotary_dim / 2]), or (x[2i], x[2i + 1]) when
+ * interleaved.  Pair i becomes
+ *   m * (a cos t - b sin t, b cos t + a sin t),  t = p * radians[i],
+ * and the other dims stay as they are.  With norm weights (q_norm, k_norm: bf16
+ * [head_dim]) a head is first divided by sqrt(mean of its squares + eps) and
+ * multiplied by the weights, all of its dims.  Computed in fp32, rounded once to
+ * bf16; the angle is good to 2^-31 of a turn at every position from -2^31 to
+ * 2^31 - 1.  Dims that are neither normalised nor rotated keep their bits.  (The
+ * squares are summed in fp32: heads of values past about 10^18 have no norm.)
+ * Rotating by negated positions is the transposed rotation: it takes gradients of
+ * the outputs to gradients of the inputs, and for m = 1 outputs back to inputs.
+ *
+ * daa_rope: plain data, filled by daa_rope_init from the radians per token of each
+ * of the rotary_dim / 2 pairs (a host array; whatever scaling a model uses for long
+ * contexts is in them) and the magnitude m.  The calls read it on the host.
+ * Errors: DAA_ERR_UNSUPPORTED for head_dim not 64 or 128, or a rotary_dim that is
+ * not a multiple of 16 from 16 to head_dim; DAA_ERR_INVALID_ARG for NULL arguments,
+ * interleaved not 0 or 1, a magnitude that is not finite and > 0 (as fp32), or
+ * |radians| that is not at most DAA_ROPE_MAX_RADIANS.
+ */
+#define DAA_ROPE_MAX_RADIANS 1048576.0
+
+typedef struct {
+  uint64_t turns[64]; /* of pair i: turns a token, times 2^64, modulo 2^64 */
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float magnitude;
+} daa_rope;
+
+daa_status daa_rope_init(daa_rope* rope, int32_t head_dim, int32_t rotary_dim, int32_t interleaved,
+                         const double* radians, double magnitude);
+
+/* bf16 rows [num_rows][heads][head_dim] on the device: the head_dim values of a head
+ * side by side, strides in elements.  q, k and v may be views of one projection's
+ * output.  Addresses are 16-byte aligned, strides multiples of 8 (of a dimension of
+ * one entry they are not looked at). */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} daa_rows;
+
+typedef struct {
+  daa_rows q, k, v;         /* read */
+  daa_rows q_out, k_out;    /* written */
+  int32_t num_rows;
+  const int32_t* positions; /* device, int32 [num_rows] */
+  const void* q_norm;       /* device, bf16 [head_dim], or NULL: no norm */
+  const void* k_norm;
+  float eps;                /* finite, >= 0; read when there is a norm */
+} daa_rope_rows;
+
+/*
+ * daa_apply_rope: q_out = rotated q, k_out = rotated k, by `positions`.  num_q_heads
+ * >= 1, num_k_heads >= 0 (0: k and k_out are not looked at; v never is).
+ *
+ * daa_append_rope, daa_append_rope_q4: daa_kv_append and daa_kv_append_q4 of the
+ * rotated k and of v, and q_out = rotated q, in one pass over the projections'
+ * rows.  The pages get exactly the bytes of daa_apply_rope followed by those calls.
+ * Rows belong to requests by append_indptr, and a row's position is its place in
+ * its request, kv_len_r - n_r + t, unless `positions` gives others (draft trees:
+ * the depths; the page and slot are by its place always).  q.data NULL: there are
+ * no query rows (q_out.data is NULL then); dims.num_qo_heads must be valid all the
+ * same.  k_out is not looked at.  dims, kv_pages, kv_exp and the table as in the calls named.
+ * num_rows may be more than append_indptr[batch]: rows behind the last request are
+ * padding, and nothing is written for them (a captured step's buffers hold the
+ * most rows that a step may have).
+ *
+ * An output may be its own input (same address and strides: in place).  Otherwise no
+ * output may share an element with another output or an input, or lie in the pool:
+ * what cannot be told apart by ranges, by columns of the same rows or by heads of
+ * the same order is refused.
+ * One kernel launch each, no workspace, nothing kept: all can be captured into a CUDA
+ * graph, and calls on different rows and pages may overlap.
+ * Errors: DAA_ERR_INVALID_ARG for NULL arguments (positions of daa_apply_rope among
+ * them), negative counts or strides, an eps or overlap as above, a rope of another
+ * head_dim than dims; DAA_ERR_UNSUPPORTED for more than 2^31 - 1 heads of all rows,
+ * and shapes as daa_kv_append; DAA_ERR_SHAPE for rows without requests (batch 0);
+ * DAA_ERR_ALIGNMENT; DAA_ERR_CUDA.  Lengths and page ids are checked on the device:
+ * nothing is written for a row of a request with inconsistent lengths (error word 3);
+ * of a row whose page id is outside the pool only q_out is (error word 1).
+ */
+daa_status daa_apply_rope(const daa_rope* rope, const daa_rope_rows* rows, int32_t num_q_heads, int32_t num_k_heads,
+                          void* stream);
+
+daa_status daa_append_rope(const daa_rope* rope, const daa_rope_rows* rows, void* kv_pages,
+                           const int32_t* append_indptr, const int32_t* page_indices, const int32_t* kv_indptr,
+                           const int32_t* last_page_len, int32_t batch, daa_dims dims, void* stream);
+
+daa_status daa_append_rope_q4(const daa_rope* rope, const daa_rope_rows* rows, void* kv_pages, const int32_t* kv_exp,
+                              const int32_t* append_indptr, const int32_t* page_indices, const int32_t* kv_indptr,
+                              const int32_t* last_page_len, int32_t batch, daa_dims dims, void* stream);
+
+/*
  * Reads the device error word of the current device into *code (0 = none, 1 =
  * page id out of range, 2 = a bounded wait timed out, 3 = inconsistent request
  * lengths, 4 = a step table that needs more pages than are free) and clears it
@@ -695,7 +796,8 @@ daa_status daa_selftest_bounded_wait(int32_t* gave_up);
  * 4 tensor-core prefill, 5 tensor-core decode split-KV (decode and verify
  * items), 6 tensor-core short multi-token items (head_dim 128: requests whose
  * rows fit two 128-row Q tiles), 7 step tables and released pages, 8 4-bit
- * append, 9 4-bit pages to bf16, 10 attention over 4-bit pages.
+ * append, 9 4-bit pages to bf16, 10 attention over 4-bit pages, 11 rotated rows,
+ * 12 and 13 the append with rotation into bf16 and 4-bit pages.
  */
 daa_status daa_trace_enable(int32_t capacity);
 daa_status daa_trace_disable(void);

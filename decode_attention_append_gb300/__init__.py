@@ -97,7 +97,7 @@ class PlanInfo(ctypes.Structure):
 class _Rope(ctypes.Structure):
     """daa_rope: the frequencies of a rotation."""
     _fields_ = [("turns", ctypes.c_uint64 * 64), ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
-                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float)]
+                ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_double)]
 
 
 def library_path() -> str:

@@ -37,7 +37,8 @@ daa_status check_rope(const daa_rope* r) {
   if (!r) return DAA_ERR_INVALID_ARG;
   if (!head_dim_ok(r->head_dim) || r->rotary_dim < 16 || r->rotary_dim > r->head_dim || r->rotary_dim % 16 != 0)
     return DAA_ERR_UNSUPPORTED;
-  if ((r->interleaved != 0 && r->interleaved != 1) || !std::isfinite(r->magnitude) || !(r->magnitude > 0.f))
+  if ((r->interleaved != 0 && r->interleaved != 1) || !(r->magnitude >= DAA_ROPE_MIN_MAGNITUDE) ||
+      !(r->magnitude <= DAA_ROPE_MAX_MAGNITUDE))
     return DAA_ERR_INVALID_ARG;
   return DAA_OK;
 }
@@ -143,7 +144,8 @@ daa_status common_args(const daa_rope* rope, const daa_rope_rows* io, int64_t q_
   std::memcpy(a.turns, rope->turns, sizeof(a.turns));
   a.rotary_dim = rope->rotary_dim;
   a.interleaved = rope->interleaved;
-  a.magnitude = rope->magnitude;
+  a.magnitude = (float)rope->magnitude;
+  a.magnitude_low = (float)(rope->magnitude - a.magnitude);
   a.n_rows = io->num_rows;
   a.Hq = (int)q_heads;
   a.Hk = (int)k_heads;
@@ -222,7 +224,7 @@ daa_status daa_rope_init(daa_rope* rope, int32_t head_dim, int32_t rotary_dim, i
   r.head_dim = head_dim;
   r.rotary_dim = rotary_dim;
   r.interleaved = interleaved;
-  r.magnitude = (float)magnitude;
+  r.magnitude = magnitude;
   const daa_status st = check_rope(&r);
   if (st != DAA_OK) return st;
   for (int i = 0; i < rotary_dim / 2; ++i) {

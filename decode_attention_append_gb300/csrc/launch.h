@@ -243,7 +243,7 @@ struct RopeArgs {
   RopeRows q, k, v, q_out, k_out;  // v: appends only; k_out: kRopeRows only
   int n_rows, Hq, Hk;      // Hq 0: no query rows; Hk: kv heads
   int rotary_dim, interleaved;
-  float magnitude, eps;
+  float magnitude, magnitude_low, eps;  // the magnitude in two parts
   const uint16_t *q_norm, *k_norm;  // [head_dim] or null
   const int32_t* positions;         // [n_rows]; null: those of the page table
   uint8_t* pool;           // bf16 or 4-bit pages
@@ -252,9 +252,9 @@ struct RopeArgs {
   int batch;
   int64_t num_pages;
   int* err;
-  int per_cta, max_rows, step_rows, step_heads;  // set by the launch
+  int parts, part_heads;   // of a row, one a warp; set by the launch
 };
-cudaError_t launch_rope(RopeArgs a, int head_dim, RopeTarget target, int sms, bool programmatic,
+cudaError_t launch_rope(const RopeArgs& a, int head_dim, RopeTarget target, int sms, bool programmatic,
                         cudaStream_t stream);
 
 // SMs of the current device, and a launch between the tracer's events (api.cu).

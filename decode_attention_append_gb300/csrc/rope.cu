@@ -8,20 +8,22 @@
 // after an optional division of the head by its root mean square over the head_dim
 // dims and a product with weights.  Everything is fp32 from the loaded bf16 values
 // to one rounding at the end.  (Between the norm and the rotation nothing is
-// rounded; a model that keeps bf16 there differs by that rounding, 2^-9.)
+// rounded; a model that keeps bf16 there differs by that rounding, 2^-8.)
 //
 // Angles.  p f_i grows to 10^5 and more, where fp32 has no digits of the angle left.
 // A pair's turns a token are held as a 64-bit fraction of a turn: p times it, modulo
-// 2^64, is the angle modulo one turn, exact but for p 2^-65 turns; its upper 32 bits
-// (2^-32 turns, 1.5e-9 rad) go through sincospif.  No table of positions is needed,
-// nothing is read for it, and no position is too far or negative.
+// 2^64, is the angle modulo one turn, exact but for p 2^-65 turns.  Its upper 8 bits,
+// rounded, name a table entry (sine and cosine of n / 256 turns); the rest, at most
+// 2^-9 turns, goes through short series and the addition theorems (cos_sin).  No table
+// of positions is needed, and no position is too far or negative.
 //
-// Layout.  A head is D / 16 threads of two 16-byte chunks each: chunks j and
-// j + rotary_dim / 16 for the half layout, so that a thread holds whole pairs, and a
-// warp's loads and stores are 64 to 128 contiguous bytes a head.  CTAs take equal
-// ranges of the flat (row, head) space, q then k then v heads of a row; each range's
-// sines (one pair of values a thread and row) are computed once into shared memory
-// and read by all heads of the row.
+// Layout.  A warp takes a row, or a part of its heads where rows are few.  It finds
+// the row's request and place, works out the row's sines once (one pair a lane, by way
+// of shared memory), and then streams heads: a head is D / 16 lanes of two 16-byte
+// chunks each, chunks j and j + rotary_dim / 16 for the half layout, so that a lane
+// holds whole pairs and keeps its eight sines and cosines in registers.  Loads run
+// kAhead heads ahead of their use, the first ones ahead of the search.  Warps share
+// nothing but constants: no barrier behind the first.
 #include <algorithm>
 
 #include "launch.h"
@@ -31,15 +33,133 @@
 namespace daa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kP = 16;
-constexpr int kMaxBatch = 1023;            // requests whose lengths a CTA holds
-constexpr int kMaxAngleBytes = 24 * 1024;  // sines and cosines of a CTA's rows
-constexpr int kSmallU = 1, kLargeU = 4;    // heads of a thread in flight
+constexpr int kAhead = 4;  // heads of a lane in flight
 
 // Where a row's k and v go: page * 16 + slot, or:
 constexpr int64_t kNoPage = -1;  // a bad page id: its q is rotated all the same
 constexpr int64_t kNoRow = -2;   // a row of no request: nothing of it is written
+
+// ------------------------------------------------------------------- angles
+// Sine and cosine of n / 256 turns, each as the sum of two fp32 numbers.
+constexpr int kSteps = 256;
+constexpr double kTwoPi = 6.283185307179586;
+
+struct SineTable {
+  float v[kSteps][4];  // cosine: upper, lower; sine: upper, lower
+};
+
+constexpr double series(double x, int first) {  // Taylor's, of sine (1) or cosine (0), |x| <= pi / 4
+  double term = first ? x : 1.0, sum = term;
+  for (int n = first + 1; n < 24; n += 2) {
+    term *= -x * x / (n * (n + 1.0));
+    sum += term;
+  }
+  return sum;
+}
+
+constexpr SineTable make_table() {
+  SineTable t{};
+  for (int n = 0; n < kSteps; ++n) {
+    const int quarter = n / 64, r = n % 64;
+    const double a = (r <= 32 ? r : 64 - r) * (kTwoPi / kSteps);
+    const double x = series(a, r <= 32 ? 0 : 1), y = series(a, r <= 32 ? 1 : 0);  // cosine, sine within the quarter
+    const double c = quarter == 0 ? x : quarter == 1 ? -y : quarter == 2 ? -x : y;
+    const double s = quarter == 0 ? y : quarter == 1 ? x : quarter == 2 ? -y : -x;
+    t.v[n][0] = (float)c;
+    t.v[n][1] = (float)(c - t.v[n][0]);
+    t.v[n][2] = (float)s;
+    t.v[n][3] = (float)(s - t.v[n][2]);
+  }
+  return t;
+}
+
+__device__ constexpr SineTable g_sines = make_table();
+
+// a + b = s + e exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float t = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+}
+// a b = p + e exactly.
+__device__ __forceinline__ void two_prod(float a, float b, float& p, float& e) {
+  p = __fmul_rn(a, b);
+  e = __fmaf_rn(a, b, -p);
+}
+
+// m cos and m sin of phase * 2^-64 turns, each the sum of two fp32 numbers, good to 2^-35 of m.
+struct CosSin {
+  float ch, cl, sh, sl;
+};
+__device__ __forceinline__ CosSin cos_sin(uint64_t phase, const float4* table, float mh, float ml) {
+  const uint32_t n = (uint32_t)((phase + (1ull << 55)) >> 56);
+  const int64_t rest = (int64_t)(phase - ((uint64_t)n << 56));  // -2^55 .. 2^55 - 1
+  const float4 t = table[n];
+  // d = vh + vl radians, |d| <= pi / 256: from 2^-40 turns in two parts
+  constexpr double unit = kTwoPi / 1099511627776.0;
+  constexpr float kh = (float)unit, kl = (float)(unit - kh);
+  const int32_t r = (int32_t)(rest >> 24);
+  const float dh = (float)r, dl = (float)(r - (int32_t)dh);
+  float vh, vl;
+  two_prod(dh, kh, vh, vl);
+  vl = __fadd_rn(vl, __fmaf_rn(dh, kl, __fmul_rn(dl, kh)));
+  // cos d - 1 = u + ul, sin d = vh + sl:  d^2 / 2 <= 2^-13.7, d^3 / 6 <= 2^-21.6
+  float z, zl;
+  two_prod(vh, vh, z, zl);
+  const float u = -0.5f * z;
+  const float ul = __fmaf_rn(z * z, 1.f / 24, __fmaf_rn(-vh, vl, -0.5f * zl));
+  const float sl = __fmaf_rn(vh * z, __fmaf_rn(z, 1.f / 120, -1.f / 6), vl);
+  // cos (t + d) = C + C u - S v,  sin (t + d) = S + S u + C v
+  CosSin o;
+  float a, ae, b, be, d, de, h, he;
+  two_prod(t.x, u, a, ae);
+  two_prod(t.z, vh, b, be);
+  two_sum(a, -b, d, de);
+  two_sum(t.x, d, h, he);
+  float low = __fadd_rn(__fadd_rn(he, de), __fsub_rn(ae, be));
+  low = __fadd_rn(low, __fmaf_rn(t.x, ul, __fmaf_rn(-t.z, sl, __fmaf_rn(-t.w, vh, __fmaf_rn(t.y, u, t.y)))));
+  const float c = __fadd_rn(h, low), cl = __fsub_rn(low, __fsub_rn(c, h));
+  two_prod(t.z, u, a, ae);
+  two_prod(t.x, vh, b, be);
+  two_sum(a, b, d, de);
+  two_sum(t.z, d, h, he);
+  low = __fadd_rn(__fadd_rn(he, de), __fadd_rn(ae, be));
+  low = __fadd_rn(low, __fmaf_rn(t.z, ul, __fmaf_rn(t.x, sl, __fmaf_rn(t.y, vh, __fmaf_rn(t.w, u, t.w)))));
+  const float s = __fadd_rn(h, low), s_l = __fsub_rn(low, __fsub_rn(s, h));
+  two_prod(c, mh, a, ae);
+  ae = __fadd_rn(ae, __fmaf_rn(c, ml, __fmul_rn(cl, mh)));
+  o.ch = __fadd_rn(a, ae);
+  o.cl = __fsub_rn(ae, __fsub_rn(o.ch, a));
+  two_prod(s, mh, a, ae);
+  ae = __fadd_rn(ae, __fmaf_rn(s, ml, __fmul_rn(s_l, mh)));
+  o.sh = __fadd_rn(a, ae);
+  o.sl = __fsub_rn(ae, __fsub_rn(o.sh, a));
+  return o;
+}
+
+// ----------------------------------------------------------------- rotations
+// (a, b) -> (a c - b s, b c + a s), each a product and a fused product.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = __fmaf_rn(a, c, -__fmul_rn(b, s));
+  b = __fmaf_rn(b, c, __fmul_rn(a, s));
+  a = x;
+}
+
+// a c + b s to fp32's nearest, all four in two parts (errors are 2^-46 of |a c| + |b s|).
+__device__ __forceinline__ float sum_of_products(float ah, float al, float ch, float cl, float bh, float bl, float sh,
+                                                 float sl) {
+  float p, pe, q, qe, d, de;
+  two_prod(ah, ch, p, pe);
+  two_prod(bh, sh, q, qe);
+  two_sum(p, q, d, de);
+  pe = __fadd_rn(pe, __fmaf_rn(ah, cl, __fmul_rn(al, ch)));
+  qe = __fadd_rn(qe, __fmaf_rn(bh, sl, __fmul_rn(bl, sh)));
+  const float y = __fadd_rn(d, __fadd_rn(de, __fadd_rn(pe, qe)));
+  // past fp32's range the small parts are no numbers: the plain form is what is meant
+  return fabsf(y) <= 3.4028234e38f ? y : __fmaf_rn(ah, ch, __fmul_rn(bh, sh));
+}
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   uint4 v;
@@ -61,26 +181,42 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
   f[3] = v.w;
 }
 
-// (a, b) -> (a c - b s, b c + a s), each a product and a fused product.
-__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
-  const float x = __fmaf_rn(a, c, -__fmul_rn(b, s));
-  b = __fmaf_rn(b, c, __fmul_rn(a, s));
-  a = x;
-}
-
-// The page, slot and position of new row `row`.
-__device__ __forceinline__ int64_t find_place(const RopeArgs& a, const int32_t* indptr, const int32_t* kv_begin,
-                                              const int32_t* last_lens, int row, int& pos) {
+// ------------------------------------------------------------- a row's place
+// The page and slot of new row `row`, and its position; a warp's lanes together.
+__device__ __forceinline__ int64_t find_place(const RopeArgs& a, int row, int lane, int& pos) {
   pos = 0;
-  if (row >= indptr[a.batch]) return kNoRow;  // padding behind the last request
-  int lo = 0, hi = a.batch - 1;  // largest r with indptr[r] <= row
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (indptr[mid] <= row) lo = mid; else hi = mid - 1;
+  // the last request r with append_indptr[r] <= row: narrowed to 256 by probes, then counted
+  int lo = 0, n = a.batch;
+  while (n > 256) {
+    const int step = (n + 31) / 32;
+    const bool below = lane * step < n && ld_word(a.append_indptr + lo + lane * step) <= row;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  const int a0 = indptr[lo], a1 = indptr[lo + 1];
-  const int p0 = kv_begin[lo], np = kv_begin[lo + 1] - p0;
-  const int last_len = np > 0 ? last_lens[lo] : 0;
+  int r = lo - 1;
+  {
+    int v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = INT32_MAX;
+      if (32 * i < n && 32 * i + lane < n) v[i] = ld_word(a.append_indptr + lo + 32 * i + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r += __popc(__ballot_sync(0xffffffffu, v[i] <= row));
+  }
+  r = max(r, 0);
+  const int32_t* p = lane == 0   ? a.append_indptr + r
+                     : lane == 1 ? a.append_indptr + r + 1
+                     : lane == 2 ? a.kv_indptr + r
+                     : lane == 3 ? a.kv_indptr + r + 1
+                     : lane == 4 ? a.last_page_len + r
+                                 : a.append_indptr + a.batch;
+  const int word = lane < 6 ? ld_word(p) : 0;
+  const int a0 = __shfl_sync(0xffffffffu, word, 0), a1 = __shfl_sync(0xffffffffu, word, 1);
+  const int p0 = __shfl_sync(0xffffffffu, word, 2), np = __shfl_sync(0xffffffffu, word, 3) - p0;
+  const int last_len = __shfl_sync(0xffffffffu, word, 4);
+  if (row >= __shfl_sync(0xffffffffu, word, 5)) return kNoRow;  // padding behind the last request
   const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * kP + last_len : 0;
   if (row < a0 || row >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || p0 < 0 || last_len < 1 || last_len > kP) {
     set_device_error(a.err, kDevErrShape);
@@ -95,199 +231,238 @@ __device__ __forceinline__ int64_t find_place(const RopeArgs& a, const int32_t* 
   return page * kP + pos % kP;
 }
 
-template <int D, int TARGET, bool NORM, int U>
+template <int D, int TARGET, bool NORM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int L = D / 16, G = kThreads / L;  // threads of a head, heads of a CTA at a time
+  constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
-  extern __shared__ __align__(16) uint8_t smem[];
-  const int hp = a.rotary_dim / 2;
-  float* s_cos = reinterpret_cast<float*>(smem);
-  float* s_sin = s_cos + a.max_rows * hp;
-  float* s_w = s_sin + a.max_rows * hp;  // weights of q, of k
-  int64_t* s_at = reinterpret_cast<int64_t*>(s_w + (NORM ? 2 * D : 0));
-  int* s_pos = reinterpret_cast<int*>(s_at + a.max_rows);
-  int* s_table = s_pos + a.max_rows;
+  __shared__ float4 s_table[kSteps];
+  __shared__ uint64_t s_turns[64];
+  __shared__ __align__(16) float s_angle[kWarps][Q4 ? 4 : 2][64];  // cosines, sines, and their lower parts
+  __shared__ __align__(16) float s_w[NORM ? 2 : 1][D];
 
-  const int tid = threadIdx.x, group = tid / L, j = tid % L;
-  const uint32_t mask = ((L == 8 ? 0xFFu : 0xFu)) << (tid & 31 & ~(L - 1));  // the head's lanes
-  const int H = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-  const int first = blockIdx.x * a.per_cta;
-  const int count = min(a.per_cta, a.n_rows * H - first);
-  const int row0 = first / H, in0 = first - row0 * H;
-  const int nrows = (in0 + count - 1) / H + 1;
-  // chunks of 8 dims of this thread; in a 4-bit cache's rows two side by side, a block
-  const int nrot = a.rotary_dim / 16;
-  const bool pairs = a.interleaved != 0;
-  const int c0 = pairs ? j : j < nrot ? j : 2 * j;
-  const int c1 = pairs ? j + L : j < nrot ? j + nrot : 2 * j + 1;
-  const int pair = tid % hp, angle_rows = kThreads / hp;  // this thread's share of the sines
-  const uint64_t turns = a.turns[pair];
-  const int row_a = (in0 + group) / H, head_a = in0 + group - row_a * H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, group = lane / L, j = lane % L;
+  const uint32_t mask = (L == 8 ? 0xFFu : 0xFu) << (lane & ~(L - 1));  // the head's lanes
   grid_dep_launch();
+  for (int t = tid; t < kSteps; t += kThreads) s_table[t] = *reinterpret_cast<const float4*>(g_sines.v[t]);
+  if (tid < 64) s_turns[tid] = a.turns[tid];
+  __syncthreads();
   grid_dep_wait();
-
-  // the values depend on nothing else: load them first
-  uint32_t w[U][8];
-  {
-    int row = row_a, head = head_a;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u * G + group < count) {
-        const bool is_q = head < a.Hq, is_k = !is_q && head < a.Hq + a.Hk;
-        const RopeRows& x = is_q ? a.q : !APPEND || is_k ? a.k : a.v;
-        const int h = is_q ? head : head - a.Hq - (!APPEND || is_k ? 0 : a.Hk);
-        const bool side = Q4 && !is_q && (pairs || !is_k);
-        const uint16_t* p = x.p + (row0 + row) * x.row + h * x.head;
-        const uint4 lo = ld_stream(p + 8 * (side ? 2 * j : c0)), hi = ld_stream(p + 8 * (side ? 2 * j + 1 : c1));
-        w[u][0] = lo.x, w[u][1] = lo.y, w[u][2] = lo.z, w[u][3] = lo.w;
-        w[u][4] = hi.x, w[u][5] = hi.y, w[u][6] = hi.z, w[u][7] = hi.w;
-      }
-      row += a.step_rows;
-      head += a.step_heads;
-      if (head >= H) {
-        head -= H;
-        ++row;
-      }
-    }
-  }
   if (NORM) {
     for (int t = tid; t < 2 * D; t += kThreads) {
       const uint16_t* n = t < D ? a.q_norm : a.k_norm;
       uint16_t b = 0;
       if (n) asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(n + t % D));
-      s_w[t] = __uint_as_float((uint32_t)b << 16);
+      s_w[t / D][t % D] = __uint_as_float((uint32_t)b << 16);
     }
+    __syncthreads();
   }
-  if (APPEND) {
-    const int32_t *indptr = a.append_indptr, *kv_begin = a.kv_indptr, *last_lens = a.last_page_len;
-    if (a.batch <= kMaxBatch) {
-      int* s_kv = s_table + a.batch + 1;
-      int* s_last = s_kv + a.batch + 1;
-      for (int t = tid; t <= a.batch; t += kThreads) {
-        s_table[t] = ld_word(indptr + t);
-        s_kv[t] = ld_word(kv_begin + t);
-        if (t < a.batch) s_last[t] = ld_word(last_lens + t);
-      }
-      __syncthreads();
-      indptr = s_table;
-      kv_begin = s_kv;
-      last_lens = s_last;
-    }
-    for (int t = tid; t < nrows; t += kThreads) {
-      int pos;
-      s_at[t] = find_place(a, indptr, kv_begin, last_lens, row0 + t, pos);
-      s_pos[t] = a.positions ? ld_word(a.positions + row0 + t) : pos;
-    }
-  } else {
-    for (int t = tid; t < nrows; t += kThreads) s_pos[t] = ld_word(a.positions + row0 + t);
-  }
-  __syncthreads();
-  if (tid < angle_rows * hp) {
-    for (int r = tid / hp; r < nrows; r += angle_rows) {
-      const uint64_t phase = turns * (uint64_t)(int64_t)s_pos[r];
-      float s, c;
-      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-      s_cos[r * hp + pair] = c * a.magnitude;
-      s_sin[r * hp + pair] = s * a.magnitude;
-    }
-  }
-  __syncthreads();
 
-  int row = row_a, head = head_a;
+  const int task = blockIdx.x * kWarps + warp;
+  const int row = task / a.parts, first = (task - row * a.parts) * a.part_heads;
+  if (row >= a.n_rows) return;
+  const int H = a.Hq + (APPEND ? 2 : 1) * a.Hk;
+  const int end = min(first + a.part_heads, H);
+  // chunks of 8 dims of this lane; in a 4-bit cache's rows two side by side, a block
+  const int nrot = a.rotary_dim / 16;
+  const bool pairs = a.interleaved != 0;
+  const int c0 = pairs ? j : j < nrot ? j : 2 * j;
+  const int c1 = pairs ? j + L : j < nrot ? j + nrot : 2 * j + 1;
+  const uint16_t* q_row = a.q.p + row * a.q.row;
+  const uint16_t* k_row = a.k.p + row * a.k.row;
+  const uint16_t* v_row = a.v.p + row * a.v.row;
+  auto side_by_side = [&](int head) { return Q4 && head >= a.Hq && (pairs || head >= a.Hq + a.Hk); };
+  auto load = [&](int head, uint32_t (&w)[8]) {
+    const int h = head - a.Hq;
+    const uint16_t* p = h < 0 ? q_row + head * a.q.head : !APPEND || h < a.Hk ? k_row + h * a.k.head : v_row + (h - a.Hk) * a.v.head;
+    const bool side = side_by_side(head);
+    const uint4 lo = ld_stream(p + 8 * (side ? 2 * j : c0)), hi = ld_stream(p + 8 * (side ? 2 * j + 1 : c1));
+    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+    w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+  };
+  uint32_t w[kAhead][8];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int r = row, hd = head;
-    row += a.step_rows;
-    head += a.step_heads;
-    if (head >= H) {
-      head -= H;
-      ++row;
+  for (int u = 0; u < kAhead; ++u)
+    if (first + u * G + group < end) load(first + u * G + group, w[u]);
+
+  int pos = 0;
+  int64_t at = 0;
+  if (APPEND) {
+    at = find_place(a, row, lane, pos);
+    if (at == kNoRow) return;
+  }
+  if (a.positions) pos = ld_word(a.positions + row);
+  float(&angle)[Q4 ? 4 : 2][64] = s_angle[warp];
+  for (int p = lane; p < a.rotary_dim / 2; p += 32) {
+    const CosSin x = cos_sin(s_turns[p] * (uint64_t)(int64_t)pos, s_table, a.magnitude, a.magnitude_low);
+    angle[0][p] = x.ch;
+    angle[1][p] = x.sh;
+    if (Q4) {
+      angle[2][p] = x.cl;
+      angle[3][p] = x.sl;
     }
-    if (u * G + group >= count) continue;
-    const int64_t at = APPEND ? s_at[r] : 0;
-    if (at == kNoRow) continue;
-    const bool is_q = hd < a.Hq, is_k = !is_q && (!APPEND || hd < a.Hq + a.Hk);
-    const int h = is_q ? hd : hd - a.Hq - (is_k ? 0 : a.Hk);
-    const bool side = Q4 && !is_q && (pairs || !is_k);
-    const int d0 = side ? 2 * j : c0, d1 = side ? 2 * j + 1 : c1;
-    uint32_t(&v)[8] = w[u];
-    if (is_q || is_k) {
-      float x[16];
+  }
+  __syncwarp();
+  // this lane's pairs: whether its two chunks turn, and by what
+  const bool t0 = pairs ? c0 < 2 * nrot : j < nrot, t1 = pairs ? c1 < 2 * nrot : j < nrot;
+  const int i0 = pairs ? 4 * c0 : 8 * j, i1 = pairs ? 4 * c1 : 8 * j + 4;
+  float c[8], s[8];
+  if (t0) {
+    load4(angle[0] + i0, c);
+    load4(angle[1] + i0, s);
+  }
+  if (t1) {
+    load4(angle[0] + i1, c + 4);
+    load4(angle[1] + i1, s + 4);
+  }
+
+  // q, and k that is not quantised: normalised, turned, rounded
+  auto rotate = [&](uint32_t (&v)[8], bool is_q) {
+    float x[16];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[2 * i] = bf16lo_to_f32(v[i]);
-        x[2 * i + 1] = bf16hi_to_f32(v[i]);
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = bf16lo_to_f32(v[i]);
+      x[2 * i + 1] = bf16hi_to_f32(v[i]);
+    }
+    const bool norm = NORM && (is_q ? a.q_norm : a.k_norm) != nullptr;
+    if (norm) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) ss = __fmaf_rn(x[i], x[i], ss);
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
+      const float k = rsqrtf(ss * (1.f / D) + a.eps);
+      const float* wt = s_w[is_q ? 0 : NORM];
+      float g[16];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        load4(wt + 8 * c0 + i, g + i);
+        load4(wt + 8 * c1 + i, g + 8 + i);
       }
-      bool t0 = pairs ? d0 < 2 * nrot : j < nrot, t1 = pairs ? d1 < 2 * nrot : j < nrot;
-      float c[8], s[8];
-      const float *cr = s_cos + r * hp, *sr = s_sin + r * hp;
-      const int i0 = pairs ? 4 * d0 : 8 * j, i1 = pairs ? 4 * d1 : 8 * j + 4;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * k * g[i];
+    }
+    if (!pairs) {
       if (t0) {
-        load4(cr + i0, c);
-        load4(sr + i0, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
+      }
+    } else {
+      if (t0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
       }
       if (t1) {
-        load4(cr + i1, c + 4);
-        load4(sr + i1, s + 4);
-      }
-      const bool norm = NORM && (is_q ? a.q_norm : a.k_norm) != nullptr;
-      if (norm) {
-        float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int m = L / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(mask, ss, m);
-        const float k = rsqrtf(ss * (1.f / D) + a.eps);
-        const float* wt = s_w + (is_q ? 0 : D);
-        float g[16];
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          load4(wt + 8 * d0 + i, g + i);
-          load4(wt + 8 * d1 + i, g + 8 + i);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * k * g[i];
-      }
-      if (!pairs) {
-        if (t0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
-        }
-      } else {
-        if (t0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
-        }
-        if (t1) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) turn(x[8 + 2 * i], x[9 + 2 * i], c[4 + i], s[4 + i]);
-        }
-      }
-      // dims that are neither normalised nor rotated keep their bits
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (norm || t0) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-        if (norm || t1) v[4 + i] = pack_bf16x2(x[8 + 2 * i], x[9 + 2 * i]);
+        for (int i = 0; i < 4; ++i) turn(x[8 + 2 * i], x[9 + 2 * i], c[4 + i], s[4 + i]);
       }
     }
+    // dims that are neither normalised nor rotated keep their bits
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (norm || t0) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      if (norm || t1) v[4 + i] = pack_bf16x2(x[8 + 2 * i], x[9 + 2 * i]);
+    }
+  };
+
+  // k that is quantised, in two parts: a code changes by up to a third where a key
+  // falls on the other side of a border, so it is the definition that decides and not
+  // the order of fp32 operations.  As above, to the nearest fp32 and then to bf16.
+  auto rotate_exactly = [&](uint32_t (&v)[8], int d0, int d1) {
+    float x[16], xl[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = bf16lo_to_f32(v[i]);
+      x[2 * i + 1] = bf16hi_to_f32(v[i]);
+      xl[2 * i] = xl[2 * i + 1] = 0.f;
+    }
+    const bool norm = NORM && a.k_norm != nullptr;
+    if (norm) {
+      float ss = 0.f, sl = 0.f, e;  // the squares are exact
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        two_sum(ss, __fmul_rn(x[i], x[i]), ss, e);
+        sl = __fadd_rn(sl, e);
+      }
+#pragma unroll
+      for (int m = L / 2; m > 0; m >>= 1) {
+        two_sum(ss, __shfl_xor_sync(mask, ss, m), ss, e);
+        sl = __fadd_rn(__fadd_rn(sl, __shfl_xor_sync(mask, sl, m)), e);
+      }
+      two_sum(ss * (1.f / D), a.eps, ss, e);
+      sl = __fmaf_rn(sl, 1.f / D, e);
+      // one step of Newton's from r: 1 / sqrt(ss + sl) = r (1 + t / 2), t = 1 - (ss + sl) r^2
+      const float r = rsqrtf(ss);
+      float rr, re;
+      two_prod(r, r, rr, re);
+      const float t = __fsub_rn(__fmaf_rn(-ss, rr, 1.f), __fmaf_rn(ss, re, __fmul_rn(sl, rr)));
+      const float rl = isfinite(t) ? 0.5f * r * t : 0.f;
+      const float* wt = s_w[NORM];
+      float g[16];
+#pragma unroll
+      for (int i = 0; i < 8; i += 4) {
+        load4(wt + 8 * d0 + i, g + i);
+        load4(wt + 8 * d1 + i, g + 8 + i);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float y = __fmul_rn(x[i], g[i]);  // 16 bits: exact
+        two_prod(y, r, x[i], xl[i]);
+        xl[i] = __fmaf_rn(y, rl, xl[i]);
+      }
+    }
+    const bool z0 = pairs ? d0 < 2 * nrot : j < nrot, z1 = pairs ? d1 < 2 * nrot : j < nrot;
+    const int e0 = pairs ? 4 * d0 : 8 * j, e1 = pairs ? 4 * d1 : 8 * j + 4;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (half ? z1 : z0) {
+        float ch[4], sh[4], cl[4], sl[4];
+        const int at_pair = half ? e1 : e0;
+        load4(angle[0] + at_pair, ch);
+        load4(angle[1] + at_pair, sh);
+        load4(angle[Q4 ? 2 : 0] + at_pair, cl);
+        load4(angle[Q4 ? 3 : 0] + at_pair, sl);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // half layout: pairs 4 half + i of the two chunks; else of this half's chunk
+          const int m = pairs ? 8 * half + 2 * i : 4 * half + i, n = pairs ? m + 1 : m + 8;
+          const float y = sum_of_products(x[m], xl[m], ch[i], cl[i], -x[n], -xl[n], sh[i], sl[i]);
+          x[n] = sum_of_products(x[n], xl[n], ch[i], cl[i], x[m], xl[m], sh[i], sl[i]);
+          x[m] = y;
+          xl[m] = xl[n] = 0.f;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (norm || z0) v[i] = pack_bf16x2(__fadd_rn(x[2 * i], xl[2 * i]), __fadd_rn(x[2 * i + 1], xl[2 * i + 1]));
+      if (norm || z1) v[4 + i] = pack_bf16x2(__fadd_rn(x[8 + 2 * i], xl[8 + 2 * i]), __fadd_rn(x[9 + 2 * i], xl[9 + 2 * i]));
+    }
+  };
+
+  uint16_t* q_out = a.q_out.p + row * a.q_out.row;
+  const int64_t page = at / kP;
+  const int slot = (int)(at % kP);
+  auto finish = [&](int head, uint32_t (&v)[8]) {
+    const int h = head - a.Hq;  // of k, then of v
+    const bool is_q = h < 0, is_k = !is_q && (!APPEND || h < a.Hk);
+    const bool side = side_by_side(head);
+    const int d0 = side ? 2 * j : c0, d1 = side ? 2 * j + 1 : c1;
+    if (Q4 && is_k) rotate_exactly(v, d0, d1);
+    else if (is_q || is_k) rotate(v, is_q);
     if (is_q || !APPEND) {
-      const RopeRows& y = is_q ? a.q_out : a.k_out;
-      uint16_t* p = y.p + (row0 + r) * y.row + h * y.head;
-      st_16(p + 8 * d0, v);
-      st_16(p + 8 * d1, v + 4);
-      continue;
-    }
-    if (at == kNoPage) continue;
-    const int64_t page = at / kP;
-    const int slot = (int)(at % kP), kv = is_k ? 0 : 1;
-    if (!Q4) {
-      uint16_t* p = reinterpret_cast<uint16_t*>(a.pool) + (((page * 2 + kv) * a.Hk + h) * kP + slot) * D;
-      st_16(p + 8 * d0, v);
-      st_16(p + 8 * d1, v + 4);
+      uint16_t* p = is_q ? q_out + head * a.q_out.head : a.k_out.p + row * a.k_out.row + h * a.k_out.head;
+      st_16(p + 8 * c0, v);
+      st_16(p + 8 * c1, v + 4);
+    } else if (at == kNoPage) {
+    } else if (!Q4) {
+      // a page is [2][Hk][16][D]: v's heads follow k's
+      uint16_t* p = reinterpret_cast<uint16_t*>(a.pool) + ((page * 2 * a.Hk + h) * kP + slot) * D;
+      st_16(p + 8 * c0, v);
+      st_16(p + 8 * c1, v + 4);
     } else {
       uint4 b[2] = {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7])};
       if (!side) {
-        // chunks 2j and 2j + 1 of the head, from the threads that have them
+        // chunks 2j and 2j + 1 of the head, from the lanes that have them
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * j + i;
@@ -302,37 +477,41 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
           b[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      const float me = a.kv_exp ? q4_pow2(-ld_word(a.kv_exp + kv * a.Hk + h)) : 1.f;
+      const int kv = is_k ? 0 : 1, hk = h - kv * a.Hk;
+      const float me = a.kv_exp ? q4_pow2(-ld_word(a.kv_exp + h)) : 1.f;
       uint8_t scale;
       const uint2 codes = quantise_block(b[0], b[1], me, scale);
-      uint8_t* slice = a.pool + ((page * a.Hk + h) * 2 + kv) * (int64_t)q4_slice_bytes(D);
+      uint8_t* slice = a.pool + ((page * a.Hk + hk) * 2 + kv) * (int64_t)q4_slice_bytes(D);
       *reinterpret_cast<uint2*>(slice + slot * (D / 2) + j * 8) = codes;
       slice[kP * (D / 2) + (kv == 0 ? slot * L + j : j * kP + slot)] = scale;
+    }
+  };
+
+  for (int base = first + group; base < end; base += kAhead * G) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int head = base + u * G;
+      if (head < end) {
+        finish(head, w[u]);
+        if (head + kAhead * G < end) load(head + kAhead * G, w[u]);
+      }
     }
   }
 }
 
 template <int D, int TARGET>
 cudaError_t launch(RopeArgs a, int sms, bool programmatic, cudaStream_t stream) {
-  constexpr int G = kThreads / (D / 16);
+  constexpr int G = 32 / (D / 16);
   const int H = a.Hq + (TARGET != kRopeRows ? 2 : 1) * a.Hk;
-  const int64_t total = (int64_t)a.n_rows * H;
-  const bool large = total >= (int64_t)sms * 16 * G;
-  const int hp = a.rotary_dim / 2;
-  auto rows_of = [&](int items) { return (items + H - 2) / H + 1; };
-  a.per_cta = G * (large ? kLargeU : kSmallU);
-  const int most = kMaxAngleBytes / (8 * hp);
-  if (rows_of(a.per_cta) > most) a.per_cta = (most - 1) * H;
-  a.max_rows = rows_of(a.per_cta);
-  a.step_rows = G / H;
-  a.step_heads = G % H;
-  const bool norm = a.q_norm || a.k_norm;
-  const size_t smem = (size_t)a.max_rows * (hp * 8 + 12) + (norm ? 2 * D * 4 : 0) +
-                      (TARGET != kRopeRows && a.batch <= kMaxBatch ? 12 * ((size_t)a.batch + 1) : 0);
-  const int64_t grid = (total + a.per_cta - 1) / a.per_cta;
-  auto kern = norm ? (large ? rope_kernel<D, TARGET, true, kLargeU> : rope_kernel<D, TARGET, true, kSmallU>)
-                   : (large ? rope_kernel<D, TARGET, false, kLargeU> : rope_kernel<D, TARGET, false, kSmallU>);
-  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), smem, stream, programmatic, a);
+  const int rounds = (H + G - 1) / G;
+  // few rows: their heads over more warps, as many as the GPU starts at once
+  const int64_t want = (int64_t)sms * 16;
+  int parts = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, want / a.n_rows));
+  a.part_heads = (rounds + parts - 1) / parts * G;
+  a.parts = (H + a.part_heads - 1) / a.part_heads;
+  const int64_t tasks = (int64_t)a.n_rows * a.parts, grid = (tasks + kWarps - 1) / kWarps;
+  auto kern = a.q_norm || a.k_norm ? rope_kernel<D, TARGET, true> : rope_kernel<D, TARGET, false>;
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, programmatic, a);
 }
 
 template <int TARGET>
@@ -342,7 +521,8 @@ cudaError_t launch_d(const RopeArgs& a, int head_dim, int sms, bool programmatic
 
 }  // namespace
 
-cudaError_t launch_rope(RopeArgs a, int head_dim, RopeTarget target, int sms, bool programmatic, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeArgs& a, int head_dim, RopeTarget target, int sms, bool programmatic,
+                        cudaStream_t stream) {
   return target == kRopeRows    ? launch_d<kRopeRows>(a, head_dim, sms, programmatic, stream)
          : target == kRopePages ? launch_d<kRopePages>(a, head_dim, sms, programmatic, stream)
                                 : launch_d<kRopePagesQ4>(a, head_dim, sms, programmatic, stream);

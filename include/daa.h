@@ -685,17 +685,19 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
  * contexts is in them) and the magnitude m.  The calls read it on the host.
  * Errors: DAA_ERR_UNSUPPORTED for head_dim not 64 or 128, or a rotary_dim that is
  * not a multiple of 16 from 16 to head_dim; DAA_ERR_INVALID_ARG for NULL arguments,
- * interleaved not 0 or 1, a magnitude that is not finite and > 0 (as fp32), or
- * |radians| that is not at most DAA_ROPE_MAX_RADIANS.
+ * interleaved not 0 or 1, a magnitude outside DAA_ROPE_MIN_MAGNITUDE ..
+ * DAA_ROPE_MAX_MAGNITUDE, or |radians| that is not at most DAA_ROPE_MAX_RADIANS.
  */
 #define DAA_ROPE_MAX_RADIANS 1048576.0
+#define DAA_ROPE_MIN_MAGNITUDE 0.0009765625
+#define DAA_ROPE_MAX_MAGNITUDE 1024.0
 
 typedef struct {
   uint64_t turns[64]; /* of pair i: turns a token, times 2^64, modulo 2^64 */
   int32_t head_dim;
   int32_t rotary_dim;
   int32_t interleaved;
-  float magnitude;
+  double magnitude;
 } daa_rope;
 
 daa_status daa_rope_init(daa_rope* rope, int32_t head_dim, int32_t rotary_dim, int32_t interleaved,

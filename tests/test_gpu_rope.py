@@ -298,15 +298,26 @@ def test_append(daa, case):
     assert torch.equal(pool.view(torch.int16), wb)
 
 
+def _exact_keys(k, pos, rope, weight, eps=float(np.float32(1e-6))):
+    y, _ = ref.rotate(_np(k), pos, rope.frequencies, rope.rotary_dim, rope.interleaved, rope.magnitude, None if weight is None else _np(weight), eps)
+    y = torch.from_numpy(y).float().bfloat16().to(DEV)
+    if weight is None:
+        y[..., rope.rotary_dim:] = k[..., rope.rotary_dim:]
+    return y
+
+
 @pytest.mark.parametrize("exps", [False, True])
 @pytest.mark.parametrize("case", APPENDS, ids=lambda c: f"{c[0]}x{c[1]}x{c[2]}r{c[3]}")
 def test_append_q4(daa, case, exps):
     hq, hk, d, rot, inter, norm, how, cached, new = case
     t, n, q, k, v, wq, wk, rope, rng = _case(daa, *case)
-    pos = _dev(ref.places(t)[:, 3].astype(np.int32))
+    at = ref.places(t)[:, 3]
+    pos = _dev(at.astype(np.int32))
     e = rng.integers(-3, 4, (2, hk)).astype(np.int32)
     e_dev = _dev(e) if exps else None
-    q_want, k_want = daa.apply_rope(q, k, pos, rope, q_norm=wq, k_norm=wk)
+    q_want, _ = daa.apply_rope(q, None, pos, rope, q_norm=wq)
+    # keys by the definition alone, to fp32's nearest and then to bf16: bytes, not bounds
+    k_want = _exact_keys(k, at, rope, wk)
     want = torch.full((n, hk, 2, 9 * d), 0xAB, dtype=torch.uint8, device=DEV)
     pool = want.clone()
     daa.kv_append_q4(k_want, v.contiguous(), want, *_dev_table(t), kv_exp=e_dev)
@@ -331,6 +342,7 @@ def test_given_positions_turn_but_do_not_place(daa, q4):
     pos = np.concatenate([30 + depth, 7 + depth[:6]]).astype(np.int32)
     q_want, k_want = daa.apply_rope(q, k, _dev(pos), rope)
     if q4:
+        k_want = _exact_keys(k, pos, rope, None)
         pool, want = daa.new_q4_pool(n, 2, 128), daa.new_q4_pool(n, 2, 128)
         got = daa.append_rope_q4(q, k, v, pool, *_dev_table(t), rope, positions=_dev(pos))
         daa.kv_append_q4(k_want, v.contiguous(), want, *_dev_table(t))

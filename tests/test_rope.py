@@ -39,7 +39,7 @@ def test_frequencies(daa, scaling, n, base):
     assert np.allclose(f, want, rtol=1e-13, atol=0)
     assert m == (pytest.approx(0.1 * math.log(o["factor"]) + 1, rel=1e-15) if kind == "yarn" else 1.0)
     r = daa.Rope(128 if n > 64 else 64, base, n, scaling=scaling)
-    assert np.array_equal(r.frequencies, f) and r.magnitude == m and r._rope.magnitude == np.float32(m)
+    assert np.array_equal(r.frequencies, f) and r.magnitude == m and r._rope.magnitude == m
 
 
 @pytest.mark.parametrize("bad", [

@@ -34,8 +34,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import importlib.util
 import os
-import struct
 import threading
 import weakref
 from dataclasses import dataclass
@@ -1290,45 +1290,41 @@ class Rope:
         self._addr = ctypes.addressof(self._rope)
 
 
-_rope_rows = struct.Struct("@PqqPqqPqqPqqPqqiPPPf0P").pack  # daa_rope_rows
+_native = None
 
 
-def _heads(t, name, dev: int, rows: int, d: int):
-    """(address, row stride, head stride, heads) of bf16 rows [rows, heads, d] on device `dev`, any strides but d's."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or not t.is_cuda:
+def _load_native():
+    """The module that hands tensors to the calls with rotation (built by ``build.build()``)."""
+    global _native
+    load_library()
+    with _lock:
+        if _native is None:
+            path = os.path.join(_HERE, "_build", "_binding.so")
+            if not os.path.exists(path):
+                raise ImportError(f"_binding.so not built at {path}; run decode_attention_append_gb300.build.build()")
+            spec = importlib.util.spec_from_file_location("_binding", path)
+            mod = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(mod)
+            _native = mod
+    return _native
+
+
+def _rows_like(x, name, stream):
+    """New contiguous rows of the shape of x, for the call's stream."""
+    if not (isinstance(x, torch.Tensor) and x.is_cuda):
         raise TypeError(f"{name} must be a bf16 CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    shape = t.shape
-    if len(shape) != 3 or shape[0] != rows or shape[2] != d:
-        raise ValueError(f"{name} must be [{rows}, heads, {d}]")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}'s head_dim values must be side by side")
-    return t.data_ptr(), s[0], s[1], shape[1]
+    with _use_stream(stream, x.get_device()):
+        return torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
 
 
-def _norm_addr(w, name, dev, d):
-    if w is None:
-        return 0
-    p = _addr(w, name, torch.bfloat16, dev)
-    if w.shape != (d,):
-        raise ValueError(f"{name} must be [{d}]")
-    return p
+def _handle(stream):
+    return stream if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _rope_of(rope):
+def _rope_addr(rope):
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    return rope.head_dim
-
-
-def _new_rows(x, rows, heads, d, dev, stream):
-    with _use_stream(stream, dev):
-        return torch.empty(rows, heads, d, dtype=torch.bfloat16, device=x.device)
-
-
-_NONE = (0, 0, 0)
+    return rope._addr
 
 
 def apply_rope(q, k, positions, rope, q_out=None, k_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
@@ -1339,79 +1335,15 @@ def apply_rope(q, k, positions, rope, q_out=None, k_out=None, q_norm=None, k_nor
     mean square (with ``eps``) and multiplied by these first.  No autograd: the
     gradients of the inputs are this call on those of the outputs at negated
     positions (without norms)."""
-    d = _rope_of(rope)
-    dev = q.get_device() if isinstance(q, torch.Tensor) else -1
-    if dev < 0:
-        raise TypeError("q must be a bf16 CUDA tensor")
-    rows = q.shape[0] if q.dim() == 3 else 0
-    pq = _heads(q, "q", dev, rows, d)
-    p_pos = _addr(positions, "positions", torch.int32, dev)
-    if positions.shape != (rows,):
-        raise ValueError("positions must be [rows]")
     if q_out is None:
-        q_out = _new_rows(q, rows, pq[3], d, dev, stream)
-    po = _heads(q_out, "q_out", dev, rows, d)
-    if po[3] != pq[3]:
-        raise ValueError("q_out must have the shape of q")
-    pk, pko, hk = _NONE, _NONE, 0
-    if k is not None:
-        *pk, hk = _heads(k, "k", dev, rows, d)
-        if k_out is None:
-            k_out = _new_rows(q, rows, hk, d, dev, stream)
-        *pko, ho = _heads(k_out, "k_out", dev, rows, d)
-        if ho != hk:
-            raise ValueError("k_out must have the shape of k")
-    elif k_out is not None or k_norm is not None:
-        raise ValueError("k_out and k_norm go with k")
-    io = _rope_rows(*pq[:3], *pk, *_NONE, *po[:3], *pko, rows, p_pos, _norm_addr(q_norm, "q_norm", dev, d),
-                    _norm_addr(k_norm, "k_norm", dev, d), eps)
-    _call(load_library().daa_apply_rope, "apply_rope", dev, stream, rope._addr, io, pq[3], hk)
+        q_out = _rows_like(q, "q", stream)
+    if k_out is None and k is not None:
+        k_out = _rows_like(k, "k", stream)
+    st = (_native or _load_native()).apply_rope(q, k, positions, _rope_addr(rope), q_out, k_out, q_norm, k_norm, eps,
+                                                _handle(stream))
+    if st != DAA_OK:
+        raise DaaError(st, "apply_rope")
     return q_out, k_out
-
-
-def _append_rope_args(q, k_new, v_new, dev, dims, table, rope, positions, q_out, q_norm, k_norm, eps, stream):
-    """(q_out, rows record, table addresses, batch) of an append with rotation."""
-    d = _rope_of(rope)
-    if d != dims.head_dim:
-        raise ValueError(f"rope is of head_dim {d}, the pool of {dims.head_dim}")
-    i32 = torch.int32
-    rows = k_new.shape[0] if isinstance(k_new, torch.Tensor) and k_new.dim() == 3 else 0
-    *pk, hk = _heads(k_new, "k_new", dev, rows, d)
-    *pv, hv = _heads(v_new, "v_new", dev, rows, d)
-    if hk != dims.num_kv_heads or hv != hk:
-        raise ValueError("k_new and v_new must be [nnz_new, Hkv, head_dim]")
-    pq, po = _NONE, _NONE
-    if q is not None:
-        *pq, hq = _heads(q, "q", dev, rows, d)
-        if q_out is None:
-            q_out = _new_rows(q, rows, hq, d, dev, stream)
-        *po, ho = _heads(q_out, "q_out", dev, rows, d)
-        if ho != hq:
-            raise ValueError("q_out must have the shape of q")
-    elif q_out is not None or q_norm is not None:
-        raise ValueError("q_out and q_norm go with q")
-    p_pos = 0
-    if positions is not None:
-        p_pos = _addr(positions, "positions", i32, dev)
-        if positions.shape != (rows,):
-            raise ValueError("positions must be [nnz_new]")
-    append_indptr, page_indices, kv_indptr, last_page_len = table
-    at = (_addr(append_indptr, "append_indptr", i32, dev), _addr(page_indices, "page_indices", i32, dev),
-          _addr(kv_indptr, "kv_indptr", i32, dev), _addr(last_page_len, "last_page_len", i32, dev))
-    batch = append_indptr.numel() - 1
-    if kv_indptr.numel() != batch + 1 or last_page_len.numel() != batch:
-        raise ValueError("append_indptr and kv_indptr have batch + 1 entries, last_page_len batch")
-    io = _rope_rows(*pq, *pk, *pv, *po, *_NONE, rows, p_pos, _norm_addr(q_norm, "q_norm", dev, d),
-                    _norm_addr(k_norm, "k_norm", dev, d), eps)
-    return q_out, io, at, batch
-
-
-@functools.lru_cache(maxsize=64)
-def _dims_of(shape, num_qo_heads) -> _Dims:
-    if len(shape) != 5 or shape[1] != 2:
-        raise ValueError("kv_pages must be [num_pages, 2, Hkv, page_size, head_dim]")
-    n, _, hkv, p, d = shape
-    return _Dims(hkv if num_qo_heads is None else num_qo_heads, hkv, d, p, n)
 
 
 def append_rope(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len, rope,
@@ -1423,15 +1355,13 @@ def append_rope(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indpt
     as the depths of draft trees.  Rows behind the last request (nnz_new more than
     append_indptr[batch]) are padding: nothing is written for them.  Strides, norms and
     in-place as ``apply_rope``."""
-    dev = kv_pages.get_device() if isinstance(kv_pages, torch.Tensor) else -1
-    if dev < 0:
-        raise TypeError("kv_pages must be a contiguous bf16 CUDA tensor")
-    pool = _addr(kv_pages, "kv_pages", torch.bfloat16, dev)
-    dims = _dims_of(kv_pages.shape, q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else None)
-    q_out, io, at, batch = _append_rope_args(q, k_new, v_new, dev, dims,
-                                             (append_indptr, page_indices, kv_indptr, last_page_len), rope, positions,
-                                             q_out, q_norm, k_norm, eps, stream)
-    _call(load_library().daa_append_rope, "append_rope", dev, stream, rope._addr, io, pool, *at, batch, dims)
+    if q_out is None and q is not None:
+        q_out = _rows_like(q, "q", stream)
+    st = (_native or _load_native()).append_rope(q, k_new, v_new, kv_pages, None, append_indptr, page_indices,
+                                                 kv_indptr, last_page_len, _rope_addr(rope), positions, q_out, q_norm,
+                                                 k_norm, eps, _handle(stream))
+    if st != DAA_OK:
+        raise DaaError(st, "append_rope")
     return q_out
 
 
@@ -1439,13 +1369,13 @@ def append_rope_q4(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_in
                    positions=None, kv_exp=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
     """``append_rope`` into a 4-bit pool: the rotated keys (in bf16) and v_new are quantised
     as ``kv_append_q4`` does."""
-    dev, pool, exp, dims = _q4_pool(kv_pages, kv_exp,
-                                    q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else None)
-    q_out, io, at, batch = _append_rope_args(q, k_new, v_new, dev, dims,
-                                             (append_indptr, page_indices, kv_indptr, last_page_len), rope, positions,
-                                             q_out, q_norm, k_norm, eps, stream)
-    _call(load_library().daa_append_rope_q4, "append_rope_q4", dev, stream, rope._addr, io, pool, exp, *at, batch,
-          dims)
+    if q_out is None and q is not None:
+        q_out = _rows_like(q, "q", stream)
+    st = (_native or _load_native()).append_rope_q4(q, k_new, v_new, kv_pages, kv_exp, append_indptr, page_indices,
+                                                    kv_indptr, last_page_len, _rope_addr(rope), positions, q_out,
+                                                    q_norm, k_norm, eps, _handle(stream))
+    if st != DAA_OK:
+        raise DaaError(st, "append_rope_q4")
     return q_out
 
 

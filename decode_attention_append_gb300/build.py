@@ -1,8 +1,10 @@
-"""Build libdaa.so in-tree with nvcc for sm_103a (no cmake, no torch extension).
+"""Build libdaa.so in-tree with nvcc for sm_103a (no cmake), and the module that
+hands torch tensors to some of its calls (``csrc/binding.cpp``, with g++).
 
 Each CUDA translation unit compiles in parallel to an object file under
 ``_build/``; they link into one shared library with the CUDA runtime linked
-statically.  Rebuilds only what changed.
+statically.  The module links against it and against the torch that is installed,
+and is built again for another one.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -10,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdaa.so")
+BINDING = os.path.join(BUILD, "_binding.so")
 SOURCES = ["api.cu", "append.cu", "decode.cu", "merge.cu", "prefill.cu", "prefill_pair.cu", "noalloc.cu",
            "api_q4.cu", "append_q4.cu", "decode_q4.cu", "step_table.cu",
            "api_rope.cu", "rope.cu"]
@@ -56,6 +60,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
 
+    # the module's object file goes by the torch and Python that it is for
+    import torch
+    tag = f"{torch.__version__}-{sys.version_info[0]}.{sys.version_info[1]}".replace("/", "_")
+    src, binding = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-{tag}.o")
+    if force or _stale(binding, [src, os.path.join(ROOT, "include", "daa.h")]):
+        jobs.insert(0, [shutil.which("g++") or "g++", *_torch_flags(torch), "-c", src, "-o", binding])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:
@@ -70,7 +81,26 @@ def build(verbose: bool = False, force: bool = False) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    stamp = os.path.join(BUILD, f"binding-{tag}.linked.o")  # empty: which torch the module is linked for
+    if force or _stale(BINDING, [binding, LIB]) or not os.path.exists(stamp):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+        run(["g++", "-shared", "-o", tmp, binding, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+             f"-L{BUILD}", "-l:libdaa.so", "-Wl,-rpath,$ORIGIN"])
+        for f in os.listdir(BUILD):
+            if f.endswith(".linked.o"):
+                os.remove(os.path.join(BUILD, f))
+        os.replace(tmp, BINDING)
+        open(stamp, "w").close()
     return LIB
+
+
+def _torch_flags(torch):
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    return ["-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{d}" for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"),
+                                 sysconfig.get_path("include"), os.path.join(cuda, "include")))]
 
 
 if __name__ == "__main__":

@@ -35,7 +35,10 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kP = 16;
-constexpr int kAhead = 4;  // heads of a lane in flight
+// heads of a lane in flight
+template <int TARGET> constexpr int kAheadOf = 4;
+template <> constexpr int kAheadOf<kRopePagesQ4> = 3;
+template <> constexpr int kAheadOf<kRopeRows> = 2;
 
 // Where a row's k and v go: page * 16 + slot, or:
 constexpr int64_t kNoPage = -1;  // a bad page id: its q is rotated all the same
@@ -46,7 +49,7 @@ constexpr int64_t kNoRow = -2;   // a row of no request: nothing of it is writte
 constexpr int kSteps = 256;
 constexpr double kTwoPi = 6.283185307179586;
 
-struct SineTable {
+struct __align__(16) SineTable {
   float v[kSteps][4];  // cosine: upper, lower; sine: upper, lower
 };
 
@@ -147,18 +150,23 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = x;
 }
 
-// a c + b s to fp32's nearest, all four in two parts (errors are 2^-46 of |a c| + |b s|).
-__device__ __forceinline__ float sum_of_products(float ah, float al, float ch, float cl, float bh, float bl, float sh,
-                                                 float sl) {
-  float p, pe, q, qe, d, de;
-  two_prod(ah, ch, p, pe);
-  two_prod(bh, sh, q, qe);
-  two_sum(p, q, d, de);
-  pe = __fadd_rn(pe, __fmaf_rn(ah, cl, __fmul_rn(al, ch)));
-  qe = __fadd_rn(qe, __fmaf_rn(bh, sl, __fmul_rn(bl, sh)));
-  const float y = __fadd_rn(d, __fadd_rn(de, __fadd_rn(pe, qe)));
-  // past fp32's range the small parts are no numbers: the plain form is what is meant
-  return fabsf(y) <= 3.4028234e38f ? y : __fmaf_rn(ah, ch, __fmul_rn(bh, sh));
+// a c + b s = d + e, to 2^-40 of |a| + |b|, with c and s in 16 bits and the rest.
+// Of a and b of 8 bits the upper products are exact; of 16 bits (LONG) they are not.
+template <bool LONG>
+__device__ __forceinline__ void sum_of_products(float a, float c, float cl, float b, float s, float sl, float& d,
+                                                float& e) {
+  float low;
+  if (LONG) {
+    float p, pe, q, qe;
+    two_prod(a, c, p, pe);
+    two_prod(b, s, q, qe);
+    two_sum(p, q, d, e);
+    low = __fmaf_rn(a, cl, __fmaf_rn(b, sl, __fadd_rn(pe, qe)));
+  } else {
+    two_sum(__fmul_rn(a, c), __fmul_rn(b, s), d, e);
+    low = __fmaf_rn(a, cl, __fmul_rn(b, sl));
+  }
+  e = __fadd_rn(e, low);
 }
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -235,9 +243,11 @@ template <int D, int TARGET, bool NORM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
+  constexpr int kAhead = kAheadOf<TARGET>;
   __shared__ float4 s_table[kSteps];
   __shared__ uint64_t s_turns[64];
-  __shared__ __align__(16) float s_angle[kWarps][Q4 ? 4 : 2][64];  // cosines, sines, and their lower parts
+  // a row's cosines and sines; of both, 16 bits and what these leave
+  __shared__ __align__(16) float s_angle[kWarps][Q4 ? 6 : 2][64];
   __shared__ __align__(16) float s_w[NORM ? 2 : 1][D];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, group = lane / L, j = lane % L;
@@ -291,14 +301,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (at == kNoRow) return;
   }
   if (a.positions) pos = ld_word(a.positions + row);
-  float(&angle)[Q4 ? 4 : 2][64] = s_angle[warp];
-  for (int p = lane; p < a.rotary_dim / 2; p += 32) {
-    const CosSin x = cos_sin(s_turns[p] * (uint64_t)(int64_t)pos, s_table, a.magnitude, a.magnitude_low);
-    angle[0][p] = x.ch;
-    angle[1][p] = x.sh;
-    if (Q4) {
-      angle[2][p] = x.cl;
-      angle[3][p] = x.sl;
+  float(&angle)[Q4 ? 6 : 2][64] = s_angle[warp];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int p = 32 * i + lane;
+    if (p < a.rotary_dim / 2) {
+      const CosSin x = cos_sin(s_turns[p] * (uint64_t)(int64_t)pos, s_table, a.magnitude, a.magnitude_low);
+      angle[0][p] = x.ch;
+      angle[1][p] = x.sh;
+      if (Q4) {
+        const float ch = __uint_as_float(__float_as_uint(x.ch) & 0xFFFFFF00u);
+        const float sh = __uint_as_float(__float_as_uint(x.sh) & 0xFFFFFF00u);
+        angle[Q4 ? 2 : 0][p] = ch;
+        angle[Q4 ? 3 : 0][p] = __fadd_rn(__fsub_rn(x.ch, ch), x.cl);
+        angle[Q4 ? 4 : 0][p] = sh;
+        angle[Q4 ? 5 : 0][p] = __fadd_rn(__fsub_rn(x.sh, sh), x.sl);
+      }
     }
   }
   __syncwarp();
@@ -368,14 +386,14 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   // falls on the other side of a border, so it is the definition that decides and not
   // the order of fp32 operations.  As above, to the nearest fp32 and then to bf16.
   auto rotate_exactly = [&](uint32_t (&v)[8], int d0, int d1) {
-    float x[16], xl[16];
+    float x[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[2 * i] = bf16lo_to_f32(v[i]);
       x[2 * i + 1] = bf16hi_to_f32(v[i]);
-      xl[2 * i] = xl[2 * i + 1] = 0.f;
     }
     const bool norm = NORM && a.k_norm != nullptr;
+    float r = 1.f, rl = 0.f;
     if (norm) {
       float ss = 0.f, sl = 0.f, e;  // the squares are exact
 #pragma unroll
@@ -391,11 +409,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       two_sum(ss * (1.f / D), a.eps, ss, e);
       sl = __fmaf_rn(sl, 1.f / D, e);
       // one step of Newton's from r: 1 / sqrt(ss + sl) = r (1 + t / 2), t = 1 - (ss + sl) r^2
-      const float r = rsqrtf(ss);
+      r = rsqrtf(ss);
       float rr, re;
       two_prod(r, r, rr, re);
       const float t = __fsub_rn(__fmaf_rn(-ss, rr, 1.f), __fmaf_rn(ss, re, __fmul_rn(sl, rr)));
-      const float rl = isfinite(t) ? 0.5f * r * t : 0.f;
+      rl = isfinite(t) ? 0.5f * r * t : 0.f;
       const float* wt = s_w[NORM];
       float g[16];
 #pragma unroll
@@ -404,38 +422,60 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         load4(wt + 8 * d1 + i, g + 8 + i);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y = __fmul_rn(x[i], g[i]);  // 16 bits: exact
-        two_prod(y, r, x[i], xl[i]);
-        xl[i] = __fmaf_rn(y, rl, xl[i]);
-      }
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], g[i]);  // 16 bits: exact
     }
+    auto scaled = [&](float d, float e) {  // (d + e) (r + rl)
+      if (!NORM || !norm) return __fadd_rn(d, e);
+      float h, he;
+      two_prod(d, r, h, he);
+      return __fadd_rn(h, __fadd_rn(he, __fmaf_rn(d, rl, __fmul_rn(e, r))));
+    };
     const bool z0 = pairs ? d0 < 2 * nrot : j < nrot, z1 = pairs ? d1 < 2 * nrot : j < nrot;
     const int e0 = pairs ? 4 * d0 : 8 * j, e1 = pairs ? 4 * d1 : 8 * j + 4;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      // half layout: pairs 4 half + i of the two chunks; else those of this half's chunk
       if (half ? z1 : z0) {
-        float ch[4], sh[4], cl[4], sl[4];
         const int at_pair = half ? e1 : e0;
-        load4(angle[0] + at_pair, ch);
-        load4(angle[1] + at_pair, sh);
-        load4(angle[Q4 ? 2 : 0] + at_pair, cl);
-        load4(angle[Q4 ? 3 : 0] + at_pair, sl);
+        float ch[4], cl[4], sh[4], sl[4];
+        load4(angle[Q4 ? 2 : 0] + at_pair, ch);
+        load4(angle[Q4 ? 3 : 0] + at_pair, cl);
+        load4(angle[Q4 ? 4 : 0] + at_pair, sh);
+        load4(angle[Q4 ? 5 : 0] + at_pair, sl);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // half layout: pairs 4 half + i of the two chunks; else of this half's chunk
-          const int m = pairs ? 8 * half + 2 * i : 4 * half + i, n = pairs ? m + 1 : m + 8;
-          const float y = sum_of_products(x[m], xl[m], ch[i], cl[i], -x[n], -xl[n], sh[i], sl[i]);
-          x[n] = sum_of_products(x[n], xl[n], ch[i], cl[i], x[m], xl[m], sh[i], sl[i]);
-          x[m] = y;
-          xl[m] = xl[n] = 0.f;
+          float p, pe, q, qe;
+          if (pairs) {
+            float &u = x[8 * half + 2 * i], &w = x[8 * half + 2 * i + 1];
+            sum_of_products<NORM>(u, ch[i], cl[i], -w, sh[i], sl[i], p, pe);
+            sum_of_products<NORM>(w, ch[i], cl[i], u, sh[i], sl[i], q, qe);
+            u = scaled(p, pe);
+            w = scaled(q, qe);
+          } else {
+            float &u = x[4 * half + i], &w = x[4 * half + i + 8];
+            sum_of_products<NORM>(u, ch[i], cl[i], -w, sh[i], sl[i], p, pe);
+            sum_of_products<NORM>(w, ch[i], cl[i], u, sh[i], sl[i], q, qe);
+            u = scaled(p, pe);
+            w = scaled(q, qe);
+          }
+        }
+      } else if (norm) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (pairs) {
+            x[8 * half + 2 * i] = scaled(x[8 * half + 2 * i], 0.f);
+            x[8 * half + 2 * i + 1] = scaled(x[8 * half + 2 * i + 1], 0.f);
+          } else {
+            x[4 * half + i] = scaled(x[4 * half + i], 0.f);
+            x[4 * half + i + 8] = scaled(x[4 * half + i + 8], 0.f);
+          }
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (norm || z0) v[i] = pack_bf16x2(__fadd_rn(x[2 * i], xl[2 * i]), __fadd_rn(x[2 * i + 1], xl[2 * i + 1]));
-      if (norm || z1) v[4 + i] = pack_bf16x2(__fadd_rn(x[8 + 2 * i], xl[8 + 2 * i]), __fadd_rn(x[9 + 2 * i], xl[9 + 2 * i]));
+      if (norm || z0) v[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      if (norm || z1) v[4 + i] = pack_bf16x2(x[8 + 2 * i], x[9 + 2 * i]);
     }
   };
 
@@ -447,7 +487,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const bool is_q = h < 0, is_k = !is_q && (!APPEND || h < a.Hk);
     const bool side = side_by_side(head);
     const int d0 = side ? 2 * j : c0, d1 = side ? 2 * j + 1 : c1;
-    if (Q4 && is_k) rotate_exactly(v, d0, d1);
+    // past 2^100 products leave fp32's range, and their small parts are no numbers
+    if (Q4 && is_k && (NORM || max_abs_bits(v) < 0x7180u)) rotate_exactly(v, d0, d1);
     else if (is_q || is_k) rotate(v, is_q);
     if (is_q || !APPEND) {
       uint16_t* p = is_q ? q_out + head * a.q_out.head : a.k_out.p + row * a.k_out.row + h * a.k_out.head;

@@ -2,6 +2,7 @@
 (found before anything is enqueued).  No GPU."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -11,6 +12,9 @@ import rope_support as ref
 
 OK, INVALID, SHAPE, UNSUPPORTED, ALIGNMENT = 0, -1, -2, -4, -7
 A = 0x100000  # an address that passes a null and alignment check and is never read
+
+
+_rec = struct.Struct("@PqqPqqPqqPqqPqqiPPPf0P").pack  # daa_rope_rows
 
 
 @pytest.fixture(scope="module")
@@ -105,7 +109,7 @@ def _append(daa, q4=False, batch=0, rope=None, pool=0x70000000, table=A, dims=(4
     T = 512  # elements of a projection's row: q, k, v
     io = dict(q=(A, T, 64), k=(A + 512, T, 64), v=(A + 768, T, 64), q_out=(0x900000, 256, 64), k_out=(0, 0, 0), pos=0, qn=0, kn=0, eps=1e-6)
     io.update(change)
-    rec = daa._rope_rows(*io["q"], *io["k"], *io["v"], *io["q_out"], *io["k_out"], rows, io["pos"], io["qn"], io["kn"], io["eps"])
+    rec = _rec(*io["q"], *io["k"], *io["v"], *io["q_out"], *io["k_out"], rows, io["pos"], io["qn"], io["kn"], io["eps"])
     rope = daa.Rope(64) if rope is None else rope
     lib = daa.load_library()
     tab = [table, A, A, A]
@@ -154,15 +158,15 @@ def test_rows_within_the_pool_are_refused(daa, name):
 def test_bad_records_are_refused(daa):
     lib = daa.load_library()
     rope = daa.Rope(64)
-    rec = daa._rope_rows(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, A, 0, 0, 0.0)
+    rec = _rec(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, A, 0, 0, 0.0)
     assert lib.daa_apply_rope(None, rec, 1, 0, None) == INVALID
     assert lib.daa_apply_rope(rope._addr, None, 1, 0, None) == INVALID
     assert lib.daa_apply_rope(rope._addr, rec, 0, 1, None) == INVALID
     assert lib.daa_apply_rope(rope._addr, rec, 1, -1, None) == INVALID
     assert lib.daa_apply_rope(rope._addr, rec, 1, 1, None) == INVALID  # no k
-    none = daa._rope_rows(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, 0, 0, 0, 0.0)
+    none = _rec(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, 0, 0, 0, 0.0)
     assert lib.daa_apply_rope(rope._addr, none, 1, 0, None) == INVALID  # no positions
-    empty = daa._rope_rows(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
+    empty = _rec(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
     assert lib.daa_apply_rope(rope._addr, empty, 1, 1, None) == OK
     other = daa._Rope.from_buffer_copy(bytes(rope._rope))
     for field, value, expect in (("rotary_dim", 72, UNSUPPORTED), ("head_dim", 32, UNSUPPORTED), ("interleaved", 7, INVALID), ("magnitude", -1.0, INVALID)):

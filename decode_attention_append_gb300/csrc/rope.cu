@@ -36,13 +36,11 @@ namespace {
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kP = 16;
 // heads of a lane in flight
-template <int TARGET> constexpr int kAheadOf = 4;
-template <> constexpr int kAheadOf<kRopePagesQ4> = 3;
+template <int TARGET> constexpr int kAheadOf = 5;
+template <> constexpr int kAheadOf<kRopePagesQ4> = 2;
 template <> constexpr int kAheadOf<kRopeRows> = 2;
-
-// Where a row's k and v go: page * 16 + slot, or:
-constexpr int64_t kNoPage = -1;  // a bad page id: its q is rotated all the same
-constexpr int64_t kNoRow = -2;   // a row of no request: nothing of it is written
+// CTAs of an SM that registers are left for
+constexpr int ctas_of(int target, bool norm) { return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? 4 : (norm ? 4 : 5); }
 
 // ------------------------------------------------------------------- angles
 // Sine and cosine of n / 256 turns, each as the sum of two fp32 numbers.
@@ -190,9 +188,9 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
 }
 
 // ------------------------------------------------------------- a row's place
-// The page and slot of new row `row`, and its position; a warp's lanes together.
-__device__ __forceinline__ int64_t find_place(const RopeArgs& a, int row, int lane, int& pos) {
-  pos = 0;
+// New row `row`: its position in its request and the index of its page id, or false for
+// a row of which nothing is written.  A warp's lanes together.
+__device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane, int& pos, int& page_at) {
   // the last request r with append_indptr[r] <= row: narrowed to 256 by probes, then counted
   int lo = 0, n = a.batch;
   while (n > 256) {
@@ -211,7 +209,8 @@ __device__ __forceinline__ int64_t find_place(const RopeArgs& a, int row, int la
       if (32 * i < n && 32 * i + lane < n) v[i] = ld_word(a.append_indptr + lo + 32 * i + lane);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r += __popc(__ballot_sync(0xffffffffu, v[i] <= row));
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < n) r += __popc(__ballot_sync(0xffffffffu, v[i] <= row));
   }
   r = max(r, 0);
   const int32_t* p = lane == 0   ? a.append_indptr + r
@@ -224,23 +223,19 @@ __device__ __forceinline__ int64_t find_place(const RopeArgs& a, int row, int la
   const int a0 = __shfl_sync(0xffffffffu, word, 0), a1 = __shfl_sync(0xffffffffu, word, 1);
   const int p0 = __shfl_sync(0xffffffffu, word, 2), np = __shfl_sync(0xffffffffu, word, 3) - p0;
   const int last_len = __shfl_sync(0xffffffffu, word, 4);
-  if (row >= __shfl_sync(0xffffffffu, word, 5)) return kNoRow;  // padding behind the last request
+  if (row >= __shfl_sync(0xffffffffu, word, 5)) return false;  // padding behind the last request
   const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * kP + last_len : 0;
   if (row < a0 || row >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || p0 < 0 || last_len < 1 || last_len > kP) {
     set_device_error(a.err, kDevErrShape);
-    return kNoRow;
+    return false;
   }
   pos = (int)kv_len - (a1 - a0) + (row - a0);
-  const int64_t page = ld_word(a.page_indices + p0 + pos / kP);
-  if (page < 0 || page >= a.num_pages) {
-    set_device_error(a.err, kDevErrPageRange);
-    return kNoPage;
-  }
-  return page * kP + pos % kP;
+  page_at = p0 + pos / kP;
+  return true;
 }
 
 template <int D, int TARGET, bool NORM>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
   constexpr int kAhead = kAheadOf<TARGET>;
@@ -248,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   __shared__ uint64_t s_turns[64];
   // a row's cosines and sines; of both, 16 bits and what these leave
   __shared__ __align__(16) float s_angle[kWarps][Q4 ? 6 : 2][64];
-  __shared__ __align__(16) float s_w[NORM ? 2 : 1][D];
+  __shared__ __align__(16) float s_w[NORM ? 2 : 1][D];  // norm weights of q and k
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, group = lane / L, j = lane % L;
   const uint32_t mask = (L == 8 ? 0xFFu : 0xFu) << (lane & ~(L - 1));  // the head's lanes
@@ -257,21 +252,22 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   if (tid < 64) s_turns[tid] = a.turns[tid];
   __syncthreads();
   grid_dep_wait();
-  if (NORM) {
-    for (int t = tid; t < 2 * D; t += kThreads) {
-      const uint16_t* n = t < D ? a.q_norm : a.k_norm;
-      uint16_t b = 0;
-      if (n) asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(n + t % D));
-      s_w[t / D][t % D] = __uint_as_float((uint32_t)b << 16);
-    }
-    __syncthreads();
+  // norm weights: asked for now, in shared memory once the first heads are asked for too
+  constexpr int kWeights = NORM ? 2 * D / kThreads : 0;
+  uint16_t weight[NORM ? kWeights : 1];
+#pragma unroll
+  for (int i = 0; i < kWeights; ++i) {
+    const int t = tid + i * kThreads;
+    const uint16_t* n = t < D ? a.q_norm : a.k_norm;
+    weight[i] = 0;
+    if (n) asm volatile("ld.global.u16 %0, [%1];" : "=h"(weight[i]) : "l"(n + t % D));
   }
 
   const int task = blockIdx.x * kWarps + warp;
   const int row = task / a.parts, first = (task - row * a.parts) * a.part_heads;
-  if (row >= a.n_rows) return;
+  const bool live = row < a.n_rows;
   const int H = a.Hq + (APPEND ? 2 : 1) * a.Hk;
-  const int end = min(first + a.part_heads, H);
+  const int end = live ? min(first + a.part_heads, H) : 0;
   // chunks of 8 dims of this lane; in a 4-bit cache's rows two side by side, a block
   const int nrot = a.rotary_dim / 16;
   const bool pairs = a.interleaved != 0;
@@ -294,13 +290,21 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   for (int u = 0; u < kAhead; ++u)
     if (first + u * G + group < end) load(first + u * G + group, w[u]);
 
-  int pos = 0;
-  int64_t at = 0;
-  if (APPEND) {
-    at = find_place(a, row, lane, pos);
-    if (at == kNoRow) return;
+  int given = 0;
+  if (live && a.positions) given = ld_word(a.positions + row);
+  if (NORM) {
+#pragma unroll
+    for (int i = 0; i < kWeights; ++i)
+      s_w[(tid + i * kThreads) / D][(tid + i * kThreads) % D] = __uint_as_float((uint32_t)weight[i] << 16);
+    __syncthreads();
   }
-  if (a.positions) pos = ld_word(a.positions + row);
+  if (!live) return;
+  int place = 0, page_at = 0, page = 0;
+  if (APPEND) {
+    if (!find_place(a, row, lane, place, page_at)) return;
+    page = ld_word(a.page_indices + page_at);
+  }
+  const int pos = a.positions ? given : place, slot = place % kP;
   float(&angle)[Q4 ? 6 : 2][64] = s_angle[warp];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -480,8 +484,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   };
 
   uint16_t* q_out = a.q_out.p + row * a.q_out.row;
-  const int64_t page = at / kP;
-  const int slot = (int)(at % kP);
+  const bool no_page = APPEND && (page < 0 || page >= a.num_pages);  // its q is rotated all the same
+  if (no_page) set_device_error(a.err, kDevErrPageRange);
   auto finish = [&](int head, uint32_t (&v)[8]) {
     const int h = head - a.Hq;  // of k, then of v
     const bool is_q = h < 0, is_k = !is_q && (!APPEND || h < a.Hk);
@@ -494,10 +498,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       uint16_t* p = is_q ? q_out + head * a.q_out.head : a.k_out.p + row * a.k_out.row + h * a.k_out.head;
       st_16(p + 8 * c0, v);
       st_16(p + 8 * c1, v + 4);
-    } else if (at == kNoPage) {
+    } else if (no_page) {
     } else if (!Q4) {
       // a page is [2][Hk][16][D]: v's heads follow k's
-      uint16_t* p = reinterpret_cast<uint16_t*>(a.pool) + ((page * 2 * a.Hk + h) * kP + slot) * D;
+      uint16_t* p = reinterpret_cast<uint16_t*>(a.pool) + (((int64_t)page * 2 * a.Hk + h) * kP + slot) * D;
       st_16(p + 8 * c0, v);
       st_16(p + 8 * c1, v + 4);
     } else {
@@ -522,7 +526,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       const float me = a.kv_exp ? q4_pow2(-ld_word(a.kv_exp + h)) : 1.f;
       uint8_t scale;
       const uint2 codes = quantise_block(b[0], b[1], me, scale);
-      uint8_t* slice = a.pool + ((page * a.Hk + hk) * 2 + kv) * (int64_t)q4_slice_bytes(D);
+      uint8_t* slice = a.pool + (((int64_t)page * a.Hk + hk) * 2 + kv) * q4_slice_bytes(D);
       *reinterpret_cast<uint2*>(slice + slot * (D / 2) + j * 8) = codes;
       slice[kP * (D / 2) + (kv == 0 ? slot * L + j : j * kP + slot)] = scale;
     }

@@ -31,10 +31,12 @@ page), int32 CSR arrays on the same CUDA device.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
 import importlib.util
+import math
 import os
 import threading
 import weakref
@@ -43,7 +45,7 @@ from dataclasses import dataclass
 import numpy as np
 import torch
 
-from .rope import rope_frequencies
+from .rope import frequencies_of, rope_frequencies
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libdaa.so")
@@ -1266,8 +1268,8 @@ class Rope:
     by position * ``frequencies[i]`` and is multiplied by ``magnitude``.  Pairs are dims
     (i, i + rotary_dim / 2), or (2i, 2i + 1) when ``interleaved``.  The frequencies are
     those of ``base`` and ``scaling`` (``rope_frequencies``), or given as
-    ``frequencies`` (radians a token, rotary_dim / 2 of them).  Host data, for every
-    device and layer."""
+    ``frequencies`` (radians a token, rotary_dim / 2 of them).  Host data, fixed once it
+    is made, for every device and layer."""
 
     def __init__(self, head_dim, base=10000.0, rotary_dim=None, interleaved=False, scaling=None, frequencies=None,
                  magnitude=None):
@@ -1275,19 +1277,24 @@ class Rope:
         self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
         self.interleaved = bool(interleaved)
         if frequencies is None:
-            f, m = rope_frequencies(self.rotary_dim, base, scaling)
+            f, m = frequencies_of(self.rotary_dim, base, scaling)
         elif scaling is not None:
             raise ValueError("a scaling changes the base's frequencies: give one of scaling and frequencies")
         else:
-            f, m = np.array(frequencies, np.float64), 1.0
-        if f.shape != (self.rotary_dim // 2,) or not np.isfinite(f).all():
+            f, m = [float(x) for x in frequencies], 1.0
+        if len(f) != self.rotary_dim // 2 or not all(map(math.isfinite, f)):
             raise ValueError("frequencies must be rotary_dim / 2 finite numbers")
-        self.frequencies = f = np.ascontiguousarray(f)
+        self._frequencies = array.array("d", f)
         self.magnitude = float(m if magnitude is None else magnitude)
         self._rope = _Rope()
         _check(load_library().daa_rope_init(ctypes.byref(self._rope), self.head_dim, self.rotary_dim,
-                                            int(self.interleaved), _ptr(f), self.magnitude), "Rope")
-        self._addr = ctypes.addressof(self._rope)
+                                            int(self.interleaved), self._frequencies.buffer_info()[0],
+                                            self.magnitude), "Rope")
+
+    @property
+    def frequencies(self) -> np.ndarray:
+        """Radians a token of each pair (a copy)."""
+        return np.array(self._frequencies)
 
 
 _native = None
@@ -1324,7 +1331,7 @@ def _handle(stream):
 def _rope_addr(rope):
     if not isinstance(rope, Rope):
         raise TypeError("rope must be a Rope")
-    return rope._addr
+    return ctypes.addressof(rope._rope)
 
 
 def apply_rope(q, k, positions, rope, q_out=None, k_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
@@ -1367,8 +1374,9 @@ def append_rope(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indpt
 
 def append_rope_q4(q, k_new, v_new, kv_pages, append_indptr, page_indices, kv_indptr, last_page_len, rope,
                    positions=None, kv_exp=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6, stream=None):
-    """``append_rope`` into a 4-bit pool: the rotated keys (in bf16) and v_new are quantised
-    as ``kv_append_q4`` does."""
+    """``append_rope`` into a 4-bit pool: the rotated keys and v_new are quantised as
+    ``kv_append_q4`` does.  These keys are rotated to the nearest fp32 value, and rounded
+    to bf16 from that, so that a code does not hang on the order of fp32 operations."""
     if q_out is None and q is not None:
         q_out = _rows_like(q, "q", stream)
     st = (_native or _load_native()).append_rope_q4(q, k_new, v_new, kv_pages, kv_exp, append_indptr, page_indices,

@@ -112,7 +112,9 @@ daa_status common_args(const daa_rope* rope, const daa_rope_rows* io, int64_t q_
   if ((io->q_norm || io->k_norm) && !(std::isfinite(io->eps) && io->eps >= 0.f)) return DAA_ERR_INVALID_ARG;
   if (!aligned(io->q_norm, 2) || !aligned(io->k_norm, 2) || !aligned(io->positions, 4)) return DAA_ERR_ALIGNMENT;
   if (n == 0) return DAA_OK;
-  if (n * (q_heads + (append ? 2 : 1) * k_heads) > INT32_MAX) return DAA_ERR_UNSUPPORTED;
+  if (q_heads > DAA_ROPE_MAX_HEADS || k_heads > DAA_ROPE_MAX_HEADS ||
+      n * (q_heads + (append ? 2 : 1) * k_heads) > DAA_ROPE_MAX_HEADS)
+    return DAA_ERR_UNSUPPORTED;
   struct One {
     const daa_rows* x;
     int64_t heads;
@@ -181,6 +183,7 @@ daa_status append(const daa_rope* rope, const daa_rope_rows* io, void* kv_pages,
   if (st != DAA_OK) return st;
   if (io->num_rows == 0) return DAA_OK;
   if (batch == 0) return DAA_ERR_SHAPE;
+  if (batch > DAA_ROPE_MAX_HEADS) return DAA_ERR_UNSUPPORTED;
   if (!kv_pages || !append_indptr || !page_indices || !kv_indptr || !last_page_len) return DAA_ERR_INVALID_ARG;
   if (!aligned(kv_pages, 16) || !aligned(kv_exp, 4) || !aligned(append_indptr, 4) || !aligned(page_indices, 4) ||
       !aligned(kv_indptr, 4) || !aligned(last_page_len, 4))

@@ -218,14 +218,17 @@ __device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane,
                      : lane == 2 ? a.kv_indptr + r
                      : lane == 3 ? a.kv_indptr + r + 1
                      : lane == 4 ? a.last_page_len + r
-                                 : a.append_indptr + a.batch;
-  const int word = lane < 6 ? ld_word(p) : 0;
+                     : lane == 5 ? a.append_indptr + a.batch
+                                 : a.kv_indptr + a.batch;
+  const int word = lane < 7 ? ld_word(p) : 0;
   const int a0 = __shfl_sync(0xffffffffu, word, 0), a1 = __shfl_sync(0xffffffffu, word, 1);
   const int p0 = __shfl_sync(0xffffffffu, word, 2), np = __shfl_sync(0xffffffffu, word, 3) - p0;
   const int last_len = __shfl_sync(0xffffffffu, word, 4);
   if (row >= __shfl_sync(0xffffffffu, word, 5)) return false;  // padding behind the last request
   const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * kP + last_len : 0;
-  if (row < a0 || row >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || p0 < 0 || last_len < 1 || last_len > kP) {
+  const int64_t pages_end = __shfl_sync(0xffffffffu, word, 6);
+  if (row < a0 || row >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || p0 < 0 || (int64_t)p0 + np > pages_end ||
+      last_len < 1 || last_len > kP) {
     set_device_error(a.err, kDevErrShape);
     return false;
   }
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
     const bool side = side_by_side(head);
     const int d0 = side ? 2 * j : c0, d1 = side ? 2 * j + 1 : c1;
     // past 2^100 products leave fp32's range, and their small parts are no numbers
-    if (Q4 && is_k && (NORM || max_abs_bits(v) < 0x7180u)) rotate_exactly(v, d0, d1);
+    if (Q4 && is_k && ((NORM && a.k_norm) || max_abs_bits(v) < 0x7180u)) rotate_exactly(v, d0, d1);
     else if (is_q || is_k) rotate(v, is_q);
     if (is_q || !APPEND) {
       uint16_t* p = is_q ? q_out + head * a.q_out.head : a.k_out.p + row * a.k_out.row + h * a.k_out.head;

@@ -28,6 +28,12 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
     * ``wavelength``: pairs of ``high`` (4) turns or more in the ``original`` context
       as they were, of ``low`` (1) or fewer f_i / s, mixed in between by their turns.
     """
+    f, m = frequencies_of(rotary_dim, base, scaling)
+    return np.array(f), m
+
+
+def frequencies_of(rotary_dim, base, scaling):
+    """``rope_frequencies`` with the frequencies in a list."""
     n, base = int(rotary_dim), float(base)
     if n < 2 or n % 2:
         raise ValueError("rotary_dim must be even and at least 2")
@@ -35,7 +41,7 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
         raise ValueError("base must be finite and > 0")
     f = [base ** (-2 * i / n) for i in range(n // 2)]
     if scaling is None:
-        return np.array(f), 1.0
+        return f, 1.0
     kind = scaling.get("type")
     if kind not in _SCALINGS:
         raise ValueError(f"scaling type must be one of {', '.join(sorted(_SCALINGS))}")
@@ -52,18 +58,18 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
             raise ValueError(f"{kind} scaling needs the original context, > 0")
         turns = float(original) / (2 * math.pi)
     if kind == "linear":
-        return np.array(f) / s, 1.0
+        return [x / s for x in f], 1.0
     if kind == "ntk":
         if n < 4:
             raise ValueError("ntk scaling needs a rotary_dim of 4 or more")
         base *= s ** (n / (n - 2))
-        return np.array([base ** (-2 * i / n) for i in range(n // 2)]), 1.0
+        return [base ** (-2 * i / n) for i in range(n // 2)], 1.0
     if kind == "wavelength":
         low, high = float(scaling.get("low", 1.0)), float(scaling.get("high", 4.0))
         if not 0 <= low < high < math.inf:
             raise ValueError("wavelength scaling needs 0 <= low < high")
         keep = [min(max((turns * x - low) / (high - low), 0.0), 1.0) for x in f]
-        return np.array([k * x + (1 - k) * x / s for k, x in zip(keep, f)]), 1.0
+        return [k * x + (1 - k) * x / s for k, x in zip(keep, f)], 1.0
     fast, slow = float(scaling.get("beta_fast", 32.0)), float(scaling.get("beta_slow", 1.0))
     if not 0 < slow <= fast < math.inf or base <= 1:
         raise ValueError("yarn scaling needs 0 < beta_slow <= beta_fast and a base > 1")
@@ -71,4 +77,4 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=None):
     pair_of = lambda b: n / 2 * math.log(turns / b) / math.log(base)  # noqa: E731
     lo, hi = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), n - 1)
     mix = [min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0) for i in range(n // 2)]
-    return np.array([x * (1 - k) + x / s * k for k, x in zip(mix, f)]), float(scaling.get("magnitude", 0.1 * math.log(s) + 1))
+    return [x * (1 - k) + x / s * k for k, x in zip(mix, f)], float(scaling.get("magnitude", 0.1 * math.log(s) + 1))

@@ -674,7 +674,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
  * and the other dims stay as they are.  With norm weights (q_norm, k_norm: bf16
  * [head_dim]) a head is first divided by sqrt(mean of its squares + eps) and
  * multiplied by the weights, all of its dims.  Computed in fp32, rounded once to
- * bf16; the angle is good to 2^-31 of a turn at every position from -2^31 to
+ * bf16; the angle is good to 2^-33 of a turn at every position from -2^31 to
  * 2^31 - 1.  Dims that are neither normalised nor rotated keep their bits.  (The
  * squares are summed in fp32: heads of values past about 10^18 have no norm.)
  * Rotating by negated positions is the transposed rotation: it takes gradients of
@@ -689,6 +689,7 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
  * DAA_ROPE_MAX_MAGNITUDE, or |radians| that is not at most DAA_ROPE_MAX_RADIANS.
  */
 #define DAA_ROPE_MAX_RADIANS 1048576.0
+#define DAA_ROPE_MAX_HEADS 1073741824 /* of all rows of a call */
 #define DAA_ROPE_MIN_MAGNITUDE 0.0009765625
 #define DAA_ROPE_MAX_MAGNITUDE 1024.0
 
@@ -729,7 +730,10 @@ typedef struct {
  *
  * daa_append_rope, daa_append_rope_q4: daa_kv_append and daa_kv_append_q4 of the
  * rotated k and of v, and q_out = rotated q, in one pass over the projections'
- * rows.  The pages get exactly the bytes of daa_apply_rope followed by those calls.
+ * rows.  bf16 pages get exactly the bytes of daa_apply_rope followed by daa_kv_append.
+ * Keys on their way to 4 bits are rotated to the nearest fp32 value (up to one in some
+ * 2^13 that lies next to the middle of two), rounded to bf16 from that, and quantised:
+ * their codes are those of the definition, not of an order of fp32 operations.
  * Rows belong to requests by append_indptr, and a row's position is its place in
  * its request, kv_len_r - n_r + t, unless `positions` gives others (draft trees:
  * the depths; the page and slot are by its place always).  q.data NULL: there are
@@ -747,8 +751,8 @@ typedef struct {
  * graph, and calls on different rows and pages may overlap.
  * Errors: DAA_ERR_INVALID_ARG for NULL arguments (positions of daa_apply_rope among
  * them), negative counts or strides, an eps or overlap as above, a rope of another
- * head_dim than dims; DAA_ERR_UNSUPPORTED for more than 2^31 - 1 heads of all rows,
- * and shapes as daa_kv_append; DAA_ERR_SHAPE for rows without requests (batch 0);
+ * head_dim than dims; DAA_ERR_UNSUPPORTED for more than DAA_ROPE_MAX_HEADS heads of
+ * all rows or requests, and shapes as daa_kv_append; DAA_ERR_SHAPE for rows without requests (batch 0);
  * DAA_ERR_ALIGNMENT; DAA_ERR_CUDA.  Lengths and page ids are checked on the device:
  * nothing is written for a row of a request with inconsistent lengths (error word 3);
  * of a row whose page id is outside the pool only q_out is (error word 1).

@@ -39,11 +39,10 @@ def _angle(p, f):
 
 def check(got, want, norm):
     """Values of bf16 rows against (y, size) of ``rotate``, by the roundings on the way:
-    angle   2^-32 turns cut off and p 2^-65 turns of the frequency's rounding (below 2^-28 rad), and the reduced angle to
-            fp32: half a step of a value up to one half-turn, 2^-25 half-turns, 2^-23.3 rad
-    sines   off by at most two steps, 2^-23; the magnitude and its product 2^-24 each
+    angle   p 2^-65 turns of the frequency's rounding and 2^-40 turns cut off: below 2^-31 rad
+    sines   to fp32 by one rounding, 2^-24, from values that are good to 2^-35
     turn    a product, a fused product: 2^-24 of each of the two terms and of the result
-    together below m (|a| + |b|) (2^-23.3 + 2^-23 + 2^-23 + 2^-23 + 2^-28) < size 2^-21
+    together below m (|a| + |b|) (2^-31 + 2^-24 + 2^-35 + 2^-23) < size 2^-21
     norm    the sum of squares: 19 additions, halved by the root, 9.5 2^-24; mean and eps 2 2^-24; the root 2^-22; two
             products 2 2^-24: below 18 2^-24 < 2^-19.8 of each value, 2^-19.2 with the above
     out     half a step of bf16, 2^-8 of the value"""

@@ -415,6 +415,90 @@ def test_bad_pages_and_lengths(daa, q4):
                 assert torch.equal(slot_of(pool, page, s), slot_of(good, page, s))
 
 
+def test_page_lists_that_end_too_early(daa):
+    """kv_indptr that goes on past its own end: nothing behind it is read, and the request's rows are refused."""
+    rng = np.random.default_rng(21)
+    t, n = q4_support.make_table(rng, [20, 20], [4, 4])
+    q, k, v = _rows(rng, 8, 4, 2, 64, "flat")
+    rope, pool = daa.Rope(64), _nan_pool(n, 2, 64)
+    b = {x: y.copy() for x, y in t.items()}
+    b["kv_indptr"][1] = 10 ** 6  # request 0 owns a million pages, of four
+    out = torch.full((8, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    daa.append_rope(q, k, v, pool, *_dev_table(b), rope, q_out=out)
+    assert daa.device_error(reset=True) == 3
+    assert (out == 7).all() and (pool.view(torch.int16) == NAN).all()
+
+
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("how", ["flat", "fused", "heads"])
+def test_append_in_place(daa, q4, how):
+    """The rotated queries in the place of the given ones, k and v beside them untouched."""
+    rng = np.random.default_rng(22)
+    t, n = q4_support.make_table(rng, [20, 300], [50, 1])
+    q, k, v = _rows(rng, 51, 6, 2, 128, how)
+    rope, tab = daa.Rope(128, rotary_dim=96), _dev_table(t)
+    call = daa.append_rope_q4 if q4 else daa.append_rope
+    pool = daa.new_q4_pool(n, 2, 128) if q4 else _nan_pool(n, 2, 128)
+    want, k0, v0 = pool.clone(), k.clone(), v.clone()
+    q_want = call(q, k, v, want, *tab, rope)
+    assert call(q, k, v, pool, *tab, rope, q_out=q) is q
+    assert torch.equal(q, q_want) and torch.equal(k, k0) and torch.equal(v, v0)
+    assert torch.equal(pool.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+def test_keys_that_are_no_numbers_into_4_bits(daa, norm):
+    """As the cache stores them: NaN as zero, infinities as the largest values, rotated first; and keys of any size."""
+    rng = np.random.default_rng(23)
+    t, n = q4_support.make_table(rng, [3], [6])
+    tab, rope = _dev_table(t), daa.Rope(64, rotary_dim=32)
+    q, k, v = _rows(rng, 6, 2, 1, 64, "flat")
+    k.view(torch.int16)[1, 0, 40] = 0x7F80  # not rotated
+    k.view(torch.int16)[2, 0, 3] = -0x80  # rotated: with its mate no number, or infinite
+    k.view(torch.int16)[3, 0, 50] = 0x7FC1
+    k[4] *= 2.0 ** 101
+    k[5] *= 2.0 ** -101
+    v.view(torch.int16)[0, 0, 9] = 0x7F80
+    pos = _dev(ref.places(t)[:, 3].astype(np.int32))
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV) if norm else None
+    pool, want = daa.new_q4_pool(n, 1, 64), daa.new_q4_pool(n, 1, 64)
+    daa.append_rope_q4(q, k, v, pool, *tab, rope, q_norm=w)  # the norm is q's alone
+    _, k_want = daa.apply_rope(q, k, pos, rope)
+    exact = _exact_keys(k[[0, 5]], ref.places(t)[[0, 5], 3], rope, None)
+    k_want[[0, 5]] = exact
+    daa.kv_append_q4(k_want, v, want, *tab)
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_pages_and_rows_past_32_bits(daa, q4):
+    """The last page of a pool of more than 2^32 bytes and values, and rows more than 2^31 elements apart."""
+    rng = np.random.default_rng(24)
+    hk, d = 16, 128
+    n = (1 << 32) // (hk * 2 * (9 * d if q4 else 16 * d)) + 3
+    pool = torch.empty(n, hk, 2, 9 * d, dtype=torch.uint8, device=DEV) if q4 else torch.empty(n, 2, hk, 16, d, dtype=torch.bfloat16, device=DEV)
+    assert pool.numel() > 1 << 32
+    pool[[0, n - 2, n - 1]] = 0
+    i32 = lambda x: _dev(np.array(x, np.int32))  # noqa: E731
+    tab = i32([0, 2]), i32([n - 1, n - 2]), i32([0, 2]), i32([1])
+    far = (1 << 31) + 8
+    x = torch.empty(far + 18 * d, dtype=torch.bfloat16, device=DEV)
+    rows = _bf16(rng, (2, 48, d))
+    q, k, v = (x.as_strided((2, h, d), (far, d, 1), o * d) for h, o in ((16, 0), (1, 16), (1, 17)))
+    k, v = k.expand(2, hk, d), v.expand(2, hk, d)
+    q.copy_(rows[:, :16])
+    k[:, :1].copy_(rows[:, 16:17])
+    v[:, :1].copy_(rows[:, 17:18])
+    rope = daa.Rope(d)
+    call = daa.append_rope_q4 if q4 else daa.append_rope
+    got = call(q, k, v, pool, *tab, rope)
+    small = torch.zeros_like(pool[:2])
+    want = call(q.contiguous(), k.contiguous(), v.contiguous(), small, tab[0], i32([1, 0]), *tab[2:], rope)
+    assert torch.equal(got, want) and torch.equal(pool[n - 2:], small) and not pool[0].any()
+    daa.append_rope(q, k, v, pool, *tab, rope, q_out=q) if not q4 else daa.append_rope_q4(q, k, v, pool, *tab, rope, q_out=q)
+    assert torch.equal(q, want)
+
+
 @pytest.mark.parametrize("q4", [False, True])
 def test_empty_calls(daa, q4):
     rope = daa.Rope(64)

@@ -104,6 +104,23 @@ def test_python_refusals(daa):
         daa.append_rope_q4(x, x, x, torch.zeros(4, 2, 2, 9 * 64, dtype=torch.uint8), pos, pos, pos, pos, rope)
 
 
+def test_copies_of_a_rope_stand_alone(daa):
+    import copy
+    import gc
+    import pickle
+    r = daa.Rope(128, rotary_dim=64, interleaved=True, scaling=dict(type="yarn", factor=4.0, original=512))
+    want = bytes(r._rope)
+    others = [copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))]
+    f = r.frequencies
+    f[:] = 0  # a copy
+    assert r.frequencies.all()
+    del r
+    gc.collect()
+    for o in others:
+        assert daa._rope_addr(o) == ctypes.addressof(o._rope) and bytes(o._rope) == want
+        assert o.magnitude == others[0].magnitude and np.array_equal(o.frequencies, others[0].frequencies)
+
+
 def _append(daa, q4=False, batch=0, rope=None, pool=0x70000000, table=A, dims=(4, 2, 64, 16, 64), rows=8, **change):
     """An append of 8 rows that cannot launch: with batch 0 it is refused as SHAPE once its rows are accepted."""
     T = 512  # elements of a projection's row: q, k, v
@@ -114,8 +131,8 @@ def _append(daa, q4=False, batch=0, rope=None, pool=0x70000000, table=A, dims=(4
     lib = daa.load_library()
     tab = [table, A, A, A]
     if q4:
-        return lib.daa_append_rope_q4(rope._addr, rec, pool, None, *tab, batch, daa._Dims(*dims), None)
-    return lib.daa_append_rope(rope._addr, rec, pool, *tab, batch, daa._Dims(*dims), None)
+        return lib.daa_append_rope_q4(ctypes.addressof(rope._rope), rec, pool, None, *tab, batch, daa._Dims(*dims), None)
+    return lib.daa_append_rope(ctypes.addressof(rope._rope), rec, pool, *tab, batch, daa._Dims(*dims), None)
 
 
 @pytest.mark.parametrize("q4", [False, True])
@@ -160,14 +177,14 @@ def test_bad_records_are_refused(daa):
     rope = daa.Rope(64)
     rec = _rec(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, A, 0, 0, 0.0)
     assert lib.daa_apply_rope(None, rec, 1, 0, None) == INVALID
-    assert lib.daa_apply_rope(rope._addr, None, 1, 0, None) == INVALID
-    assert lib.daa_apply_rope(rope._addr, rec, 0, 1, None) == INVALID
-    assert lib.daa_apply_rope(rope._addr, rec, 1, -1, None) == INVALID
-    assert lib.daa_apply_rope(rope._addr, rec, 1, 1, None) == INVALID  # no k
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), None, 1, 0, None) == INVALID
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), rec, 0, 1, None) == INVALID
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), rec, 1, -1, None) == INVALID
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), rec, 1, 1, None) == INVALID  # no k
     none = _rec(A, 64, 64, 0, 0, 0, 0, 0, 0, 0x900000, 64, 64, 0, 0, 0, 8, 0, 0, 0, 0.0)
-    assert lib.daa_apply_rope(rope._addr, none, 1, 0, None) == INVALID  # no positions
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), none, 1, 0, None) == INVALID  # no positions
     empty = _rec(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0.0)
-    assert lib.daa_apply_rope(rope._addr, empty, 1, 1, None) == OK
+    assert lib.daa_apply_rope(ctypes.addressof(rope._rope), empty, 1, 1, None) == OK
     other = daa._Rope.from_buffer_copy(bytes(rope._rope))
     for field, value, expect in (("rotary_dim", 72, UNSUPPORTED), ("head_dim", 32, UNSUPPORTED), ("interleaved", 7, INVALID), ("magnitude", -1.0, INVALID)):
         bad = daa._Rope.from_buffer_copy(bytes(other))

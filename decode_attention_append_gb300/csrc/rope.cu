@@ -35,12 +35,18 @@ namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr int kP = 16;
-// heads of a lane in flight
-template <int TARGET> constexpr int kAheadOf = 5;
-template <> constexpr int kAheadOf<kRopePagesQ4> = 2;
-template <> constexpr int kAheadOf<kRopeRows> = 2;
-// CTAs of an SM that registers are left for
-constexpr int ctas_of(int target, bool norm) { return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? 4 : (norm ? 4 : 5); }
+// Heads of a lane in flight, and CTAs of an SM that registers are left for.  Rows are
+// bound by HBM and want warps: 16,416 rows of 72 heads 96 us with two and 7 CTAs, 104
+// with 6, 98 with 8 (spills).  Pages want loads in flight: 32,832 rows of 80 heads 200
+// us with five heads and 4 CTAs, 202 with four.  The 4-bit append is bound by
+// instructions and latency: 36,760 rows of 48 heads 147 us with three and 5 CTAs, 155
+// with two, 158 with 4 CTAs; with norms (96 registers do not hold it) 4 CTAs.
+constexpr int ahead_of(int target, bool norm) {
+  return target == kRopeRows ? 2 : target == kRopePages ? 5 : norm ? 2 : 3;
+}
+constexpr int ctas_of(int target, bool norm) {
+  return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? 4 : (norm ? 4 : 5);
+}
 
 // ------------------------------------------------------------------- angles
 // Sine and cosine of n / 256 turns, each as the sum of two fp32 numbers.
@@ -78,65 +84,113 @@ constexpr SineTable make_table() {
 
 __device__ constexpr SineTable g_sines = make_table();
 
+// Two fp32 numbers in one instruction, each rounded by itself; below, T is float or F2.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 both(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void apart(F2 x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 neg(F2 a) { return F2{a.v ^ 0x8000000080000000ull}; }
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, both(-1.f, -1.f), a); }
+__device__ __forceinline__ float mul(float a, float b) { return __fmul_rn(a, b); }
+__device__ __forceinline__ float add(float a, float b) { return __fadd_rn(a, b); }
+__device__ __forceinline__ float fma(float a, float b, float c) { return __fmaf_rn(a, b, c); }
+__device__ __forceinline__ float neg(float a) { return -a; }
+__device__ __forceinline__ float sub(float a, float b) { return __fsub_rn(a, b); }
+__device__ __forceinline__ F2 same(float a) { return both(a, a); }
+
 // a + b = s + e exactly.
-__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
-  s = __fadd_rn(a, b);
-  const float t = __fsub_rn(s, a);
-  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+template <class T>
+__device__ __forceinline__ void two_sum(T a, T b, T& s, T& e) {
+  s = add(a, b);
+  const T t = sub(s, a);
+  e = add(sub(a, sub(s, t)), sub(b, t));
 }
 // a b = p + e exactly.
-__device__ __forceinline__ void two_prod(float a, float b, float& p, float& e) {
-  p = __fmul_rn(a, b);
-  e = __fmaf_rn(a, b, -p);
+template <class T>
+__device__ __forceinline__ void two_prod(T a, T b, T& p, T& e) {
+  p = mul(a, b);
+  e = fma(a, b, neg(p));
 }
 
-// m cos and m sin of phase * 2^-64 turns, each the sum of two fp32 numbers, good to 2^-35 of m.
+// m cos and m sin of two phases of 2^-64 turns, each the sum of two fp32 numbers, good to
+// 2^-35 of m.
 struct CosSin {
-  float ch, cl, sh, sl;
+  F2 ch, cl, sh, sl;
 };
-__device__ __forceinline__ CosSin cos_sin(uint64_t phase, const float4* table, float mh, float ml) {
-  const uint32_t n = (uint32_t)((phase + (1ull << 55)) >> 56);
-  const int64_t rest = (int64_t)(phase - ((uint64_t)n << 56));  // -2^55 .. 2^55 - 1
-  const float4 t = table[n];
-  // d = vh + vl radians, |d| <= pi / 256: from 2^-40 turns in two parts
+__device__ __forceinline__ CosSin cos_sin(uint64_t phase0, uint64_t phase1, const float4* table, float mh, float ml) {
+  // d = dh + dl in 2^-40 turns beside the table's angle, |d| <= 1 / 512 turns
+  auto split = [&](uint64_t phase, float4& t, float& dh, float& dl) {
+    const uint32_t n = (uint32_t)((phase + (1ull << 55)) >> 56);
+    const int32_t r = (int32_t)((int64_t)(phase - ((uint64_t)n << 56)) >> 24);
+    t = table[n];
+    dh = (float)r;
+    dl = (float)(r - (int32_t)dh);
+  };
+  float4 t0, t1;
+  float dh0, dl0, dh1, dl1;
+  split(phase0, t0, dh0, dl0);
+  split(phase1, t1, dh1, dl1);
+  const F2 C = both(t0.x, t1.x), Cl = both(t0.y, t1.y), S = both(t0.z, t1.z), Sl = both(t0.w, t1.w);
+  const F2 dh = both(dh0, dh1), dl = both(dl0, dl1);
+  // in radians vh + vl, |d| <= pi / 256
   constexpr double unit = kTwoPi / 1099511627776.0;
   constexpr float kh = (float)unit, kl = (float)(unit - kh);
-  const int32_t r = (int32_t)(rest >> 24);
-  const float dh = (float)r, dl = (float)(r - (int32_t)dh);
-  float vh, vl;
-  two_prod(dh, kh, vh, vl);
-  vl = __fadd_rn(vl, __fmaf_rn(dh, kl, __fmul_rn(dl, kh)));
+  F2 vh, vl;
+  two_prod(dh, same(kh), vh, vl);
+  vl = add(vl, fma(dh, same(kl), mul(dl, same(kh))));
   // cos d - 1 = u + ul, sin d = vh + sl:  d^2 / 2 <= 2^-13.7, d^3 / 6 <= 2^-21.6
-  float z, zl;
+  F2 z, zl;
   two_prod(vh, vh, z, zl);
-  const float u = -0.5f * z;
-  const float ul = __fmaf_rn(z * z, 1.f / 24, __fmaf_rn(-vh, vl, -0.5f * zl));
-  const float sl = __fmaf_rn(vh * z, __fmaf_rn(z, 1.f / 120, -1.f / 6), vl);
+  const F2 half = same(-0.5f), u = mul(z, half);
+  const F2 ul = fma(mul(z, z), same(1.f / 24), fma(neg(vh), vl, mul(zl, half)));
+  const F2 sl = fma(mul(vh, z), fma(z, same(1.f / 120), same(-1.f / 6)), vl);
   // cos (t + d) = C + C u - S v,  sin (t + d) = S + S u + C v
+  auto turned = [&](F2 A, F2 Al, F2 B, F2 Bl, F2& h, F2& low) {
+    F2 a, ae, b, be, d, de, g, ge;
+    two_prod(A, u, a, ae);
+    two_prod(B, vh, b, be);
+    two_sum(a, b, d, de);
+    two_sum(A, d, g, ge);
+    low = add(add(ge, de), add(ae, be));
+    low = add(low, fma(A, ul, fma(B, sl, fma(Bl, vh, fma(Al, u, Al)))));
+    h = add(g, low);
+    low = sub(low, sub(h, g));
+  };
+  auto scaled = [&](F2 h, F2 l, F2& oh, F2& ol) {
+    F2 a, ae;
+    two_prod(h, same(mh), a, ae);
+    ae = add(ae, fma(h, same(ml), mul(l, same(mh))));
+    oh = add(a, ae);
+    ol = sub(ae, sub(oh, a));
+  };
   CosSin o;
-  float a, ae, b, be, d, de, h, he;
-  two_prod(t.x, u, a, ae);
-  two_prod(t.z, vh, b, be);
-  two_sum(a, -b, d, de);
-  two_sum(t.x, d, h, he);
-  float low = __fadd_rn(__fadd_rn(he, de), __fsub_rn(ae, be));
-  low = __fadd_rn(low, __fmaf_rn(t.x, ul, __fmaf_rn(-t.z, sl, __fmaf_rn(-t.w, vh, __fmaf_rn(t.y, u, t.y)))));
-  const float c = __fadd_rn(h, low), cl = __fsub_rn(low, __fsub_rn(c, h));
-  two_prod(t.z, u, a, ae);
-  two_prod(t.x, vh, b, be);
-  two_sum(a, b, d, de);
-  two_sum(t.z, d, h, he);
-  low = __fadd_rn(__fadd_rn(he, de), __fadd_rn(ae, be));
-  low = __fadd_rn(low, __fmaf_rn(t.z, ul, __fmaf_rn(t.x, sl, __fmaf_rn(t.y, vh, __fmaf_rn(t.w, u, t.w)))));
-  const float s = __fadd_rn(h, low), s_l = __fsub_rn(low, __fsub_rn(s, h));
-  two_prod(c, mh, a, ae);
-  ae = __fadd_rn(ae, __fmaf_rn(c, ml, __fmul_rn(cl, mh)));
-  o.ch = __fadd_rn(a, ae);
-  o.cl = __fsub_rn(ae, __fsub_rn(o.ch, a));
-  two_prod(s, mh, a, ae);
-  ae = __fadd_rn(ae, __fmaf_rn(s, ml, __fmul_rn(s_l, mh)));
-  o.sh = __fadd_rn(a, ae);
-  o.sl = __fsub_rn(ae, __fsub_rn(o.sh, a));
+  F2 h, l;
+  turned(C, Cl, neg(S), neg(Sl), h, l);
+  scaled(h, l, o.ch, o.cl);
+  turned(S, Sl, C, Cl, h, l);
+  scaled(h, l, o.sh, o.sl);
   return o;
 }
 
@@ -150,21 +204,20 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 
 // a c + b s = d + e, to 2^-40 of |a| + |b|, with c and s in 16 bits and the rest.
 // Of a and b of 8 bits the upper products are exact; of 16 bits (LONG) they are not.
-template <bool LONG>
-__device__ __forceinline__ void sum_of_products(float a, float c, float cl, float b, float s, float sl, float& d,
-                                                float& e) {
-  float low;
+template <bool LONG, class T>
+__device__ __forceinline__ void sum_of_products(T a, T c, T cl, T b, T s, T sl, T& d, T& e) {
+  T low;
   if (LONG) {
-    float p, pe, q, qe;
+    T p, pe, q, qe;
     two_prod(a, c, p, pe);
     two_prod(b, s, q, qe);
     two_sum(p, q, d, e);
-    low = __fmaf_rn(a, cl, __fmaf_rn(b, sl, __fadd_rn(pe, qe)));
+    low = fma(a, cl, fma(b, sl, add(pe, qe)));
   } else {
-    two_sum(__fmul_rn(a, c), __fmul_rn(b, s), d, e);
-    low = __fmaf_rn(a, cl, __fmul_rn(b, sl));
+    two_sum(mul(a, c), mul(b, s), d, e);
+    low = fma(a, cl, mul(b, sl));
   }
-  e = __fadd_rn(e, low);
+  e = add(e, low);
 }
 
 __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
@@ -237,11 +290,11 @@ __device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane,
   return true;
 }
 
-template <int D, int TARGET, bool NORM>
+template <int D, int TARGET, bool NORM, bool FULL>
 __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
-  constexpr int kAhead = kAheadOf<TARGET>;
+  constexpr int kAhead = ahead_of(TARGET, NORM);
   __shared__ float4 s_table[kSteps];
   __shared__ uint64_t s_turns[64];
   // a row's cosines and sines; of both, 16 bits and what these leave
@@ -272,10 +325,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
   const int H = a.Hq + (APPEND ? 2 : 1) * a.Hk;
   const int end = live ? min(first + a.part_heads, H) : 0;
   // chunks of 8 dims of this lane; in a 4-bit cache's rows two side by side, a block
-  const int nrot = a.rotary_dim / 16;
-  const bool pairs = a.interleaved != 0;
-  const int c0 = pairs ? j : j < nrot ? j : 2 * j;
-  const int c1 = pairs ? j + L : j < nrot ? j + nrot : 2 * j + 1;
+  const int nrot = FULL ? L : a.rotary_dim / 16;
+  const bool pairs = !FULL && a.interleaved != 0;
+  const int c0 = FULL || pairs || j < nrot ? j : 2 * j;
+  const int c1 = FULL || pairs ? j + L : j < nrot ? j + nrot : 2 * j + 1;
   const uint16_t* q_row = a.q.p + row * a.q.row;
   const uint16_t* k_row = a.k.p + row * a.k.row;
   const uint16_t* v_row = a.v.p + row * a.v.row;
@@ -309,39 +362,41 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
   }
   const int pos = a.positions ? given : place, slot = place % kP;
   float(&angle)[Q4 ? 6 : 2][64] = s_angle[warp];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int p = 32 * i + lane;
-    if (p < a.rotary_dim / 2) {
-      const CosSin x = cos_sin(s_turns[p] * (uint64_t)(int64_t)pos, s_table, a.magnitude, a.magnitude_low);
-      angle[0][p] = x.ch;
-      angle[1][p] = x.sh;
-      if (Q4) {
-        const float ch = __uint_as_float(__float_as_uint(x.ch) & 0xFFFFFF00u);
-        const float sh = __uint_as_float(__float_as_uint(x.sh) & 0xFFFFFF00u);
-        angle[Q4 ? 2 : 0][p] = ch;
-        angle[Q4 ? 3 : 0][p] = __fadd_rn(__fsub_rn(x.ch, ch), x.cl);
-        angle[Q4 ? 4 : 0][p] = sh;
-        angle[Q4 ? 5 : 0][p] = __fadd_rn(__fsub_rn(x.sh, sh), x.sl);
-      }
+  {
+    // pairs lane and lane + 32 (where there are so many)
+    const CosSin x = cos_sin(s_turns[lane] * (uint64_t)(int64_t)pos, s_turns[lane + 32] * (uint64_t)(int64_t)pos, s_table,
+                             a.magnitude, a.magnitude_low);
+    auto put = [&](int i, F2 y) { apart(y, angle[i][lane], angle[i][lane + 32]); };
+    put(0, x.ch);
+    put(1, x.sh);
+    if (Q4) {
+      const F2 ch{x.ch.v & 0xFFFFFF00FFFFFF00ull}, sh{x.sh.v & 0xFFFFFF00FFFFFF00ull};
+      put(Q4 ? 2 : 0, ch);
+      put(Q4 ? 3 : 0, add(sub(x.ch, ch), x.cl));
+      put(Q4 ? 4 : 0, sh);
+      put(Q4 ? 5 : 0, add(sub(x.sh, sh), x.sl));
     }
   }
   __syncwarp();
   // this lane's pairs: whether its two chunks turn, and by what
-  const bool t0 = pairs ? c0 < 2 * nrot : j < nrot, t1 = pairs ? c1 < 2 * nrot : j < nrot;
-  const int i0 = pairs ? 4 * c0 : 8 * j, i1 = pairs ? 4 * c1 : 8 * j + 4;
-  float c[8], s[8];
-  if (t0) {
-    load4(angle[0] + i0, c);
-    load4(angle[1] + i0, s);
-  }
-  if (t1) {
-    load4(angle[0] + i1, c + 4);
-    load4(angle[1] + i1, s + 4);
-  }
+  auto turns = [&](int chunk) { return FULL || (pairs ? chunk < 2 * nrot : j < nrot); };
+  auto sines_of = [&](int d0, int d1, float (&c)[8], float (&s)[8]) {
+    const int i0 = pairs ? 4 * d0 : 8 * j, i1 = pairs ? 4 * d1 : 8 * j + 4;
+    if (turns(d0)) {
+      load4(angle[0] + i0, c);
+      load4(angle[1] + i0, s);
+    }
+    if (turns(d1)) {
+      load4(angle[0] + i1, c + 4);
+      load4(angle[1] + i1, s + 4);
+    }
+  };
+  float lane_c[8], lane_s[8];  // of chunks c0 and c1
+  sines_of(c0, c1, lane_c, lane_s);
 
-  // q, and k that is not quantised: normalised, turned, rounded
-  auto rotate = [&](uint32_t (&v)[8], bool is_q) {
+  // normalised, turned by c and s, rounded: chunks d0 and d1
+  auto rotate = [&](uint32_t (&v)[8], bool is_q, int d0, int d1, const float (&c)[8], const float (&s)[8]) {
+    const bool t0 = turns(d0), t1 = turns(d1);
     float x[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -360,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
       float g[16];
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        load4(wt + 8 * c0 + i, g + i);
-        load4(wt + 8 * c1 + i, g + 8 + i);
+        load4(wt + 8 * d0 + i, g + i);
+        load4(wt + 8 * d1 + i, g + 8 + i);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = x[i] * k * g[i];
@@ -389,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
     }
   };
 
-  // k that is quantised, in two parts: a code changes by up to a third where a key
+  // The same of k that is quantised, in two parts: a code changes by up to a third where a key
   // falls on the other side of a border, so it is the definition that decides and not
   // the order of fp32 operations.  As above, to the nearest fp32 and then to bf16.
   auto rotate_exactly = [&](uint32_t (&v)[8], int d0, int d1) {
@@ -437,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
       two_prod(d, r, h, he);
       return __fadd_rn(h, __fadd_rn(he, __fmaf_rn(d, rl, __fmul_rn(e, r))));
     };
-    const bool z0 = pairs ? d0 < 2 * nrot : j < nrot, z1 = pairs ? d1 < 2 * nrot : j < nrot;
+    const bool z0 = turns(d0), z1 = turns(d1);
     const int e0 = pairs ? 4 * d0 : 8 * j, e1 = pairs ? 4 * d1 : 8 * j + 4;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -494,9 +549,18 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
     const bool is_q = h < 0, is_k = !is_q && (!APPEND || h < a.Hk);
     const bool side = side_by_side(head);
     const int d0 = side ? 2 * j : c0, d1 = side ? 2 * j + 1 : c1;
-    // past 2^100 products leave fp32's range, and their small parts are no numbers
-    if (Q4 && is_k && ((NORM && a.k_norm) || max_abs_bits(v) < 0x7180u)) rotate_exactly(v, d0, d1);
-    else if (is_q || is_k) rotate(v, is_q);
+    if (Q4 && is_k) {
+      // past 2^100 products leave fp32's range, and their small parts are no numbers
+      if ((NORM && a.k_norm) || max_abs_bits(v) < 0x7180u) {
+        rotate_exactly(v, d0, d1);
+      } else {
+        float c[8], s[8];
+        sines_of(d0, d1, c, s);
+        rotate(v, false, d0, d1, c, s);
+      }
+    } else if (is_q || is_k) {
+      rotate(v, is_q, c0, c1, lane_c, lane_s);
+    }
     if (is_q || !APPEND) {
       uint16_t* p = is_q ? q_out + head * a.q_out.head : a.k_out.p + row * a.k_out.row + h * a.k_out.head;
       st_16(p + 8 * c0, v);
@@ -514,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 2 * j + i;
-          const int from = t < nrot ? t : t < 2 * nrot ? t - nrot : t / 2;
-          const bool upper = t < 2 * nrot ? t >= nrot : (t & 1) != 0;
+          const int from = t < nrot ? t : FULL || t < 2 * nrot ? t - nrot : t / 2;
+          const bool upper = FULL || t < 2 * nrot ? t >= nrot : (t & 1) != 0;
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -558,7 +622,9 @@ cudaError_t launch(RopeArgs a, int sms, bool programmatic, cudaStream_t stream) 
   a.part_heads = (rounds + parts - 1) / parts * G;
   a.parts = (H + a.part_heads - 1) / a.part_heads;
   const int64_t tasks = (int64_t)a.n_rows * a.parts, grid = (tasks + kWarps - 1) / kWarps;
-  auto kern = a.q_norm || a.k_norm ? rope_kernel<D, TARGET, true> : rope_kernel<D, TARGET, false>;
+  const bool norm = a.q_norm || a.k_norm, full = a.rotary_dim == D && !a.interleaved;
+  auto kern = norm ? (full ? rope_kernel<D, TARGET, true, true> : rope_kernel<D, TARGET, true, false>)
+                   : (full ? rope_kernel<D, TARGET, false, true> : rope_kernel<D, TARGET, false, false>);
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, programmatic, a);
 }
 

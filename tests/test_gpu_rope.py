@@ -446,15 +446,16 @@ def test_append_in_place(daa, q4, how):
     assert torch.equal(pool.view(torch.uint8), want.view(torch.uint8))
 
 
+@pytest.mark.parametrize("inter,rot", [(False, 32), (True, 32), (False, 64), (True, 64), (False, 48), (True, 48)])
 @pytest.mark.parametrize("norm", [False, True])
-def test_keys_that_are_no_numbers_into_4_bits(daa, norm):
+def test_keys_that_are_no_numbers_into_4_bits(daa, norm, inter, rot):
     """As the cache stores them: NaN as zero, infinities as the largest values, rotated first; and keys of any size."""
     rng = np.random.default_rng(23)
     t, n = q4_support.make_table(rng, [3], [6])
-    tab, rope = _dev_table(t), daa.Rope(64, rotary_dim=32)
+    tab, rope = _dev_table(t), daa.Rope(64, rotary_dim=rot, interleaved=inter)
     q, k, v = _rows(rng, 6, 2, 1, 64, "flat")
-    k.view(torch.int16)[1, 0, 40] = 0x7F80  # not rotated
-    k.view(torch.int16)[2, 0, 3] = -0x80  # rotated: with its mate no number, or infinite
+    k.view(torch.int16)[1, 0, 40] = 0x7F80  # rotated or not
+    k.view(torch.int16)[2, 0, 3] = -0x80
     k.view(torch.int16)[3, 0, 50] = 0x7FC1
     k[4] *= 2.0 ** 101
     k[5] *= 2.0 ** -101

@@ -23,7 +23,21 @@
 // chunks each, chunks j and j + rotary_dim / 16 for the half layout, so that a lane
 // holds whole pairs and keeps its eight sines and cosines in registers.  Loads run
 // kAhead heads ahead of their use, the first ones ahead of the search.  Warps share
-// nothing but constants: no barrier behind the first.
+// nothing but constants: no barrier behind the first.  (With the sines of a CTA's rows
+// in shared memory and two barriers: 297 us for the first case below, 249 instructions a
+// warp of heads where this takes 126.  Two or four rows a warp: slower from 18
+// heads a row on, up to 10 % faster at 9, and twice the kernels.)
+//
+// Bound, and times on GB300 (graph replays; bytes at 6,785 GB/s, a copy's rate):
+//   32,832 rows of 80 heads of 128 dims appended   HBM: 200 us, 99 % of that rate
+//   16,416 rows of 72 heads rotated                HBM and the last wave: 96 us, 93 %
+//   36,760 rows of 48 heads into 4 bits            147 us, 77 %: instructions (55 % of the
+//       issue slots) and latency at 18 warps an SM.  Keys rotated as queries are would
+//       take 11 us less of it, and stray from the definition at one code in some 10^6.
+//   128 rows of 14 heads, 32 of 64                 2.8 and 1.6 us: a launch, and two or
+//       three dependent loads
+//   Few heads: rows of 9 (32,800 of them) 44 us, 56 %, of 14 50 us, 69 %: what a row costs
+//       before its heads (search, place, sines: about 450 instructions a warp).
 #include <algorithm>
 
 #include "launch.h"

@@ -251,6 +251,9 @@ APPENDS = [
     (64, 8, 128, 128, False, False, "fused", [8192, 77], [1500, 1]),
     (20, 4, 64, 64, False, True, "fused", [0, 901], [5003, 1]),
     (2, 1, 64, 32, False, False, "flat", [3 + i % 40 for i in range(2000)], [1 + i % 3 // 2 for i in range(2000)]),
+    (1, 1, 64, 16, False, False, "fused", [i % 50 for i in range(20000)], [(i * 7 % 5) // 3 for i in range(20000)]),
+    (3, 1, 64, 64, True, False, "fused", [i % 50 for i in range(257)], [1] * 257),
+    (16, 16, 64, 64, False, True, "fused", [0, 70], [0, 1300]),
 ]
 
 
@@ -575,6 +578,8 @@ def test_steps_over_a_growing_cache(daa, q4, norm):
         table = pool.step(slots, new)
         q, k, v = _rows(rng, sum(new), hq, hk, d, "fused")
         attn = (daa.BatchAttentionQ4 if q4 else daa.BatchAttention)(table, hq, pages)
+        if new[0] == 1:
+            attn.plan()
         lse = torch.empty(sum(new), hq, device=DEV)
         out = attn.step_rope(q, k, v, rope, lse=lse, **kw)
         # by the single calls: the same
@@ -713,6 +718,37 @@ def test_captured_and_replayed(daa, kind):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(pool.view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(out, want[1]) and torch.equal(ko, want[2])
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_steps_on_another_stream(daa, q4):
+    """step_rope on a stream that is still busy: what it makes in between (the rotated queries) is that stream's too."""
+    rng = np.random.default_rng(20)
+    hq, hk, d = 16, 4, 128
+    t, n = q4_support.make_table(rng, [300, 17, 900], [200, 1, 1])
+    table = daa.PageTable.from_host(*(t[x] for x in ("qo_indptr", "kv_indptr", "page_indices", "last_page_len")), DEV)
+    new_pool = (lambda: torch.zeros(n, hk, 2, 9 * d, dtype=torch.uint8, device=DEV)) if q4 else (lambda: torch.zeros(n, 2, hk, 16, d, dtype=torch.bfloat16, device=DEV))
+    q, k, v = _rows(rng, 202, hq, hk, d, "fused")
+    rope = daa.Rope(d)
+    attn = lambda p: (daa.BatchAttentionQ4 if q4 else daa.BatchAttention)(table, hq, p)  # noqa: E731
+    want = attn(new_pool()).step_rope(q, k, v, rope)
+    for raw in (False, True):
+        s = torch.cuda.Stream()
+        name = s.cuda_stream if raw else s
+        a = attn(new_pool())
+        late = torch.zeros_like(q._base)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(100_000_000)
+            late.copy_(q._base)
+        outs = []
+        for _ in range(3):
+            outs.append(a.step_rope(late[:, :hq], late[:, hq:hq + hk], late[:, hq + hk:], rope, stream=name))
+            junk = [torch.full_like(q, 9.0) for _ in range(4)]  # on this stream: not in the call's memory
+            del junk
+        s.synchronize()
+        for o in outs:
+            assert torch.equal(o, want)
 
 
 @pytest.mark.parametrize("raw", [False, True])

@@ -26,7 +26,7 @@
 // nothing but constants: no barrier behind the first.  (With the sines of a CTA's rows
 // in shared memory and two barriers: 297 us for the first case below, 249 instructions a
 // warp of heads where this takes 126.  Two or four rows a warp: slower from 18
-// heads a row on, up to 10 % faster at 9, and twice the kernels.)
+// heads a row on, and no faster than LEAN below it.)
 //
 // Bound, and times on GB300 (graph replays; bytes at 6,785 GB/s, a copy's rate):
 //   32,832 rows of 80 heads of 128 dims appended   HBM: 200 us, 99 % of that rate
@@ -36,7 +36,7 @@
 //       take 11 us less of it, and stray from the definition at one code in some 10^6.
 //   128 rows of 14 heads, 32 of 64                 2.8 and 1.6 us: a launch, and two or
 //       three dependent loads
-//   Few heads: rows of 9 (32,800 of them) 44 us, 56 %, of 14 50 us, 69 %: what a row costs
+//   32,800 rows of 10 heads appended 38 us, 66 %, of 14 44 us, 79 %: what a row costs
 //       before its heads (search, place, sines: about 450 instructions a warp).
 #include <algorithm>
 
@@ -52,15 +52,20 @@ constexpr int kP = 16;
 // Heads of a lane in flight, and CTAs of an SM that registers are left for.  Rows are
 // bound by HBM and want warps: 16,416 rows of 72 heads 96 us with two and 7 CTAs, 104
 // with 6, 98 with 8 (spills).  Pages want loads in flight: 32,832 rows of 80 heads 200
-// us with five heads and 4 CTAs, 202 with four.  The 4-bit append is bound by
-// instructions and latency: 36,760 rows of 48 heads 147 us with three and 5 CTAs, 155
-// with two, 158 with 4 CTAs; with norms (96 registers do not hold it) 4 CTAs.
-constexpr int ahead_of(int target, bool norm) {
-  return target == kRopeRows ? 2 : target == kRopePages ? 5 : norm ? 2 : 3;
+// us with five heads and 4 CTAs, 205 with two and 7; a chunk beside decodes 3.9 and 4.8.
+// But where rows are many and of few heads, what comes before a row's heads is most of
+// it, and more warps do that at a time (LEAN: two heads and 7 CTAs): 32,800 rows of 14
+// heads 44 us and not 53, of 10 38 and 47, of 20 56 and 60, of 32 no difference.  The
+// 4-bit append is bound by instructions and latency: 36,760 rows of 48 heads 147 us with
+// three heads and 5 CTAs, 155 with two, 158 with 4 CTAs; with norms (96 registers do not
+// hold it) 4 CTAs.
+constexpr int ahead_of(int target, bool norm, bool lean) {
+  return target == kRopeRows || lean ? 2 : target == kRopePages ? 5 : norm ? 2 : 3;
 }
-constexpr int ctas_of(int target, bool norm) {
-  return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? 4 : (norm ? 4 : 5);
+constexpr int ctas_of(int target, bool norm, bool lean) {
+  return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? (lean ? 7 : 4) : (norm ? 4 : 5);
 }
+constexpr int kLeanRounds = 6;  // of a warp's heads at a time, a row
 
 // ------------------------------------------------------------------- angles
 // Sine and cosine of n / 256 turns, each as the sum of two fp32 numbers.
@@ -304,11 +309,11 @@ __device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane,
   return true;
 }
 
-template <int D, int TARGET, bool NORM, bool FULL>
-__global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, int TARGET, bool NORM, bool FULL, bool LEAN>
+__global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LEAN)) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
-  constexpr int kAhead = ahead_of(TARGET, NORM);
+  constexpr int kAhead = ahead_of(TARGET, NORM, LEAN);
   __shared__ float4 s_table[kSteps];
   __shared__ uint64_t s_turns[64];
   // a row's cosines and sines; of both, 16 bits and what these leave
@@ -625,20 +630,26 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM)) rope_kernel(c
   }
 }
 
+template <int D, int TARGET, bool LEAN>
+auto kernel_of(bool norm, bool full) {
+  return norm ? (full ? rope_kernel<D, TARGET, true, true, LEAN> : rope_kernel<D, TARGET, true, false, LEAN>)
+              : (full ? rope_kernel<D, TARGET, false, true, LEAN> : rope_kernel<D, TARGET, false, false, LEAN>);
+}
+
 template <int D, int TARGET>
 cudaError_t launch(RopeArgs a, int sms, bool programmatic, cudaStream_t stream) {
   constexpr int G = 32 / (D / 16);
   const int H = a.Hq + (TARGET != kRopeRows ? 2 : 1) * a.Hk;
   const int rounds = (H + G - 1) / G;
+  const bool norm = a.q_norm || a.k_norm, full = a.rotary_dim == D && !a.interleaved;
   // few rows: their heads over more warps, as many as the GPU starts at once
-  const int64_t want = (int64_t)sms * 16;
-  int parts = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, want / a.n_rows));
+  const int64_t want = (int64_t)sms * kWarps * ctas_of(TARGET, norm, false);
+  const int parts = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, want / a.n_rows));
   a.part_heads = (rounds + parts - 1) / parts * G;
   a.parts = (H + a.part_heads - 1) / a.part_heads;
   const int64_t tasks = (int64_t)a.n_rows * a.parts, grid = (tasks + kWarps - 1) / kWarps;
-  const bool norm = a.q_norm || a.k_norm, full = a.rotary_dim == D && !a.interleaved;
-  auto kern = norm ? (full ? rope_kernel<D, TARGET, true, true> : rope_kernel<D, TARGET, true, false>)
-                   : (full ? rope_kernel<D, TARGET, false, true> : rope_kernel<D, TARGET, false, false>);
+  const bool lean = TARGET == kRopePages && parts == 1 && rounds <= kLeanRounds;
+  auto kern = lean ? kernel_of<D, TARGET, TARGET == kRopePages>(norm, full) : kernel_of<D, TARGET, false>(norm, full);
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, programmatic, a);
 }
 

@@ -254,6 +254,9 @@ APPENDS = [
     (1, 1, 64, 16, False, False, "fused", [i % 50 for i in range(20000)], [(i * 7 % 5) // 3 for i in range(20000)]),
     (3, 1, 64, 64, True, False, "fused", [i % 50 for i in range(257)], [1] * 257),
     (16, 16, 64, 64, False, True, "fused", [0, 70], [0, 1300]),
+    # many rows of few heads
+    (12, 1, 128, 128, False, False, "fused", [900, 3], [2501, 1]), (8, 1, 128, 128, False, True, "flat", [0, 30], [2000, 700]),
+    (3, 1, 128, 48, False, True, "fused", [17], [2600]), (6, 2, 64, 48, True, False, "heads", [5, 1], [2700, 3]),
 ]
 
 

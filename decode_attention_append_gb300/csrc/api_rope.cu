@@ -46,8 +46,9 @@ daa_status check_rope(const daa_rope* r) {
 // Elements from the first to one past the last, or -1 for strides that no tensor has.
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 int64_t span_of(const daa_rows& x, int64_t rows, int64_t heads, int64_t d) {
-  if (x.row_stride < 0 || x.head_stride < 0 || x.row_stride > kMaxStride || x.head_stride > kMaxStride) return -1;
-  const __int128 n = (__int128)(rows - 1) * x.row_stride + (__int128)(heads - 1) * x.head_stride + d;
+  const int64_t rs = rows > 1 ? x.row_stride : 0, hs = heads > 1 ? x.head_stride : 0;
+  if (rs < 0 || hs < 0 || rs > kMaxStride || hs > kMaxStride) return -1;
+  const __int128 n = (__int128)(rows - 1) * rs + (__int128)(heads - 1) * hs + d;
   return n > ((__int128)1 << 60) ? -1 : (int64_t)n;
 }
 
@@ -141,6 +142,13 @@ daa_status common_args(const daa_rope* rope, const daa_rope_rows* io, int64_t q_
       if (its_own && same_rows(*out[o].x, *in[i].x, n, in[i].heads)) continue;
       if (may_meet(*out[o].x, out[o].heads, *in[i].x, in[i].heads, n, d)) return DAA_ERR_INVALID_ARG;
     }
+  }
+  for (int o = 0; o < n_out; ++o) {
+    auto covers = [&](const void* p, int64_t bytes) {
+      return p && ranges_meet(out[o].x->data, 2 * span_of(*out[o].x, n, out[o].heads, d), p, bytes);
+    };
+    if (covers(io->positions, 4 * n) || covers(io->q_norm, 2 * d) || covers(io->k_norm, 2 * d))
+      return DAA_ERR_INVALID_ARG;
   }
   if (n_out == 2 && may_meet(*out[0].x, out[0].heads, *out[1].x, out[1].heads, n, d)) return DAA_ERR_INVALID_ARG;
   std::memcpy(a.turns, rope->turns, sizeof(a.turns));

@@ -154,6 +154,11 @@ def _append(daa, q4=False, batch=0, rope=None, pool=0x70000000, table=A, dims=(4
     (dict(q_out=(A + 256, 512, 64)), INVALID), (dict(q=(0x50000, 512, 64), q_out=(A, 512, 64)), SHAPE), (dict(q=(0x50000, 512, 64), q_out=(A + 128, 512, 64)), INVALID),
     (dict(q=(0x50000, 512, 64), k=(0x50000 + 512, 512, 64), v=(0x50000 + 768, 512, 64), q_out=(0x50000 + 1024 * 8, 512, 64)), SHAPE),
     (dict(q=(0x50000, 512, 64), k=(0x50000 + 512, 512, 64), v=(0x50000 + 768, 512, 64), q_out=(0x50000 + 1024 * 7, 512, 64)), INVALID),
+    # strides of one row or head are not looked at
+    (dict(rows=1, k=(A + 512, -8, 64)), SHAPE), (dict(rows=1, dims=(2, 1, 64, 16, 64), k=(A + 512, 1 << 50, -3)), SHAPE), (dict(rows=2, dims=(2, 1, 64, 16, 64), k=(A + 512, 512, 1)), SHAPE),
+    # positions and weights under an output
+    (dict(pos=0x900000 + 4092), INVALID), (dict(pos=0x900000 + 4096), SHAPE), (dict(pos=0x900000 - 28), INVALID), (dict(pos=0x900000 - 32), SHAPE),
+    (dict(qn=0x900000), INVALID), (dict(kn=0x900000 - 126), INVALID), (dict(kn=0x900000 - 128), SHAPE),
     # heads of q, k and v between one another: [rows][heads][q, k, v][64]
     (dict(q=(A, 768, 192), k=(A + 128, 768, 192), v=(A + 256, 768, 192), q_out=(A, 768, 192)), SHAPE),
     (dict(q=(A, 768, 192), k=(A + 128, 768, 192), v=(A + 192, 768, 192), q_out=(A + 128, 768, 192)), INVALID),

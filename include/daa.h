@@ -676,7 +676,8 @@ daa_status daa_batch_attention_q4_run(const void* q, const void* kv_pages, const
  * multiplied by the weights, all of its dims.  Computed in fp32, rounded once to
  * bf16; the angle is good to 2^-33 of a turn at every position from -2^31 to
  * 2^31 - 1.  Dims that are neither normalised nor rotated keep their bits.  (The
- * squares are summed in fp32: heads of values past about 10^18 have no norm.)
+ * squares are summed in fp32: heads of values past about 10^18 have no norm, nor, with
+ * eps 0, those of values under 10^-19.)
  * Rotating by negated positions is the transposed rotation: it takes gradients of
  * the outputs to gradients of the inputs, and for m = 1 outputs back to inputs.
  *

@@ -23,7 +23,9 @@
 // chunks each, chunks j and j + rotary_dim / 16 for the half layout, so that a lane
 // holds whole pairs and keeps its eight sines and cosines in registers.  Loads run
 // kAhead heads ahead of their use, the first ones ahead of the search.  Warps share
-// nothing but constants: no barrier behind the first.  (With the sines of a CTA's rows
+// nothing but constants: no barrier behind the first.  Each layout has kernels of its
+// own (keys into 4 bits with one for all: 153 us where interleaved heads take 119 and
+// parts of heads 116).  (With the sines of a CTA's rows
 // in shared memory and two barriers: 297 us for the first case below, 249 instructions a
 // warp of heads where this takes 126.  Two or four rows a warp: slower from 18
 // heads a row on, and no faster than LEAN below it.)
@@ -48,6 +50,7 @@ namespace daa {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
+enum Layout { kPart, kWhole, kInterleaved };  // pairs of halves of a part or all of the head; neighbours
 constexpr int kP = 16;
 // Heads of a lane in flight, and CTAs of an SM that registers are left for.  Rows are
 // bound by HBM and want warps: 16,416 rows of 72 heads 96 us with two and 7 CTAs, 104
@@ -57,13 +60,15 @@ constexpr int kP = 16;
 // it, and more warps do that at a time (LEAN: two heads and 7 CTAs): 32,800 rows of 14
 // heads 44 us and not 53, of 10 38 and 47, of 20 56 and 60, of 32 no difference.  The
 // 4-bit append is bound by instructions and latency: 36,760 rows of 48 heads 147 us with
-// three heads and 5 CTAs, 155 with two, 158 with 4 CTAs; with norms (96 registers do not
-// hold it) 4 CTAs.
+// three heads and 5 CTAs, 155 with two, 159 with 4 CTAs.  With norms 96 registers hold it
+// for whole heads only (16,416 rows of 48: 100 us, 105 with 4 CTAs; interleaved 113, 108).
 constexpr int ahead_of(int target, bool norm, bool lean) {
   return target == kRopeRows || lean ? 2 : target == kRopePages ? 5 : norm ? 2 : 3;
 }
-constexpr int ctas_of(int target, bool norm, bool lean) {
-  return target == kRopeRows ? (norm ? 5 : 7) : target == kRopePages ? (lean ? 7 : 4) : (norm ? 4 : 5);
+constexpr int ctas_of(int target, bool norm, int layout, bool lean) {
+  return target == kRopeRows    ? (norm ? 5 : 7)
+         : target == kRopePages ? (lean ? 7 : 4)
+                                : (norm && layout != kWhole ? 4 : 5);
 }
 constexpr int kLeanRounds = 6;  // of a warp's heads at a time, a row
 
@@ -309,10 +314,11 @@ __device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane,
   return true;
 }
 
-template <int D, int TARGET, bool NORM, bool FULL, bool LEAN>
-__global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LEAN)) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <int D, int TARGET, bool NORM, int LAYOUT, bool LEAN>
+__global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN)) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
+  constexpr bool FULL = LAYOUT == kWhole, pairs = LAYOUT == kInterleaved;
   constexpr int kAhead = ahead_of(TARGET, NORM, LEAN);
   __shared__ float4 s_table[kSteps];
   __shared__ uint64_t s_turns[64];
@@ -345,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LEAN)) rope_ke
   const int end = live ? min(first + a.part_heads, H) : 0;
   // chunks of 8 dims of this lane; in a 4-bit cache's rows two side by side, a block
   const int nrot = FULL ? L : a.rotary_dim / 16;
-  const bool pairs = !FULL && a.interleaved != 0;
   const int c0 = FULL || pairs || j < nrot ? j : 2 * j;
   const int c1 = FULL || pairs ? j + L : j < nrot ? j + nrot : 2 * j + 1;
   const uint16_t* q_row = a.q.p + row * a.q.row;
@@ -630,10 +635,15 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LEAN)) rope_ke
   }
 }
 
+template <int D, int TARGET, bool LEAN, bool NORM>
+auto kernel_of(int layout) {
+  return layout == kWhole         ? rope_kernel<D, TARGET, NORM, kWhole, LEAN>
+         : layout == kInterleaved ? rope_kernel<D, TARGET, NORM, kInterleaved, LEAN>
+                                  : rope_kernel<D, TARGET, NORM, kPart, LEAN>;
+}
 template <int D, int TARGET, bool LEAN>
-auto kernel_of(bool norm, bool full) {
-  return norm ? (full ? rope_kernel<D, TARGET, true, true, LEAN> : rope_kernel<D, TARGET, true, false, LEAN>)
-              : (full ? rope_kernel<D, TARGET, false, true, LEAN> : rope_kernel<D, TARGET, false, false, LEAN>);
+auto kernel_of(bool norm, int layout) {
+  return norm ? kernel_of<D, TARGET, LEAN, true>(layout) : kernel_of<D, TARGET, LEAN, false>(layout);
 }
 
 template <int D, int TARGET>
@@ -641,15 +651,16 @@ cudaError_t launch(RopeArgs a, int sms, bool programmatic, cudaStream_t stream) 
   constexpr int G = 32 / (D / 16);
   const int H = a.Hq + (TARGET != kRopeRows ? 2 : 1) * a.Hk;
   const int rounds = (H + G - 1) / G;
-  const bool norm = a.q_norm || a.k_norm, full = a.rotary_dim == D && !a.interleaved;
+  const bool norm = a.q_norm || a.k_norm;
+  const int layout = a.interleaved ? kInterleaved : a.rotary_dim == D ? kWhole : kPart;
   // few rows: their heads over more warps, as many as the GPU starts at once
-  const int64_t want = (int64_t)sms * kWarps * ctas_of(TARGET, norm, false);
+  const int64_t want = (int64_t)sms * kWarps * ctas_of(TARGET, norm, layout, false);
   const int parts = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, want / a.n_rows));
   a.part_heads = (rounds + parts - 1) / parts * G;
   a.parts = (H + a.part_heads - 1) / a.part_heads;
   const int64_t tasks = (int64_t)a.n_rows * a.parts, grid = (tasks + kWarps - 1) / kWarps;
   const bool lean = TARGET == kRopePages && parts == 1 && rounds <= kLeanRounds;
-  auto kern = lean ? kernel_of<D, TARGET, TARGET == kRopePages>(norm, full) : kernel_of<D, TARGET, false>(norm, full);
+  auto kern = lean ? kernel_of<D, TARGET, TARGET == kRopePages>(norm, layout) : kernel_of<D, TARGET, false>(norm, layout);
   return launch_kernel(kern, dim3((unsigned)grid), dim3(kThreads), 0, stream, programmatic, a);
 }
 

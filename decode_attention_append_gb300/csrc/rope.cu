@@ -43,6 +43,7 @@
 #include <algorithm>
 
 #include "launch.h"
+#include "place.h"
 #include "ptx.cuh"
 #include "q4.cuh"
 
@@ -299,18 +300,14 @@ __device__ __forceinline__ bool find_place(const RopeArgs& a, int row, int lane,
                                  : a.kv_indptr + a.batch;
   const int word = lane < 7 ? ld_word(p) : 0;
   const int a0 = __shfl_sync(0xffffffffu, word, 0), a1 = __shfl_sync(0xffffffffu, word, 1);
-  const int p0 = __shfl_sync(0xffffffffu, word, 2), np = __shfl_sync(0xffffffffu, word, 3) - p0;
-  const int last_len = __shfl_sync(0xffffffffu, word, 4);
-  if (row >= __shfl_sync(0xffffffffu, word, 5)) return false;  // padding behind the last request
-  const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * kP + last_len : 0;
-  const int64_t pages_end = __shfl_sync(0xffffffffu, word, 6);
-  if (row < a0 || row >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || p0 < 0 || (int64_t)p0 + np > pages_end ||
-      last_len < 1 || last_len > kP) {
+  const int p0 = __shfl_sync(0xffffffffu, word, 2), p1 = __shfl_sync(0xffffffffu, word, 3);
+  const int last_len = __shfl_sync(0xffffffffu, word, 4), rows_end = __shfl_sync(0xffffffffu, word, 5);
+  const int pages_end = __shfl_sync(0xffffffffu, word, 6);
+  if (row >= rows_end) return false;  // padding behind the last request
+  if (!row_place(row, a0, a1, p0, p1, pages_end, last_len, pos, page_at)) {
     set_device_error(a.err, kDevErrShape);
     return false;
   }
-  pos = (int)kv_len - (a1 - a0) + (row - a0);
-  page_at = p0 + pos / kP;
   return true;
 }
 

@@ -755,7 +755,8 @@ typedef struct {
  * head_dim than dims; DAA_ERR_UNSUPPORTED for more than DAA_ROPE_MAX_HEADS heads of
  * all rows or requests, and shapes as daa_kv_append; DAA_ERR_SHAPE for rows without requests (batch 0);
  * DAA_ERR_ALIGNMENT; DAA_ERR_CUDA.  Lengths and page ids are checked on the device:
- * nothing is written for a row of a request with inconsistent lengths (error word 3);
+ * nothing is written for a row of a request with inconsistent lengths (starts below
+ * zero, ends before starts or behind the last request's page, error word 3);
  * of a row whose page id is outside the pool only q_out is (error word 1).
  */
 daa_status daa_apply_rope(const daa_rope* rope, const daa_rope_rows* rows, int32_t num_q_heads, int32_t num_k_heads,

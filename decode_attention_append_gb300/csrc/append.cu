@@ -20,6 +20,7 @@
 // them (fuse_min_qo > 0), and its grid covers only the span of rows
 // [row_begin, row_begin + n_rows) that holds the others.
 #include "launch.h"
+#include "place.h"
 #include "ptx.cuh"
 
 namespace daa {
@@ -68,17 +69,16 @@ kv_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_ne
     }
     const int r = lo;
     const int a0 = __ldg(append_indptr + r), a1 = __ldg(append_indptr + r + 1);
-    const int p0 = __ldg(kv_indptr + r), np = __ldg(kv_indptr + r + 1) - p0;
-    const int last_len = np > 0 ? __ldg(last_page_len + r) : 0;
-    const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * P + last_len : 0;
-    const int n_new = a1 - a0;
+    const int p0 = __ldg(kv_indptr + r), p1 = __ldg(kv_indptr + r + 1), pages_end = __ldg(kv_indptr + batch);
+    const int last_len = __ldg(last_page_len + r);
     int64_t dst = -1;
-    if (row < a0 || row >= a1 || n_new > kv_len || (np > 0 && (last_len < 1 || last_len > P))) {
+    int pos, page_at;
+    if (!row_place(row, a0, a1, p0, p1, pages_end, last_len, pos, page_at)) {
       set_device_error(err, kDevErrShape);
     } else {
-      const int64_t pos = kv_len - n_new + (row - a0);
-      const int64_t page = __ldg(page_indices + p0 + pos / P);
-      if (fuse_min_qo > 0 && n_new >= fuse_min_qo && pos >= fused_from((int)kv_len, n_new)) {
+      const int n_new = a1 - a0, kv_len = (p1 - p0 - 1) * P + last_len;
+      const int64_t page = __ldg(page_indices + page_at);
+      if (fuse_min_qo > 0 && n_new >= fuse_min_qo && pos >= fused_from(kv_len, n_new)) {
         // written by the prefill kernel of this fused call, from the same rows
       } else if (page < 0 || page >= num_pages) {
         set_device_error(err, kDevErrPageRange);

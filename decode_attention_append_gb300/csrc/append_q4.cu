@@ -19,6 +19,7 @@
 // heads of 128 dims in 106.8 us (with a thread's 16 dims stored side by side, half a
 // sector at a time: 110.7 at best).
 #include "launch.h"
+#include "place.h"
 #include "ptx.cuh"
 #include "q4.cuh"
 
@@ -118,17 +119,13 @@ kv_append_q4_kernel(const uint4* k_new, const uint4* v_new,
       if (indptr[mid] <= row) lo = mid; else hi = mid - 1;
     }
     const int a0 = indptr[lo], a1 = indptr[lo + 1];
-    const int p0 = kv_begin[lo], np = kv_begin[lo + 1] - p0;
-    const int last_len = np > 0 ? last_lens[lo] : 0;
-    const int64_t kv_len = np > 0 ? (int64_t)(np - 1) * P + last_len : 0;
     int64_t at = -1;
-    int slot = 0;
-    if (row < a0 || row >= a1 || a1 - a0 > kv_len || (np > 0 && (last_len < 1 || last_len > P))) {
+    int slot = 0, pos, page_at;
+    if (!row_place(row, a0, a1, kv_begin[lo], kv_begin[lo + 1], kv_begin[batch], last_lens[lo], pos, page_at)) {
       set_device_error(err, kDevErrShape);
     } else {
-      const int64_t pos = kv_len - (a1 - a0) + (row - a0);
-      const int64_t page = ld_word(page_indices + p0 + pos / P);
-      slot = (int)(pos % P);
+      const int64_t page = ld_word(page_indices + page_at);
+      slot = pos % P;
       if (page < 0 || page >= num_pages) set_device_error(err, kDevErrPageRange);
       else at = page * Hkv;
     }

@@ -10,17 +10,18 @@ namespace daa {
 
 // New row `row` of the request with rows [a0, a1) and pages [p0, p1) of the first
 // pages_end ids, the last page holding last_len tokens: its position and the index of
-// its page id; false where the words do not fit together.  Differences in 64 bits: of
-// words that are no table they leave 32.
+// its page id; false where the words do not fit together.  Differences are of words
+// from zero up, and of at most 2^27 pages, so that nothing leaves 32 bits.
 __host__ __device__ inline bool row_place(int32_t row, int32_t a0, int32_t a1, int32_t p0, int32_t p1,
                                           int32_t pages_end, int32_t last_len, int32_t& pos, int32_t& page_at) {
-  constexpr int P = 16;
-  const int64_t n_new = (int64_t)a1 - a0, kv_len = ((int64_t)p1 - p0 - 1) * P + last_len;
-  if (a0 < 0 || row < a0 || row >= a1 || p0 < 0 || p1 <= p0 || p1 > pages_end || last_len < 1 || last_len > P ||
-      n_new > kv_len || kv_len > INT_MAX)
+  constexpr uint32_t P = 16;
+  const uint32_t n_new = (uint32_t)a1 - (uint32_t)a0, np = (uint32_t)p1 - (uint32_t)p0;
+  const uint32_t kv_len = (np - 1) * P + (uint32_t)last_len;
+  if (a0 < 0 || row < a0 || row >= a1 || p0 < 0 || p1 <= p0 || p1 > pages_end || np > (1u << 27) || last_len < 1 ||
+      last_len > (int32_t)P || kv_len > (uint32_t)INT_MAX || n_new > kv_len)
     return false;
-  pos = (int32_t)(kv_len - n_new + (row - a0));
-  page_at = p0 + pos / P;
+  pos = (int32_t)(kv_len - n_new + (uint32_t)(row - a0));
+  page_at = p0 + (int32_t)((uint32_t)pos / P);
   return true;
 }
 

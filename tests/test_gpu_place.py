@@ -53,7 +53,7 @@ BAD = [
 
 
 @pytest.mark.parametrize("bad", BAD, ids=str)
-@pytest.mark.parametrize("kind", ["rope", "rope_q4"])
+@pytest.mark.parametrize("kind", ["plain", "q4", "rope", "rope_q4"])
 def test_one_request(daa, kind, bad):
     t = {"qo": [0, 3], "kv": [0, 1], "last": [16], **bad}
     pool = _pool(kind)
@@ -63,17 +63,18 @@ def test_one_request(daa, kind, bad):
 
 
 @pytest.mark.parametrize("qo,never", [([0, 5, 2, 8], [3]), ([0, 2, BIG, 8], [3]), ([0, 2, -7, 8], [3, 6]), ([-3, 2, 5, 8], [1])])
-@pytest.mark.parametrize("kind", ["rope", "rope_q4"])
+@pytest.mark.parametrize("kind", ["plain", "q4", "rope", "rope_q4"])
 def test_starts_that_fall_or_run_ahead(daa, kind, qo, never):
-    """8 rows, 3 requests of one page each: rows go to their request's page or nowhere."""
+    """8 rows, 3 requests of one page each: rows go to their request's page or nowhere.  Where starts fall, rows 2 to 4 are
+    those of two requests, and it is open which of them a search finds; else there are rows of none that fits."""
     pool = _pool(kind)
     _append(daa, kind, 8, pool, qo, [1, 3, 6], [0, 1, 2, 3], [16, 16, 16])
-    assert daa.device_error(reset=True) == 3
+    assert daa.device_error(reset=True) in ((0, 3) if qo == [0, 5, 2, 8] else (3,))
     used = {int(p) for p in pool.flatten(1).any(1).nonzero().flatten()}
     assert used <= {1, 3, 6} - set(never)
 
 
-@pytest.mark.parametrize("kind", ["rope", "rope_q4"])
+@pytest.mark.parametrize("kind", ["plain", "q4", "rope", "rope_q4"])
 def test_the_others_are_as_ever(daa, kind):
     """A request whose words do not fit between two that do."""
     rng = np.random.default_rng(1)

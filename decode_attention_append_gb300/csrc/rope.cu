@@ -496,6 +496,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN))
       float rr, re;
       two_prod(r, r, rr, re);
       const float t = __fsub_rn(__fmaf_rn(-ss, rr, 1.f), __fmaf_rn(ss, re, __fmul_rn(sl, rr)));
+      // r's power of two goes to the values ahead of the weights: their products stay near the
+      // outputs' size, whatever the head's and the weights' are
+      const float two = __uint_as_float(__float_as_uint(r) & 0x7F800000u);
+      r = __uint_as_float((__float_as_uint(r) & 0x007FFFFFu) | 0x3F800000u);
       rl = isfinite(t) ? 0.5f * r * t : 0.f;
       const float* wt = s_w[NORM];
       float g[16];
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN))
         load4(wt + 8 * d1 + i, g + 8 + i);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], g[i]);  // 16 bits: exact
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], two), g[i]);  // 16 bits: exact
     }
     auto scaled = [&](float d, float e) {  // (d + e) (r + rl)
       if (!NORM || !norm) return __fadd_rn(d, e);

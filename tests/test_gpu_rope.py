@@ -477,6 +477,36 @@ def test_keys_that_are_no_numbers_into_4_bits(daa, norm, inter, rot):
     assert torch.equal(pool, want)
 
 
+@pytest.mark.parametrize("inter,rot", [(False, 64), (True, 64), (False, 32), (True, 32)])
+@pytest.mark.parametrize("eps", [1e-6, 0.0])
+@pytest.mark.parametrize("weights", [None, 1.0, 2.0 ** 100, 2.0 ** -30])
+def test_normed_keys_of_any_size_into_4_bits(daa, weights, eps, inter, rot):
+    """Keys that are normalised on their way: heads with a NaN or an infinity, of zeros, of large and small values and of both,
+    under ordinary, large and small weights, against the definition in 64 bits (values: a zero's sign is open)."""
+    rng = np.random.default_rng(25)
+    t, n = q4_support.make_table(rng, [3], [9])
+    tab, rope = _dev_table(t), daa.Rope(64, rotary_dim=rot, interleaved=inter)
+    q, k, v = _rows(rng, 9, 2, 1, 64, "flat")
+    k.view(torch.int16)[1, 0, 40] = 0x7F80  # rotated or not
+    k.view(torch.int16)[2, 0, 3] = -0x80
+    k.view(torch.int16)[3, 0, 50] = 0x7FC1
+    k[4] = 0
+    k[5] *= 2.0 ** 50
+    k[6] *= 2.0 ** -60
+    k[7, 0, :32] *= 2.0 ** -40
+    w = torch.ones(64, dtype=torch.bfloat16, device=DEV) if weights is None else _bf16(rng, (64,), weights)
+    place = ref.places(t)
+    with np.errstate(invalid="ignore", divide="ignore"):
+        k_want = _exact_keys(k, place[:, 3], rope, w, float(np.float32(eps)))
+    pool, want = daa.new_q4_pool(n, 1, 64), daa.new_q4_pool(n, 1, 64)
+    daa.append_rope_q4(q, k, v, pool, *tab, rope, k_norm=w, eps=eps)
+    daa.kv_append_q4(k_want, v, want, *tab)
+    ids = _dev(np.arange(n, dtype=np.int32))
+    got, want = daa.kv_dequant_q4(pool, ids), daa.kv_dequant_q4(want, ids)
+    for row, page, slot, _ in place.tolist():
+        assert torch.equal(got[page, :, :, slot], want[page, :, :, slot]), row
+
+
 @pytest.mark.parametrize("q4", [False, True])
 def test_pages_and_rows_past_32_bits(daa, q4):
     """The last page of a pool of more than 2^32 bytes and values, and rows more than 2^31 elements apart."""

@@ -19,18 +19,17 @@ cudaError_t traced(int32_t id, cudaStream_t s, F&& f) {
 
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 
-// 2^64 times the turns a token of a pair that turns by f radians, modulo 2^64.
-// 1 / 2 pi in two parts, so that the product is good to 2^-100 of f.
+// 2^64 times the turns a token of a pair that turns by f radians, modulo 2^64, rounded
+// once.  1 / 2 pi in two parts, so that the product is good to 2^-100 of f.
 uint64_t turns_of(double f) {
   constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   const double p = f * hi, rest = std::fma(f, hi, -p) + f * lo;
-  auto wrapped = [](double x) {  // exact: below one turn either way, then half a turn
-    double t = std::ldexp(x - std::trunc(x), 64);
-    if (t >= 0x1p63) t -= 0x1p64;
-    if (t < -0x1p63) t += 0x1p64;
-    return (uint64_t)std::llrint(t);
-  };
-  return wrapped(p) + wrapped(rest);
+  // exact: below one turn either way, then half a turn, then whole units and less than one
+  double t = std::ldexp(p - std::trunc(p), 64);
+  if (t >= 0x1p63) t -= 0x1p64;
+  if (t < -0x1p63) t += 0x1p64;
+  const double whole = std::trunc(t);
+  return (uint64_t)(int64_t)whole + (uint64_t)std::llrint((t - whole) + std::ldexp(rest, 64));
 }
 
 daa_status check_rope(const daa_rope* r) {

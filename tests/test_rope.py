@@ -70,6 +70,18 @@ def test_turns_are_exact(daa):
         assert min(off, 2 ** 64 - off) <= 1, (x, got, want)
 
 
+def test_angles_of_far_positions(daa):
+    """p times a pair's turns, modulo one, is off by p 2^-65 turns at most: 2^-41 of a turn at 2^24, 2^-34 at the last position."""
+    f = ref.frequencies(128, 500000.0)
+    r = daa.Rope(128, frequencies=f)
+    for p in (1, 131_071, 2 ** 24, -2 ** 24, 2 ** 31 - 1, -2 ** 31):
+        for x, turns in zip(f, r._rope.turns):
+            n, d = float(x).as_integer_ratio()
+            want = p * n * 10 ** 60 * 2 ** 79 // (d * ref._PI)  # p x / 2 pi in units of 2^-80
+            off = ((p * turns << 16) - want) % 2 ** 80
+            assert min(off, 2 ** 80 - off) <= abs(p) * (2 ** 15 + 1) + 1, (p, x)
+
+
 @pytest.mark.parametrize("change,expect", [
     (dict(d=96), UNSUPPORTED), (dict(d=0), UNSUPPORTED), (dict(rot=0), UNSUPPORTED), (dict(rot=24), UNSUPPORTED), (dict(rot=80), UNSUPPORTED), (dict(rot=-16), UNSUPPORTED),
     (dict(inter=2), INVALID), (dict(m=0.0), INVALID), (dict(m=-1.0), INVALID), (dict(m=float("nan")), INVALID), (dict(m=1e300), INVALID),

@@ -732,9 +732,12 @@ typedef struct {
  * daa_append_rope, daa_append_rope_q4: daa_kv_append and daa_kv_append_q4 of the
  * rotated k and of v, and q_out = rotated q, in one pass over the projections'
  * rows.  bf16 pages get exactly the bytes of daa_apply_rope followed by daa_kv_append.
- * Keys on their way to 4 bits are rotated to the nearest fp32 value (up to one in some
- * 2^13 that lies next to the middle of two), rounded to bf16 from that, and quantised:
- * their codes are those of the definition, not of an order of fp32 operations.
+ * Keys on their way to 4 bits are rotated to the nearest fp32 value, rounded to bf16
+ * from that, and quantised: their codes are those of the definition, not of an order of
+ * fp32 operations.  Nearest up to one in some 2^12 that lies next to the middle of two,
+ * at positions within 2^24 of zero; beyond, where the angle is off by p 2^-65 turns, up
+ * to twice as many with each doubling (one in some 2^6 at 2^31).  Which bf16 value it is
+ * hangs on that at one in some 2^27 and 2^22.
  * Rows belong to requests by append_indptr, and a row's position is its place in
  * its request, kv_len_r - n_r + t, unless `positions` gives others (draft trees:
  * the depths; the page and slot are by its place always).  q.data NULL: there are

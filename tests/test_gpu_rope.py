@@ -336,6 +336,23 @@ def test_append_q4(daa, case, exps):
         assert np.array_equal(pool.cpu().numpy(), host)
 
 
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (128, 128, True), (64, 32, False)])
+@pytest.mark.parametrize("at", [131_072, 2 ** 24 - 40])
+def test_keys_of_far_positions_into_4_bits(daa, at, d, rot, inter, norm):
+    """Byte for byte the definition's.  Angles off by 2^-36.7 together move a key to another bf16 value at one in some 2^27."""
+    rng = np.random.default_rng(26)
+    t, n = q4_support.make_table(rng, [0], [40])
+    q, k, v = _rows(rng, 40, 4, 4, d, "fused")
+    wk = _norms(rng, d, norm)[1]
+    rope = daa.Rope(d, 500000.0, rot, inter, dict(type="yarn", factor=16.0, original=4096))
+    pos = (at + np.arange(40)).astype(np.int32)
+    pool, want = daa.new_q4_pool(n, 4, d), daa.new_q4_pool(n, 4, d)
+    daa.append_rope_q4(q, k, v, pool, *_dev_table(t), rope, positions=_dev(pos), k_norm=wk)
+    daa.kv_append_q4(_exact_keys(k, pos, rope, wk), v.contiguous(), want, *_dev_table(t))
+    assert torch.equal(pool, want)
+
+
 @pytest.mark.parametrize("q4", [False, True])
 def test_given_positions_turn_but_do_not_place(daa, q4):
     """A draft tree's depths: rows go to the slots of their order, at the angles of the positions given."""

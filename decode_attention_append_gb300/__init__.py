@@ -1308,7 +1308,11 @@ def _load_native():
         if _native is None:
             path = os.path.join(_HERE, "_build", "_binding.so")
             if not os.path.exists(path):
-                raise ImportError(f"_binding.so not built at {path}; run decode_attention_append_gb300.build.build()")
+                why = ""
+                if os.path.exists(error := os.path.join(_HERE, "_build", "_binding.error")):
+                    with open(error) as f:
+                        why = f" (the last build of it: {f.read()})"
+                raise ImportError(f"_binding.so not built at {path}; run decode_attention_append_gb300.build.build(){why}")
             spec = importlib.util.spec_from_file_location("_binding", path)
             mod = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(mod)

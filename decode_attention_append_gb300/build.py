@@ -47,7 +47,23 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _run(cmd, verbose):
+    tool = os.path.basename(cmd[0])
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{tool} could not be run: {e}") from e
+    if verbose or r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+    if r.returncode != 0:
+        last = (r.stderr.strip().splitlines() or [""])[-1]
+        raise RuntimeError(f"{tool} failed: {' '.join(cmd[-3:])}: {last}")
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
+    """The library's path.  Without torch, its headers or Python's, only the module is
+    missing: the library is built all the same, and the calls that need the module
+    raise an ImportError with the reason."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     headers = _headers()
@@ -60,39 +76,58 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if force or _stale(o, [s] + headers):
             jobs.append([nvcc, *ARCH, *FLAGS, "-c", s, "-o", o])
 
-    # the module's object file goes by the torch and Python that it is for
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        module = ex.submit(_compile_module, verbose, force)  # beside nvcc's work
+        list(ex.map(lambda cmd: _run(cmd, verbose), jobs))
+        if force or jobs or _stale(LIB, objs):
+            tmp = LIB + f".tmp{os.getpid()}"
+            _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
+            os.replace(tmp, LIB)
+    error = os.path.join(BUILD, "_binding.error")  # why there is no module, read by the package
+    try:
+        _link_module(*module.result(), verbose, force)
+    except (ImportError, RuntimeError) as e:
+        sys.stderr.write(f"_binding.so is not built, and calls that need it will fail: {e}\n")
+        _remove(BINDING)  # of another library or torch
+        with open(error, "w") as f:
+            f.write(str(e))
+    else:
+        _remove(error)
+    return LIB
+
+
+def _remove(path):
+    if os.path.exists(path):
+        os.remove(path)
+
+
+def _compile_module(verbose, force):
+    """(torch, tag, object file): the object file goes by the torch and Python that it is for."""
     import torch
     tag = f"{torch.__version__}-{sys.version_info[0]}.{sys.version_info[1]}".replace("/", "_")
-    src, binding = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-{tag}.o")
-    if force or _stale(binding, [src, os.path.join(ROOT, "include", "daa.h")]):
-        jobs.insert(0, [shutil.which("g++") or "g++", *_torch_flags(torch), "-c", src, "-o", binding])
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, f"binding-{tag}.o")
+    if force or _stale(obj, [src, os.path.join(ROOT, "include", "daa.h")]):
+        _run([_gxx(), *_torch_flags(torch), "-c", src, "-o", obj], verbose)
+    return torch, tag, obj
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or r.returncode != 0:
-            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd[-3:])}")
 
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            list(ex.map(run, jobs))
-    if force or jobs or _stale(LIB, objs):
-        tmp = LIB + f".tmp{os.getpid()}"
-        run([nvcc, *ARCH, "-shared", "-o", tmp, *objs])
-        os.replace(tmp, LIB)
+def _link_module(torch, tag, obj, verbose, force):
     stamp = os.path.join(BUILD, f"binding-{tag}.linked.o")  # empty: which torch the module is linked for
-    if force or _stale(BINDING, [binding, LIB]) or not os.path.exists(stamp):
-        tmp = BINDING + f".tmp{os.getpid()}"
-        libs = os.path.join(os.path.dirname(torch.__file__), "lib")
-        run(["g++", "-shared", "-o", tmp, binding, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
-             f"-L{BUILD}", "-l:libdaa.so", "-Wl,-rpath,$ORIGIN"])
-        for f in os.listdir(BUILD):
-            if f.endswith(".linked.o"):
-                os.remove(os.path.join(BUILD, f))
-        os.replace(tmp, BINDING)
-        open(stamp, "w").close()
-    return LIB
+    if not force and not _stale(BINDING, [obj, LIB]) and os.path.exists(stamp):
+        return
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    _run([_gxx(), "-shared", "-o", tmp, obj, f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          f"-L{BUILD}", "-l:libdaa.so", "-Wl,-rpath,$ORIGIN"], verbose)
+    for f in os.listdir(BUILD):
+        if f.endswith(".linked.o"):
+            os.remove(os.path.join(BUILD, f))
+    os.replace(tmp, BINDING)
+    open(stamp, "w").close()
+
+
+def _gxx():
+    return shutil.which("g++") or "g++"
 
 
 def _torch_flags(torch):

@@ -51,7 +51,7 @@ namespace daa {
 namespace {
 
 constexpr int kThreads = 128, kWarps = kThreads / 32;
-enum Layout { kPart, kWhole, kInterleaved };  // pairs of halves of a part or all of the head; neighbours
+enum Layout { kPart, kWhole, kInterleaved, kEither };  // pairs of halves of a part or all of the head; neighbours; by a look
 constexpr int kP = 16;
 // Heads of a lane in flight, and CTAs of an SM that registers are left for.  Rows are
 // bound by HBM and want warps: 16,416 rows of 72 heads 96 us with two and 7 CTAs, 104
@@ -72,6 +72,13 @@ constexpr int ctas_of(int target, bool norm, int layout, bool lean) {
                                 : (norm && layout != kWhole ? 4 : 5);
 }
 constexpr int kLeanRounds = 6;  // of a warp's heads at a time, a row
+// Rows without norms of heads that are not turned whole: one kernel that looks at the layout,
+// where a warp has so many rounds of heads and rows are many (16,416 rows of 72 heads, half of
+// each turned 96.8 us, 99.8 with the layout's own kernel; interleaved 95.7 and 97.2; of 13
+// 22.8 and 23.7).  Below, and where rows share warps, the layout's own: of 9 heads 18.5 and
+// 18.6, of 5 12.3 and 13.2; 632 rows of 64 interleaved heads 4.3 and 4.6.  Heads of 64 dims
+// change over at the same rounds (24 heads 20.8 and 21.5, 36 28.7 and 28.5, 72 51.5 and 50.9).
+constexpr int kEitherRounds = 4;
 
 // ------------------------------------------------------------------- angles
 // Sine and cosine of n / 256 turns, each as the sum of two fp32 numbers.
@@ -315,7 +322,7 @@ template <int D, int TARGET, bool NORM, int LAYOUT, bool LEAN>
 __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN)) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int L = D / 16, G = 32 / L;  // lanes of a head, heads of a warp at a time
   constexpr bool APPEND = TARGET != kRopeRows, Q4 = TARGET == kRopePagesQ4;
-  constexpr bool FULL = LAYOUT == kWhole, pairs = LAYOUT == kInterleaved;
+  constexpr bool FULL = LAYOUT == kWhole;
   constexpr int kAhead = ahead_of(TARGET, NORM, LEAN);
   __shared__ float4 s_table[kSteps];
   __shared__ uint64_t s_turns[64];
@@ -323,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN))
   __shared__ __align__(16) float s_angle[kWarps][Q4 ? 6 : 2][64];
   __shared__ __align__(16) float s_w[NORM ? 2 : 1][D];  // norm weights of q and k
 
+  const bool pairs = LAYOUT == kInterleaved || (LAYOUT == kEither && a.interleaved != 0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32, group = lane / L, j = lane % L;
   const uint32_t mask = (L == 8 ? 0xFFu : 0xFu) << (lane & ~(L - 1));  // the head's lanes
   grid_dep_launch();
@@ -638,6 +646,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(TARGET, NORM, LAYOUT, LEAN))
 
 template <int D, int TARGET, bool LEAN, bool NORM>
 auto kernel_of(int layout) {
+  if constexpr (TARGET == kRopeRows && !NORM) {
+    if (layout == kEither) return rope_kernel<D, TARGET, NORM, kEither, LEAN>;
+  }
   return layout == kWhole         ? rope_kernel<D, TARGET, NORM, kWhole, LEAN>
          : layout == kInterleaved ? rope_kernel<D, TARGET, NORM, kInterleaved, LEAN>
                                   : rope_kernel<D, TARGET, NORM, kPart, LEAN>;
@@ -653,12 +664,13 @@ cudaError_t launch(RopeArgs a, int sms, bool programmatic, cudaStream_t stream) 
   const int H = a.Hq + (TARGET != kRopeRows ? 2 : 1) * a.Hk;
   const int rounds = (H + G - 1) / G;
   const bool norm = a.q_norm || a.k_norm;
-  const int layout = a.interleaved ? kInterleaved : a.rotary_dim == D ? kWhole : kPart;
+  int layout = a.interleaved ? kInterleaved : a.rotary_dim == D ? kWhole : kPart;
   // few rows: their heads over more warps, as many as the GPU starts at once
   const int64_t want = (int64_t)sms * kWarps * ctas_of(TARGET, norm, layout, false);
   const int parts = (int)std::min<int64_t>(rounds, std::max<int64_t>(1, want / a.n_rows));
   a.part_heads = (rounds + parts - 1) / parts * G;
   a.parts = (H + a.part_heads - 1) / a.part_heads;
+  if (TARGET == kRopeRows && !norm && layout != kWhole && parts == 1 && rounds >= kEitherRounds) layout = kEither;
   const int64_t tasks = (int64_t)a.n_rows * a.parts, grid = (tasks + kWarps - 1) / kWarps;
   const bool lean = TARGET == kRopePages && parts == 1 && rounds <= kLeanRounds;
   auto kern = lean ? kernel_of<D, TARGET, TARGET == kRopePages>(norm, layout) : kernel_of<D, TARGET, false>(norm, layout);

@@ -114,6 +114,29 @@ def test_rows_against_64_bits(daa, rows, hq, hk, d, rot, inter, norm, how):
         assert torch.equal(base[~mine].view(torch.int16), rest.view(torch.int16))
 
 
+@pytest.mark.parametrize("rows,hq,hk,d,rot,inter", [(5000, 12, 1, 128, 64, False), (5000, 13, 2, 128, 128, True), (4300, 12, 4, 128, 16, True),
+                                                    (5000, 9, 0, 128, 112, False), (4257, 25, 5, 64, 32, False), (6001, 36, 6, 64, 64, True)])
+def test_many_rows_give_the_bits_of_few(daa, rows, hq, hk, d, rot, inter):
+    """Many rows of many heads and the same rows a few at a time go to different kernels: the same bits, and right ones."""
+    rng = np.random.default_rng(rows + rot)
+    q, k, _ = _rows(rng, rows, hq, max(hk, 1), d, "fused")
+    k = k if hk else None
+    rope = daa.Rope(d, 10000.0, rot, inter)
+    pos = rng.integers(0, 131072, rows).astype(np.int32)
+    p = _dev(pos)
+    qo, ko = daa.apply_rope(q, k, p, rope)
+    for a in range(0, rows, 499):
+        b = min(a + 499, rows)
+        qs, ks = daa.apply_rope(q[a:b], k[a:b] if hk else None, p[a:b], rope)
+        assert torch.equal(qs.view(torch.int16), qo[a:b].view(torch.int16))
+        assert not hk or torch.equal(ks.view(torch.int16), ko[a:b].view(torch.int16))
+    at = rng.integers(0, rows, 60)
+    _check(qo[torch.from_numpy(at).to(DEV)], q[torch.from_numpy(at).to(DEV)], pos[at], rope, None, 0.0)
+    q2 = q.contiguous()  # in place
+    daa.apply_rope(q2, None, p, rope, q_out=q2)
+    assert torch.equal(q2.view(torch.int16), qo.view(torch.int16))
+
+
 @pytest.mark.parametrize("scaling", [None, dict(type="linear", factor=4.0), dict(type="ntk", factor=8.0),
                                      dict(type="wavelength", factor=8.0, original=8192)])
 def test_scalings_and_far_positions(daa, scaling):

@@ -25,10 +25,13 @@
 // kAhead heads ahead of their use, the first ones ahead of the search.  Warps share
 // nothing but constants: no barrier behind the first.  Each layout has kernels of its
 // own (keys into 4 bits with one for all: 153 us where interleaved heads take 119 and
-// parts of heads 116).  (With the sines of a CTA's rows
-// in shared memory and two barriers: 297 us for the first case below, 249 instructions a
-// warp of heads where this takes 126.  Two or four rows a warp: slower from 18
-// heads a row on, and no faster than LEAN below it.)
+// parts of heads 116); many rotated rows share one (kEitherRounds).
+//   With the sines of a CTA's rows in shared memory and two barriers: 297 us for the first
+// case below, 249 instructions a warp of heads where this takes 126.
+//   Four rows a warp, 32,800 rows: into bf16 pages 24 us for 3 heads a row where LEAN takes
+// 28, but 31 and 30 for 6, 49 and 44 for 14; into 4 bits, which has no such form, 35 us
+// where a row a warp takes 45, 45 and 51 for 6, 58 and 59 for 14, 69 and 66 for 20.  Not
+// built: a second set of kernels for rows of very few heads.
 //
 // Bound, and times on GB300 (graph replays; bytes at 6,785 GB/s, a copy's rate):
 //   32,832 rows of 80 heads of 128 dims appended   HBM: 200 us, 99 % of that rate
@@ -36,10 +39,15 @@
 //   36,760 rows of 48 heads into 4 bits            147 us, 77 %: instructions (55 % of the
 //       issue slots) and latency at 18 warps an SM.  Keys rotated as queries are would
 //       take 11 us less of it, and stray from the definition at one code in some 10^6.
+//   16,416 rows of 48 heads (8 of keys) with norms into 4 bits 101 us, 52 %, of 96 (32)
+//       222 us, 41 %: instructions (4,118 a row of 48, 57 % of the issue slots at 18 warps
+//       an SM).  Every key is normalised and turned in two parts, for the few that need it.
 //   128 rows of 14 heads, 32 of 64                 2.8 and 1.6 us: a launch, and two or
 //       three dependent loads
-//   32,800 rows of 10 heads appended 38 us, 66 %, of 14 44 us, 79 %: what a row costs
-//       before its heads (search, place, sines: about 450 instructions a warp).
+//   32,800 rows of 10 heads appended 38 us, 66 %, of 14 44 us, 79 %, rotated (9 and 13)
+//       32 and 41 us, 70 and 79 %, into 4 bits 53 and 60 us, 44 and 55 %: what a row
+//       costs before its heads (search, place, sines: about 450 instructions a warp of
+//       1,264 a row of 10 heads into 4 bits).
 #include <algorithm>
 
 #include "launch.h"
@@ -59,10 +67,16 @@ constexpr int kP = 16;
 // us with five heads and 4 CTAs, 205 with two and 7; a chunk beside decodes 3.9 and 4.8.
 // But where rows are many and of few heads, what comes before a row's heads is most of
 // it, and more warps do that at a time (LEAN: two heads and 7 CTAs): 32,800 rows of 14
-// heads 44 us and not 53, of 10 38 and 47, of 20 56 and 60, of 32 no difference.  The
-// 4-bit append is bound by instructions and latency: 36,760 rows of 48 heads 147 us with
-// three heads and 5 CTAs, 155 with two, 159 with 4 CTAs.  With norms 96 registers hold it
-// for whole heads only (16,416 rows of 48: 100 us, 105 with 4 CTAs; interleaved 113, 108).
+// heads 44 us and not 53, of 10 38 and 47, of 20 56 and 60, of 32 no difference; of 64
+// dims, where as many rounds are twice the heads, of 10 30 and 40, of 28 46 and 53, of 48
+// 69 and 71, of 64 (past kLeanRounds) 87 and 89.  The 4-bit append is bound by
+// instructions and latency: 36,760 rows of 48 heads 147 us with three heads and 5 CTAs,
+// 155 with two, 159 with 4 CTAs.  With norms 96 registers hold it for whole heads only
+// (16,416 rows of 48: 101 us, 105 with 4 CTAs; interleaved 113, 108).  Without, interleaved
+// heads spill 56 bytes at 96 registers, and neither count is best for all of them: 16,416
+// rows of 48 heads of 128 dims 78.6 us with 5 CTAs and 77.5 with 4, of 96 165 and 155, 544
+// rows of 48 6.0 and 4.9; but of 14 heads 32.5 and 34.5, of 36 57.0 and 59.7, 1,332 rows
+// of 32 6.3 and 7.2, of 28 heads of 64 dims 35.5 and 36.9.
 constexpr int ahead_of(int target, bool norm, bool lean) {
   return target == kRopeRows || lean ? 2 : target == kRopePages ? 5 : norm ? 2 : 3;
 }

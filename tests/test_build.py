@@ -34,7 +34,7 @@ def test_library_without_module(own, monkeypatch, capsys):
     package's error has the reason."""
     import decode_attention_append_gb300 as daa
     daa.load_library()
-    monkeypatch.setattr(build.shutil, "which", _which(lambda: _tool(own / "g++", "echo 'fatal error: Python.h: No such file' >&2; exit 1")))
+    monkeypatch.setattr(build.shutil, "which", _which(_tool(own / "g++", "echo 'fatal error: Python.h: No such file' >&2; exit 1")))
     (own / "_build").mkdir()
     (own / "_build" / "_binding.so").write_text("of another torch")
     lib = build.build()
@@ -46,7 +46,7 @@ def test_library_without_module(own, monkeypatch, capsys):
     monkeypatch.setattr(daa, "_HERE", str(own))
     with pytest.raises(ImportError, match="_binding.so.*g\\+\\+ failed.*Python.h"):
         daa._load_native()
-    monkeypatch.setattr(build.shutil, "which", _which(lambda: str(own / "none")))
+    monkeypatch.setattr(build.shutil, "which", _which(str(own / "none")))
     before = os.path.getmtime(lib)
     assert build.build() == lib and os.path.getmtime(lib) == before
     assert "could not be run" in _error(own)
@@ -55,7 +55,7 @@ def test_library_without_module(own, monkeypatch, capsys):
 def test_a_later_build_brings_the_module(own, monkeypatch):
     flags = []
     script = 'while [ $# -gt 0 ]; do if [ "$1" = -o ]; then echo x > "$2"; fi; shift; done'
-    monkeypatch.setattr(build.shutil, "which", _which(lambda: _tool(own / "g++", script)))
+    monkeypatch.setattr(build.shutil, "which", _which(_tool(own / "g++", script)))
     monkeypatch.setattr(build, "_torch_flags", lambda torch: flags)
     build.build()
     assert os.path.exists(build.BINDING) and not (own / "_build" / "_binding.error").exists()
@@ -66,7 +66,8 @@ def test_a_later_build_brings_the_module(own, monkeypatch):
 
 
 def test_a_failing_nvcc_is_named(own, monkeypatch):
-    monkeypatch.setattr(build, "_nvcc", lambda: _tool(own / "nvcc", "echo no >&2; exit 3"))
+    nvcc = _tool(own / "nvcc", "echo no >&2; exit 3")
+    monkeypatch.setattr(build, "_nvcc", lambda: nvcc)
     with pytest.raises(RuntimeError, match="nvcc failed.*no"):
         build.build()
 
@@ -75,4 +76,4 @@ _shutil_which = shutil.which
 
 
 def _which(gxx):
-    return lambda name, *a, **k: gxx() if name == "g++" else _shutil_which(name, *a, **k)
+    return lambda name, *a, **k: gxx if name == "g++" else _shutil_which(name, *a, **k)

@@ -204,6 +204,17 @@ daa_status append(const daa_rope* rope, const daa_rope_rows* io, void* kv_pages,
   if (in_pool(io->k, dims.num_kv_heads) || in_pool(io->v, dims.num_kv_heads) ||
       (q_heads > 0 && (in_pool(io->q, q_heads) || in_pool(io->q_out, q_heads))))
     return DAA_ERR_INVALID_ARG;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } also_read[] = {{io->positions, 4 * n},          {io->q_norm, 2 * d},
+                   {io->k_norm, 2 * d},             {kv_exp, 8 * (int64_t)dims.num_kv_heads},
+                   {append_indptr, 4 * (int64_t)batch + 4}, {kv_indptr, 4 * (int64_t)batch + 4},
+                   {last_page_len, 4 * (int64_t)batch},     {page_indices, 4}};  // of these, the number is on the device
+  for (const auto& x : also_read)
+    if (x.p && (ranges_meet(x.p, x.bytes, kv_pages, pool_bytes) ||
+                (q_heads > 0 && ranges_meet(x.p, x.bytes, io->q_out.data, 2 * span_of(io->q_out, n, q_heads, d)))))
+      return DAA_ERR_INVALID_ARG;
   a.pool = static_cast<uint8_t*>(kv_pages);
   a.kv_exp = kv_exp;
   a.append_indptr = append_indptr;

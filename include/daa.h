@@ -748,9 +748,10 @@ typedef struct {
  * most rows that a step may have).
  *
  * An output may be its own input (same address and strides: in place).  Otherwise no
- * output may share an element with another output or with the rows, positions or
- * weights that are read, or lie in the pool: what cannot be told apart by ranges, by
- * columns of the same rows or by heads of the same order is refused.
+ * output may share an element with another output or with the rows, positions, weights
+ * or tables that are read, and neither outputs nor what is read may lie in the pool:
+ * what cannot be told apart by ranges, by columns of the same rows or by heads of the
+ * same order is refused (of page_indices, whose number is on the device, the first).
  * One kernel launch each, no workspace, nothing kept: all can be captured into a CUDA
  * graph, and calls on different rows and pages may overlap.
  * Errors: DAA_ERR_INVALID_ARG for NULL arguments (positions of daa_apply_rope among

@@ -189,6 +189,32 @@ def test_rows_within_the_pool_are_refused(daa, name):
         assert got == expect, (name, hex(at))
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("name,size", [("append_indptr", 12), ("page_indices", 4), ("kv_indptr", 12), ("last_page_len", 8), ("kv_exp", 16), ("pos", 32), ("qn", 128), ("kn", 128)])
+def test_tables_under_what_is_written_are_refused(daa, q4, name, size):
+    """A table, positions or weights in the pool (64 pages) or under the rotated queries.  Found once everything else is in
+    order: not on a machine where a call that is not refused would launch."""
+    if torch.cuda.is_available():
+        pytest.skip("addresses that are none")
+    if name == "kv_exp" and not q4:
+        pytest.skip("bf16 pages have no exponents")
+    pool = 0x70000000
+    pool_end = pool + 64 * 2 * 2 * (9 * 64 if q4 else 2 * 16 * 64)
+    q_out, q_end = 0x900000, 0x900000 + 8 * 256 * 2
+    lib, rope = daa.load_library(), daa.Rope(64)
+    for at in (pool, pool_end - 4, pool - size + 4, q_out, q_end - 4, q_out - size + 4):
+        where = dict(append_indptr=0x10000, page_indices=0x20000, kv_indptr=0x30000, last_page_len=0x40000, kv_exp=0, pos=0, qn=0, kn=0)
+        where[name] = at
+        rec = _rec(A, 512, 64, A + 512, 512, 64, A + 768, 512, 64, q_out, 256, 64, 0, 0, 0, 8, where["pos"], where["qn"], where["kn"], 1e-6)
+        tab = [where[x] for x in ("append_indptr", "page_indices", "kv_indptr", "last_page_len")]
+        args = (ctypes.addressof(rope._rope), rec, pool)
+        if q4:
+            st = lib.daa_append_rope_q4(*args, where["kv_exp"] or None, *tab, 2, daa._Dims(4, 2, 64, 16, 64), None)
+        else:
+            st = lib.daa_append_rope(*args, *tab, 2, daa._Dims(4, 2, 64, 16, 64), None)
+        assert st == INVALID, hex(at)
+
+
 def test_bad_records_are_refused(daa):
     lib = daa.load_library()
     rope = daa.Rope(64)
